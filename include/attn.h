@@ -334,6 +334,122 @@ ATTN_API attn_status_t attn_bwd_noalloc(const void *q, const void *k, const void
                                         int window_left, int window_right,
                                         const int *doc_offsets, int num_docs, void *stream);
 
+/*
+ * RMS norm of every query and key head and the rotation by position, in one
+ * pass, as it stands between the QKV projection and the attention.  (The
+ * attention pages have no counterpart of this and the following entry
+ * points; they make up the rest of an attention layer's path.)  Per token t
+ * and head, with x its D values and w the head weights (shared by all query
+ * heads, and by all key heads):
+ *   r   = (sum_d x_d^2 / D + eps)^(-1/2),   u_d = w_d x_d r
+ *   y_a = u_a c - u_b s,  y_b = u_b c + u_a s     for the pairs (a, b) among
+ *         the first `rot` values: (i, i + rot/2), or (2i, 2i + 1) when
+ *         `interleaved` is 1;  c, s = cos, sin[positions[t]][i]
+ *   y_d = u_d                                     for d >= rot
+ * q, k (inputs), q_out, k_out: bf16 [tokens][Hq or Hkv][D], heads and values
+ * contiguous, consecutive tokens `*_stride` values apart (so Q and K may be
+ * views of one packed projection output); 16-byte aligned, strides multiples
+ * of 8 and >= H * D.  An output may be its own input (same pointer and
+ * stride), else they do not overlap.  Weights: [D], fp32 if w_fp32 is 1, else bf16.
+ * cos, sin: fp32 [max_positions][rot/2]; positions: int32 [tokens].  Weights
+ * and tables 16-byte aligned.  D is 64 or 128; rot a multiple of 16 in
+ * [16, D]; eps >= 0; tokens >= 1.  Everything is computed in fp32 and rounded
+ * once.  A position outside [0, max_positions) is clamped and makes
+ * attn_get_device_status() report ATTN_ERR_RANGE.
+ */
+ATTN_API attn_status_t attn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
+                                         long long q_stride, long long k_stride,
+                                         long long q_out_stride, long long k_out_stride,
+                                         const void *q_weight, const void *k_weight, int w_fp32,
+                                         const float *cos, const float *sin, const int *positions,
+                                         long long tokens, int Hq, int Hkv, int D, int rot,
+                                         int max_positions, float eps, int interleaved,
+                                         void *stream);
+
+/*
+ * Its backward: from dq, dk (the gradients of q_out, k_out: [tokens][H][D],
+ * fp32 if dq_fp32 / dk_fp32 is 1, else bf16) and the forward's inputs, the
+ * gradients of q and k (dq_in, dk_in: bf16) and of the weights (dq_weight,
+ * dk_weight: fp32 [D], summed over tokens and heads).  With g = R^T dy and
+ * h = w g:
+ *   dx_d = r h_d - r^3 x_d sum_e(h_e x_e) / D,   dw_d = sum g_d x_d r
+ * Strides and the other arguments as above; outputs do not overlap inputs,
+ * except that dq_in (dk_in) may be q (k) itself.  workspace: at least
+ * attn_qk_norm_rope_bwd_workspace_size(D) bytes, 16-byte aligned (contents on
+ * entry ignored).  The result is deterministic on a given device.
+ */
+ATTN_API size_t attn_qk_norm_rope_bwd_workspace_size(int D);
+
+ATTN_API attn_status_t attn_qk_norm_rope_bwd(
+    const void *dq, const void *dk, int dq_fp32, int dk_fp32, const void *q, const void *k,
+    void *dq_in, void *dk_in, float *dq_weight, float *dk_weight, long long dq_stride,
+    long long dk_stride, long long q_stride, long long k_stride, long long dq_in_stride,
+    long long dk_in_stride, const void *q_weight, const void *k_weight, int w_fp32,
+    const float *cos, const float *sin, const int *positions, long long tokens, int Hq, int Hkv,
+    int D, int rot, int max_positions, float eps, int interleaved, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+/* Element type of a key/value cache. */
+#define ATTN_KV_BF16 0
+#define ATTN_KV_E4M3 1
+
+/*
+ * attn_qk_norm_rope for the new tokens of a serving step: Q goes to q_out,
+ * the normed and rotated K and the plain V go to slot slots[t] of the caches
+ * [num_slots][Hkv][D] (slot = page * page_size + place in the page), as bf16
+ * or as e4m3 codes of value / descale (nearest even, saturating at +-448; the
+ * value a code stands for is descale * code, as in attn_fwd_fp8).  For a
+ * bf16 cache both descale factors are 1.  v: bf16 [tokens][Hkv][D], like k.
+ * A token with a negative slot is padding: nothing of it is read or written,
+ * its row of q_out included.  A slot >= num_slots is treated the same and
+ * reports ATTN_ERR_RANGE.  Slots of one call are distinct: of two tokens with
+ * one slot, either's values may be left there, K and V apart.
+ * slots: int32 [tokens]; caches 16-byte aligned.
+ */
+ATTN_API attn_status_t attn_qk_norm_rope_cache(
+    const void *q, const void *k, const void *v, void *q_out, long long q_stride,
+    long long k_stride, long long v_stride, long long q_out_stride, const void *q_weight,
+    const void *k_weight, int w_fp32, const float *cos, const float *sin, const int *positions,
+    const int *slots, void *k_cache, void *v_cache, int kv_dtype, float k_descale,
+    float v_descale, long long num_slots, long long tokens, int Hq, int Hkv, int D, int rot,
+    int max_positions, float eps, int interleaved, void *stream);
+
+/*
+ * Decode: attention of one new token per sequence over a paged cache.
+ *   q, o      bf16 [B][Hq][D]
+ *   k_cache, v_cache  [num_pages][page_size][Hkv][D], kv_dtype as above
+ *   seq_lens  int32 [B]: keys of each sequence, the new token's own (already
+ *             in the cache) counted; may be 0
+ *   page_table int32 [B][max_pages]: key j of sequence b is in page
+ *             page_table[b][j / page_size], place j % page_size; entries
+ *             behind the sequence's last page are not read
+ *   lse       fp32 [B][Hq]
+ * With i = seq_lens[b] - 1, key j <= i is visible iff window_left is -1, or
+ * j >= i - window_left, or j < sinks (first tokens that stay visible).
+ * Scores, softcap (0: none), alibi_slopes (fp32 [Hq] or NULL) and the results
+ * are those of attn_fwd for the one row i; a sequence without a key gets
+ * O = 0 and LSE = -inf.  What lies in the caches at hidden places (behind a
+ * sequence's end, in pages of others) has no part in the result, NaN
+ * included.  page_size is a multiple of 16; Hq % Hkv == 0; D is 64 or 128.
+ * A length outside [0, max_pages * page_size] is clamped, a page outside
+ * [0, num_pages) is replaced by page 0 (that sequence's results are then
+ * unspecified); both report ATTN_ERR_RANGE.  workspace: at least
+ * attn_decode_paged_workspace_size(D) bytes, 16-byte aligned (contents on
+ * entry ignored; calls that may run at the same time need one each).  The
+ * launch depends on no device data, so a captured call may be replayed with
+ * other lengths.  The result is deterministic on a given device; it depends,
+ * by rounding alone, on the whole batch's lengths, which set where the work
+ * is cut.
+ */
+ATTN_API size_t attn_decode_paged_workspace_size(int D);
+
+ATTN_API attn_status_t attn_decode_paged(
+    const void *q, const void *k_cache, const void *v_cache, int kv_dtype, float k_descale,
+    float v_descale, const int *page_table, const int *seq_lens, void *o, float *lse, int B,
+    int Hq, int Hkv, int D, int num_pages, int page_size, int max_pages, float scale,
+    int window_left, int sinks, float softcap, const float *alibi_slopes, void *workspace,
+    size_t workspace_bytes, void *stream);
+
 /* Synchronises `stream`, then reads and clears the device status word of
  * the current device.  Returns ATTN_OK, ATTN_ERR_DEVICE_TIMEOUT or
  * ATTN_ERR_RANGE (or ATTN_ERR_CUDA if the synchronisation itself failed). */

@@ -1,0 +1,187 @@
+"""Host-side checks of the head norms, the cache write and the decode (no GPU
+needed): bad arguments are refused before any CUDA call."""
+import ctypes
+
+import pytest
+import torch
+
+from tiled_attention_blackwell_b200 import attn, build
+
+P = 0x10000  # a fake, aligned device address: never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return attn.lib()
+
+
+NORM = dict(q=P, k=P, qo=P, ko=P, qs=512, ks=256, qos=512, kos=256, qw=P, kw=P, wf=0, cos=P, sin=P, pos=P, tokens=4,
+            Hq=4, Hkv=2, D=128, rot=64, maxpos=100, eps=1e-6, inter=0)
+
+
+def call_norm(L, **kw):
+    a = {**NORM, **kw}
+    return L.attn_qk_norm_rope(a["q"], a["k"], a["qo"], a["ko"], a["qs"], a["ks"], a["qos"], a["kos"], a["qw"],
+                               a["kw"], a["wf"], a["cos"], a["sin"], a["pos"], a["tokens"], a["Hq"], a["Hkv"],
+                               a["D"], a["rot"], a["maxpos"], a["eps"], a["inter"], None)
+
+
+def call_norm_cache(L, **kw):
+    a = {**NORM, **dict(v=P, vs=256, slots=P, kc=P, vc=P, kv=0, kd=1.0, vd=1.0, n=64), **kw}
+    return L.attn_qk_norm_rope_cache(a["q"], a["k"], a["v"], a["qo"], a["qs"], a["ks"], a["vs"], a["qos"], a["qw"],
+                                     a["kw"], a["wf"], a["cos"], a["sin"], a["pos"], a["slots"], a["kc"], a["vc"],
+                                     a["kv"], a["kd"], a["vd"], a["n"], a["tokens"], a["Hq"], a["Hkv"], a["D"],
+                                     a["rot"], a["maxpos"], a["eps"], a["inter"], None)
+
+
+def call_norm_bwd(L, **kw):
+    a = {**NORM, **dict(dq=P, dk=P, dqf=1, dkf=0, dqw=P, dkw=P, dqs=512, dks=256, ws=P, wsb=1 << 22), **kw}
+    return L.attn_qk_norm_rope_bwd(a["dq"], a["dk"], a["dqf"], a["dkf"], a["q"], a["k"], a["qo"], a["ko"], a["dqw"],
+                                   a["dkw"], a["dqs"], a["dks"], a["qs"], a["ks"], a["qos"], a["kos"], a["qw"],
+                                   a["kw"], a["wf"], a["cos"], a["sin"], a["pos"], a["tokens"], a["Hq"], a["Hkv"],
+                                   a["D"], a["rot"], a["maxpos"], a["eps"], a["inter"], a["ws"], a["wsb"], None)
+
+
+INV, UNS, MIS = attn.ATTN_ERR_INVALID_ARG, attn.ATTN_ERR_UNSUPPORTED, attn.ATTN_ERR_MISALIGNED
+COMMON = [(dict(q=0), INV), (dict(k=0), INV), (dict(qw=0), INV), (dict(cos=0), INV), (dict(pos=0), INV),
+          (dict(tokens=0), INV), (dict(tokens=-1), INV), (dict(Hq=0), INV), (dict(D=96), UNS), (dict(rot=0), INV),
+          (dict(rot=24), INV), (dict(rot=144), INV), (dict(maxpos=0), INV), (dict(eps=-1.0), INV),
+          (dict(eps=float("nan")), INV), (dict(inter=2), INV), (dict(wf=-1), INV), (dict(q=P + 8), MIS),
+          (dict(qw=P + 8), MIS), (dict(sin=P + 4), MIS), (dict(pos=P + 2), MIS), (dict(qs=511), INV),
+          (dict(qs=504), INV), (dict(ks=260), INV), (dict(tokens=1 << 40), UNS)]
+
+
+@pytest.mark.parametrize("call", [call_norm, call_norm_cache, call_norm_bwd])
+@pytest.mark.parametrize("kw,status", COMMON)
+def test_norm_refusals(L, call, kw, status):
+    assert call(L, **kw) == status
+    assert L.attn_last_error_detail().decode() != ""
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(v=0), INV), (dict(vs=128), INV), (dict(slots=0), INV), (dict(slots=P + 1), MIS), (dict(kc=0), INV),
+    (dict(vc=P + 4), MIS), (dict(kv=2), INV), (dict(n=0), INV), (dict(kd=0.5), INV), (dict(kv=1, kd=0.0), INV),
+    (dict(kv=1, vd=float("inf")), INV)])
+def test_norm_cache_refusals(L, kw, status):
+    assert call_norm_cache(L, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dq=0), INV), (dict(dqs=256), INV), (dict(dqf=2), INV), (dict(dqw=0), INV), (dict(dkw=P + 2), MIS),
+    (dict(ws=0), INV), (dict(ws=P + 8), MIS), (dict(wsb=100), INV), (dict(qo=P + 4), MIS)])
+def test_norm_bwd_refusals(L, kw, status):
+    assert call_norm_bwd(L, **kw) == status
+
+
+def call_decode(L, **kw):
+    a = dict(q=P, kc=P, vc=P, kv=0, kd=1.0, vd=1.0, table=P, lens=P, o=P, lse=P, B=2, Hq=4, Hkv=2, D=128, pages=8,
+             page=16, width=4, scale=0.1, wl=-1, sinks=0, cap=0.0, slopes=None, ws=P, wsb=1 << 24)
+    a.update(kw)
+    return L.attn_decode_paged(a["q"], a["kc"], a["vc"], a["kv"], a["kd"], a["vd"], a["table"], a["lens"], a["o"],
+                               a["lse"], a["B"], a["Hq"], a["Hkv"], a["D"], a["pages"], a["page"], a["width"],
+                               a["scale"], a["wl"], a["sinks"], a["cap"], a["slopes"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=0), INV), (dict(kc=0), INV), (dict(table=0), INV), (dict(lens=0), INV), (dict(lse=0), INV),
+    (dict(ws=0), INV), (dict(wsb=100), INV), (dict(q=P + 8), MIS), (dict(vc=P + 4), MIS), (dict(table=P + 2), MIS),
+    (dict(slopes=P + 2), MIS), (dict(B=0), INV), (dict(Hq=3), INV), (dict(pages=0), INV), (dict(width=0), INV),
+    (dict(D=96), UNS), (dict(page=8), UNS), (dict(page=24), UNS), (dict(page=0), UNS), (dict(kv=3), INV),
+    (dict(kd=2.0), INV), (dict(kv=1, vd=-1.0), INV), (dict(scale=0.0), INV), (dict(scale=float("nan")), INV),
+    (dict(wl=-2), INV), (dict(sinks=-1), INV), (dict(cap=-1.0), INV), (dict(cap=float("inf")), INV),
+    (dict(page=1 << 20, width=1 << 12), UNS), (dict(Hq=1 << 16, Hkv=1 << 16, width=1 << 20), UNS)])
+def test_decode_refusals(L, kw, status):
+    assert call_decode(L, **kw) == status
+    assert L.attn_last_error_detail().decode() != ""
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU path only")
+def test_valid_calls_without_gpu_report_cuda_error(L):
+    for call in (call_norm, call_norm_cache, call_norm_bwd, call_decode):
+        assert call(L) == attn.ATTN_ERR_CUDA
+    assert call_decode(L, kv=1, kd=0.1, vd=3.0, wl=0, sinks=4, cap=30.0, slopes=P) == attn.ATTN_ERR_CUDA
+
+
+def test_workspace_sizes(L):
+    assert attn.decode_workspace_size(128) >= 296 * 2 * 16 * 128 * 4 and attn.decode_workspace_size(0) == 0
+    assert L.attn_qk_norm_rope_bwd_workspace_size(64) >= 4 * 148 * 2 * 64 * 4
+
+
+class _CudaStandIn(torch.Tensor):
+    """A CPU tensor that reports itself as a CUDA tensor (see test_boundary)."""
+
+    @property
+    def is_cuda(self):
+        return True
+
+
+def stand_in(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype).as_subclass(_CudaStandIn)
+
+
+def norm_tensors():
+    f32, i32 = torch.float32, torch.int32
+    return dict(q=stand_in(5, 4, 128), k=stand_in(5, 2, 128), q_weight=stand_in(128), k_weight=stand_in(128),
+                cos=stand_in(9, 32, dtype=f32), sin=stand_in(9, 32, dtype=f32), positions=stand_in(5, dtype=i32))
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("q", lambda: torch.zeros(5, 4, 128, dtype=torch.bfloat16)), ("q", lambda: stand_in(5, 4, 128, dtype=torch.float16)),
+    ("q", lambda: stand_in(4, 128)), ("k", lambda: stand_in(6, 2, 128)), ("k", lambda: stand_in(5, 2, 64)),
+    ("q", lambda: stand_in(5, 128, 4).transpose(1, 2)), ("q", lambda: stand_in(4, 5, 128).transpose(0, 1)),
+    ("q_weight", lambda: stand_in(64)), ("k_weight", lambda: stand_in(128, dtype=torch.float32)),
+    ("cos", lambda: stand_in(8, 32, dtype=torch.float32)), ("sin", lambda: stand_in(9, 32)),
+    ("positions", lambda: stand_in(5, dtype=torch.int64)), ("positions", lambda: stand_in(4, dtype=torch.int32))])
+def test_norm_binding_refuses(L, name, bad):
+    t = norm_tensors()
+    t[name] = bad()
+    with pytest.raises(TypeError):
+        attn.qk_norm_rope(*t.values(), stream=0)
+    with pytest.raises(TypeError):
+        attn.qk_norm_rope_backward(stand_in(5, 4, 128), stand_in(5, 2, 128), *t.values(), stream=0)
+    with pytest.raises(TypeError):
+        attn.qk_norm_rope_cache(t["q"], t["k"], stand_in(5, 2, 128), *list(t.values())[2:],
+                                stand_in(5, dtype=torch.int32), stand_in(3, 16, 2, 128), stand_in(3, 16, 2, 128), stream=0)
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("v", lambda: stand_in(5, 4, 128)), ("slots", lambda: stand_in(5, dtype=torch.int64)),
+    ("slots", lambda: stand_in(1, 5, dtype=torch.int32)), ("k_cache", lambda: stand_in(3, 16, 2, 128, dtype=torch.float32)),
+    ("k_cache", lambda: stand_in(3, 2, 16, 128).transpose(1, 2)), ("v_cache", lambda: stand_in(3, 16, 4, 128)),
+    ("v_cache", lambda: stand_in(4, 16, 2, 128))])
+def test_cache_binding_refuses(L, name, bad):
+    t = norm_tensors()
+    extra = dict(v=stand_in(5, 2, 128), slots=stand_in(5, dtype=torch.int32), k_cache=stand_in(3, 16, 2, 128),
+                 v_cache=stand_in(3, 16, 2, 128))
+    extra[name] = bad()
+    with pytest.raises(TypeError):
+        attn.qk_norm_rope_cache(t["q"], t["k"], extra["v"], *list(t.values())[2:], extra["slots"], extra["k_cache"],
+                                extra["v_cache"], stream=0)
+
+
+def test_packed_views_are_taken():
+    qkv = torch.zeros(2, 5, 8 * 64, dtype=torch.bfloat16)
+    q, k = qkv[..., :256].unflatten(-1, (4, 64)), qkv[..., 256:384].unflatten(-1, (2, 64))
+    assert attn._token_stride("q", q, 4, 64, (torch.bfloat16,)) == 512
+    assert attn._token_stride("k", k, 2, 64, (torch.bfloat16,)) == 512
+    assert attn._token_stride("q", q[:, :1], 4, 64, (torch.bfloat16,)) == 5 * 512  # one token a row
+    assert attn._token_stride("q", q[:1, :1], 4, 64, (torch.bfloat16,)) == 256
+    assert attn._token_stride("k", k[..., :1, :], 1, 64, (torch.bfloat16,)) == 512
+    with pytest.raises(TypeError):
+        attn._token_stride("q", q[:, :3], 4, 64, (torch.bfloat16,))
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("q", lambda: stand_in(2, 4, 128, dtype=torch.float16)), ("q", lambda: stand_in(2, 1, 4, 128)),
+    ("page_table", lambda: stand_in(3, 4, dtype=torch.int32)), ("page_table", lambda: stand_in(2, 4, dtype=torch.int64)),
+    ("seq_lens", lambda: torch.zeros(2, dtype=torch.int32)), ("seq_lens", lambda: stand_in(2, 1, dtype=torch.int32)),
+    ("k_cache", lambda: stand_in(8, 16, 2, 64)), ("v_cache", lambda: stand_in(8, 16, 2, 128, dtype=torch.float8_e4m3fn))])
+def test_decode_binding_refuses(L, name, bad):
+    i32 = torch.int32
+    t = dict(q=stand_in(2, 4, 128), k_cache=stand_in(8, 16, 2, 128), v_cache=stand_in(8, 16, 2, 128),
+             page_table=stand_in(2, 4, dtype=i32), seq_lens=stand_in(2, dtype=i32))
+    t[name] = bad()
+    with pytest.raises(TypeError):
+        attn.decode_paged(*t.values(), o=stand_in(2, 4, 128), lse=stand_in(2, 4, dtype=torch.float32),
+                          workspace=stand_in(1 << 23, dtype=torch.uint8), stream=0)

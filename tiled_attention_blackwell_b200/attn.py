@@ -6,6 +6,7 @@ There is no fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -35,9 +36,15 @@ ATTN_FP4_MMA_BLOCK_SCALED = 2
 FP4_MMA = {"auto": ATTN_FP4_MMA_AUTO, "f16": ATTN_FP4_MMA_F16,
            "block_scaled": ATTN_FP4_MMA_BLOCK_SCALED}
 
+ATTN_KV_BF16 = 0
+ATTN_KV_E4M3 = 1
+
 EXPORTED = ("attn_fwd", "attn_fwd_ex", "attn_fwd_fp8", "attn_fwd_default_options",
             "attn_fp4_default_options", "attn_fwd_fp4_workspace_size", "attn_fwd_fp4", "attn_bwd",
-            "attn_bwd_ex", "attn_bwd_workspace_size", "attn_bwd_noalloc", "attn_get_device_status",
+            "attn_bwd_ex", "attn_bwd_workspace_size", "attn_bwd_noalloc", "attn_qk_norm_rope",
+            "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_size",
+            "attn_qk_norm_rope_cache", "attn_decode_paged", "attn_decode_paged_workspace_size",
+            "attn_get_device_status",
             "attn_status_string", "attn_last_error_detail", "attn_abi_version")
 
 
@@ -127,6 +134,24 @@ def lib():
             L.attn_bwd_noalloc.argtypes = [ctypes.c_void_p] * 9 + [ctypes.c_int] * 6 + \
                 [ctypes.c_float] + [ctypes.c_int] * 3 + [ctypes.c_void_p, ctypes.c_int,
                                                          ctypes.c_void_p]
+            i, ll, f, vp = ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_void_p
+            norm = [vp, vp, i, vp, vp, vp]  # weights, tables, positions
+            sizes = [ll, i, i, i, i, i, f, i]  # tokens .. interleaved
+            L.attn_qk_norm_rope.restype = i
+            L.attn_qk_norm_rope.argtypes = [vp] * 4 + [ll] * 4 + norm + sizes + [vp]
+            L.attn_qk_norm_rope_cache.restype = i
+            L.attn_qk_norm_rope_cache.argtypes = [vp] * 4 + [ll] * 4 + norm + \
+                [vp, vp, vp, i, f, f, ll] + sizes + [vp]
+            L.attn_qk_norm_rope_bwd_workspace_size.restype = ctypes.c_size_t
+            L.attn_qk_norm_rope_bwd_workspace_size.argtypes = [i]
+            L.attn_qk_norm_rope_bwd.restype = i
+            L.attn_qk_norm_rope_bwd.argtypes = [vp, vp, i, i] + [vp] * 6 + [ll] * 6 + norm + \
+                sizes + [vp, ctypes.c_size_t, vp]
+            L.attn_decode_paged_workspace_size.restype = ctypes.c_size_t
+            L.attn_decode_paged_workspace_size.argtypes = [i]
+            L.attn_decode_paged.restype = i
+            L.attn_decode_paged.argtypes = [vp, vp, vp, i, f, f, vp, vp, vp, vp] + [i] * 7 + \
+                [f, i, i, f, vp, vp, ctypes.c_size_t, vp]
             _lib = L
     return _lib
 
@@ -470,6 +495,263 @@ def attn_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, *, scale, causal=False, 
                                 float(scale), int(bool(causal)), wl, wr, docs_ptr, nd,
                                 _stream_handle(stream))
     _check(st, "attn_bwd_noalloc")
+
+
+# ----------------------------------------------- around the attention kernels
+
+def _same_device(tensors):
+    """The CUDA device of all (name, tensor) pairs; anything else raises."""
+    device = None
+    for name, t in tensors:
+        if not torch.is_tensor(t) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise TypeError(f"{name} is on {t.device}, the first tensor on {device}")
+    return device
+
+
+def _on_device(device):
+    """Makes `device` current for a call, if it is not."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _keep_for(stream, *tensors):
+    """Tells the allocator that work on `stream` uses tensors which were
+    allocated on the current stream."""
+    if stream is not None and hasattr(stream, "cuda_stream") \
+            and stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _token_stride(name, t, H, D, dtypes):
+    """Distance, in values, of consecutive tokens of a [..., H, D] tensor
+    whose heads are contiguous and whose tokens are evenly spaced."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 3 or shape[-1] != D or shape[-2] != H:
+        raise TypeError(f"{name} must be [..., {H}, {D}], got {tuple(shape)}")
+    if strides[-1] != 1 or (H > 1 and strides[-2] != D):
+        raise TypeError(f"{name}: the heads of a token must be contiguous")
+    step, upto = None, None
+    for n, st in zip(reversed(shape[:-2]), reversed(strides[:-2])):
+        if n == 1:
+            continue
+        if step is None:
+            step = upto = st
+        elif st != upto:
+            raise TypeError(f"{name}: the tokens must be evenly spaced")
+        upto *= n
+    return H * D if step is None else step
+
+
+def _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+    """Checked arguments that every form of the norm and rotation shares:
+    (weights .. positions), (tokens .. interleaved)."""
+    if q.dim() < 3 or k.dim() != q.dim() or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
+        raise TypeError(f"q and k must be [..., H, D] of the same tokens, got {tuple(q.shape)} "
+                        f"and {tuple(k.shape)}")
+    D = q.shape[-1]
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w.dtype not in (torch.bfloat16, torch.float32) or w.dtype != q_weight.dtype \
+                or tuple(w.shape) != (D,) or not w.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous bf16 or fp32 tensor of shape ({D},), "
+                            "both weights of one type")
+    for name, t in (("cos", cos), ("sin", sin)):
+        if t.dtype != torch.float32 or t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous fp32 tensor [max_positions, rot / 2]")
+    if positions.dtype != torch.int32 or positions.shape != q.shape[:-2] or not positions.is_contiguous():
+        raise TypeError(f"positions must be a contiguous int32 tensor of shape {tuple(q.shape[:-2])}")
+    return ((q_weight.data_ptr(), k_weight.data_ptr(), int(q_weight.dtype == torch.float32),
+             cos.data_ptr(), sin.data_ptr(), positions.data_ptr()),
+            (positions.numel(), q.shape[-2], k.shape[-2], D, 2 * cos.shape[1], cos.shape[0],
+             float(eps), int(bool(interleaved))))
+
+
+def rope_table(max_positions, rot, *, theta=10000.0, device="cuda"):
+    """(cos, sin), fp32 [max_positions, rot / 2], of position * theta^(-2 i / rot):
+    the angles in 64 bits (in fp32 those of far positions would be off by
+    position * 2^-24), rounded once."""
+    inv = theta ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    angles = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * inv
+    return angles.cos().float(), angles.sin().float()
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6, interleaved=False,
+                 q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q and k and the rotation by position, in one
+    pass.  Returns (q_out, k_out).
+
+    q bf16 CUDA [..., Hq, D], k bf16 [..., Hkv, D] (views of a packed QKV
+    output are fine: heads contiguous, tokens evenly spaced); weights bf16 or
+    fp32 [D]; cos, sin fp32 [max_positions, rot / 2] (see rope_table), the
+    first `rot` values of a head are rotated, in halves or, with
+    `interleaved`, in neighbouring pairs; positions int32 [...].  q_out and
+    k_out are allocated unless given; they may be q and k themselves."""
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    device = _same_device((("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight),
+                           ("cos", cos), ("sin", sin), ("positions", positions),
+                           ("q_out", q_out), ("k_out", k_out)))
+    norm, sizes = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise TypeError("q_out and k_out must have the shapes of q and k")
+    D, bf16 = q.shape[-1], (torch.bfloat16,)
+    strides = [_token_stride(n, t, t.shape[-2], D, bf16)
+               for n, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))]
+    with _on_device(device):
+        _check(lib().attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(),
+                                       k_out.data_ptr(), *strides, *norm, *sizes,
+                                       _stream_handle(stream)), "attn_qk_norm_rope")
+        _keep_for(stream, q_out, k_out)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6,
+                          interleaved=False, dq_in=None, dk_in=None, stream=None):
+    """Gradients of qk_norm_rope from dq, dk (those of its outputs; fp32 or
+    bf16, such as attention_backward returns) and its inputs.  Returns
+    (dq_in, dk_in, dq_weight, dk_weight): bf16 like q and k (allocated unless
+    given: views of a packed gradient are fine), fp32 [D]."""
+    if dq_in is None:
+        dq_in = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if dk_in is None:
+        dk_in = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    device = _same_device((("dq", dq), ("dk", dk), ("q", q), ("k", k), ("q_weight", q_weight),
+                           ("k_weight", k_weight), ("cos", cos), ("sin", sin),
+                           ("positions", positions), ("dq_in", dq_in), ("dk_in", dk_in)))
+    norm, sizes = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    if dq.shape != q.shape or dk.shape != k.shape or dq_in.shape != q.shape or dk_in.shape != k.shape:
+        raise TypeError("dq, dk, dq_in and dk_in must have the shapes of q and k")
+    D, bf16, either = q.shape[-1], (torch.bfloat16,), (torch.bfloat16, torch.float32)
+    strides = [_token_stride(n, t, t.shape[-2], D, types)
+               for n, t, types in (("dq", dq, either), ("dk", dk, either), ("q", q, bf16),
+                                   ("k", k, bf16), ("dq_in", dq_in, bf16), ("dk_in", dk_in, bf16))]
+    L = lib()
+    weights = torch.empty(2, D, dtype=torch.float32, device=device)
+    ws = torch.empty(L.attn_qk_norm_rope_bwd_workspace_size(D), dtype=torch.uint8, device=device)
+    with _on_device(device):
+        _check(L.attn_qk_norm_rope_bwd(dq.data_ptr(), dk.data_ptr(), int(dq.dtype == torch.float32),
+                                       int(dk.dtype == torch.float32), q.data_ptr(), k.data_ptr(),
+                                       dq_in.data_ptr(), dk_in.data_ptr(), weights.data_ptr(),
+                                       weights.data_ptr() + 4 * D, *strides, *norm, *sizes,
+                                       ws.data_ptr(), ws.numel(), _stream_handle(stream)),
+               "attn_qk_norm_rope_bwd")
+        _keep_for(stream, dq_in, dk_in, weights, ws)
+    return dq_in, dk_in, weights[0], weights[1]
+
+
+def _cache_type(k_cache, v_cache):
+    """ATTN_KV_* of a pair of caches [num_pages, page_size, Hkv, D]."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or t.dim() != 4 \
+                or t.shape != k_cache.shape or t.dtype != k_cache.dtype or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous bf16 or float8_e4m3fn tensor "
+                            "[num_pages, page_size, Hkv, D], both caches alike")
+    return ATTN_KV_BF16 if k_cache.dtype == torch.bfloat16 else ATTN_KV_E4M3
+
+
+def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos, sin, positions, slots, k_cache, v_cache, *,
+                       k_descale=1.0, v_descale=1.0, eps=1e-6, interleaved=False, q_out=None,
+                       stream=None):
+    """qk_norm_rope for the new tokens of a serving step: returns q_out, and
+    writes K (normed and rotated) and V of token t to slot slots[t] = page *
+    page_size + place of the caches [num_pages, page_size, Hkv, D], bf16 or
+    float8_e4m3fn (codes of value / descale).  slots int32 [...], distinct; a
+    negative slot marks padding, of which nothing is read or written (its row
+    of q_out keeps what it held)."""
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    device = _same_device((("q", q), ("k", k), ("v", v), ("q_weight", q_weight),
+                           ("k_weight", k_weight), ("cos", cos), ("sin", sin),
+                           ("positions", positions), ("slots", slots), ("k_cache", k_cache),
+                           ("v_cache", v_cache), ("q_out", q_out)))
+    norm, sizes = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    kv = _cache_type(k_cache, v_cache)
+    if v.shape != k.shape or q_out.shape != q.shape or k_cache.shape[2:] != k.shape[-2:]:
+        raise TypeError("v must have k's shape, q_out q's, and the caches k's heads")
+    if slots.dtype != torch.int32 or slots.shape != q.shape[:-2] or not slots.is_contiguous():
+        raise TypeError(f"slots must be a contiguous int32 tensor of shape {tuple(q.shape[:-2])}")
+    D, bf16 = q.shape[-1], (torch.bfloat16,)
+    strides = [_token_stride(n, t, t.shape[-2], D, bf16)
+               for n, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out))]
+    with _on_device(device):
+        _check(lib().attn_qk_norm_rope_cache(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), *strides, *norm,
+            slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv, float(k_descale),
+            float(v_descale), k_cache.shape[0] * k_cache.shape[1], *sizes, _stream_handle(stream)),
+            "attn_qk_norm_rope_cache")
+        _keep_for(stream, q_out)
+    return q_out
+
+
+def decode_workspace_size(D) -> int:
+    """Bytes of device workspace attn_decode_paged needs."""
+    return int(lib().attn_decode_paged_workspace_size(D))
+
+
+def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, scale=None, window=None, sinks=0,
+                 softcap=None, alibi_slopes=None, k_descale=1.0, v_descale=1.0, o=None, lse=None,
+                 workspace=None, stream=None):
+    """Attention of one new token per sequence over a paged cache.  Returns
+    (O, LSE).
+
+    q bf16 CUDA [B, Hq, D]; caches [num_pages, page_size, Hkv, D], bf16 or
+    float8_e4m3fn standing for descale * code; page_table int32 [B, max_pages];
+    seq_lens int32 [B], the new token counted (0: O = 0, LSE = -inf).  window
+    = (left, right) as in attention(): the last left + 1 keys stay visible, and
+    with `sinks` the first ones too.  o, lse and workspace (uint8, at least
+    decode_workspace_size(D)) are allocated unless given."""
+    if not torch.is_tensor(q) or q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise TypeError("q must be a contiguous bf16 tensor [B, Hq, D]")
+    B, Hq, D = q.shape
+    L = lib()
+    if o is None:
+        o = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(L.attn_decode_paged_workspace_size(D), dtype=torch.uint8,
+                                device=q.device)
+    slopes = _slopes(alibi_slopes, Hq, q.device, stream)
+    device = _same_device((("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
+                           ("page_table", page_table), ("seq_lens", seq_lens), ("o", o),
+                           ("lse", lse), ("workspace", workspace))
+                          + ((("alibi_slopes", slopes),) if slopes is not None else ()))
+    kv = _cache_type(k_cache, v_cache)
+    num_pages, page_size, Hkv, Dk = k_cache.shape
+    if Dk != D:
+        raise TypeError(f"the caches' heads have {Dk} values, q's {D}")
+    for name, t, dt, shape in (("page_table", page_table, torch.int32, (B, page_table.shape[-1])),
+                               ("seq_lens", seq_lens, torch.int32, (B,)),
+                               ("o", o, torch.bfloat16, (B, Hq, D)),
+                               ("lse", lse, torch.float32, (B, Hq))):
+        if t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous {dt} tensor of shape {shape}")
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 tensor")
+    wl, wr = (-1, -1) if window is None else (int(window[0]), int(window[1]))
+    if wr < -1:
+        raise ValueError("window bounds must be -1 or >= 0")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _on_device(device):
+        _check(L.attn_decode_paged(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv, float(k_descale),
+            float(v_descale), page_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+            lse.data_ptr(), B, Hq, Hkv, D, num_pages, page_size, page_table.shape[1],
+            float(scale), wl, int(sinks), float(softcap or 0.0),
+            None if slopes is None else slopes.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), _stream_handle(stream)), "attn_decode_paged")
+        _keep_for(stream, o, lse, workspace)
+    return o, lse
 
 
 def device_status(stream=None) -> int:

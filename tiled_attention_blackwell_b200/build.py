@@ -22,27 +22,32 @@ LIB = os.path.join(PKG, "libattn.so")
 COUNT_LIB = os.path.join(PKG, "libattn_count.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
+# attn_api.cu: the forward and backward; serve_api.cu: head norms with
+# rotation, the paged cache and its decode.
+UNITS = ("attn_api.cu", "serve_api.cu")
+
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-std=c++17", "-lineinfo",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-    "-shared",
+    "-shared", "--threads", "0",
 ]
 
 
 def _sources():
     deps = glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    deps += glob.glob(os.path.join(CSRC, "*.h"))
     deps.append(os.path.join(ROOT, "include", "attn.h"))
     return deps
 
 
-def _build_one(out: str, defines, force: bool, verbose: bool) -> str:
+def _build_one(out: str, units, defines, force: bool, verbose: bool) -> str:
     newest = max(os.path.getmtime(p) for p in _sources())
     if not force and os.path.exists(out) and os.path.getmtime(out) >= newest:
         return out
     tmp = out + f".tmp{os.getpid()}"
     cmd = [NVCC, *NVCC_FLAGS, *[f"-D{d}" for d in defines], "-o", tmp,
-           os.path.join(CSRC, "attn_api.cu")]
+           *[os.path.join(CSRC, u) for u in units]]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
@@ -51,13 +56,13 @@ def _build_one(out: str, defines, force: bool, verbose: bool) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/attn_api.cu (and the kernels it includes) into libattn.so."""
-    return _build_one(LIB, (), force, verbose)
+    """Compile the translation units (and the kernels they include) into libattn.so."""
+    return _build_one(LIB, UNITS, (), force, verbose)
 
 
 def build_count(force: bool = False, verbose: bool = False) -> str:
     """The rescale-statistics build, libattn_count.so."""
-    return _build_one(COUNT_LIB, ("ATTN_COUNT_RESCALES",), force, verbose)
+    return _build_one(COUNT_LIB, UNITS, ("ATTN_COUNT_RESCALES",), force, verbose)
 
 
 if __name__ == "__main__":

@@ -18,12 +18,29 @@
 #include "fwd_fp4_kernel.cuh"
 #include "fwd_kernel.cuh"
 #include "fwd_persistent.cuh"
+#include "host_common.h"
+
+using tab_host::aligned16;
+using tab_host::device_state;
+using tab_host::DeviceState;
+using tab_host::encode_fn;
+using tab_host::EncodeTiledFn;
+using tab_host::fail;
+using tab_host::kMaxDevices;
+using tab_host::ok;
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-
 thread_local char g_detail[512] = "";
+
+// The device status word.
+__device__ int g_status_word;
+
+DeviceState g_devices[kMaxDevices];
+
+}  // namespace
+
+namespace tab_host {
 
 attn_status_t fail(attn_status_t status, const char *fmt, ...) {
     va_list ap;
@@ -37,18 +54,6 @@ attn_status_t ok() {
     g_detail[0] = '\0';
     return ATTN_OK;
 }
-
-// ------------------------------------------------------- device status word
-
-__device__ int g_status_word;
-
-struct DeviceState {
-    std::once_flag once;
-    cudaError_t init_error = cudaSuccess;
-    int *status = nullptr;  // device address of g_status_word
-    int num_sms = 0;
-};
-DeviceState g_devices[kMaxDevices];
 
 attn_status_t device_state(DeviceState **out) {
     int dev = 0;
@@ -67,13 +72,6 @@ attn_status_t device_state(DeviceState **out) {
     return ATTN_OK;
 }
 
-// ----------------------------------------------------------- tensor maps
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_fn() {
     static std::once_flag once;
     static EncodeTiledFn fn = nullptr;
@@ -87,6 +85,12 @@ EncodeTiledFn encode_fn() {
     });
     return fn;
 }
+
+}  // namespace tab_host
+
+namespace {
+
+// ----------------------------------------------------------- tensor maps
 
 // bf16 tensor [B][S][H][D] as a 4-D map (D, S, H, B), box (64, 128, 1, 1),
 // 128-byte swizzle, zero fill out of bounds.
@@ -309,8 +313,6 @@ Fp4BsLayout fp4bs_layout(int B, int Hq, int Hkv, int Sq, int Sk) {
     L.total = L.vt + align256((size_t)B * Hkv * 128 * L.nkt * 64);
     return L;
 }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Shape and mask checks shared by the forward and the backward.
 attn_status_t check_common(int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,

@@ -1,0 +1,686 @@
+// Attention of one new token per sequence over a paged key/value cache.
+//
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(s_j - max s),  s_j = scale <q, k_j>
+// over the keys j < len that a window and its first tokens leave visible.
+//
+// Bound by memory: every visible key's K and V are read once (4 D bytes per
+// key and key head in bf16) for 4 D operations per query head, far below the
+// tensor cores' rate for any group of heads.  So the work is cut by bytes,
+// not by heads: the tiles of kTile keys of all (sequence, key head) pairs
+// form one list, and each block takes an equal run of it, whatever the
+// lengths are.  A block that holds all of a pair's tiles writes its output;
+// a pair that crosses a block's end leaves partial results (maximum, sums,
+// unnormalised output), which decode_join_kernel joins in the order of the
+// blocks, so the result does not depend on the timing.
+//
+// Warp roles: warps 0 .. kWarps-1 compute, warp kWarps copies.  The copying
+// warp walks the block's whole run ahead of the computing ones, across the
+// ends of pairs, so the copies never pause: 16 keys of K and of V are one
+// TMA box each (a page holds a multiple of 16 keys), in a ring of kStages
+// tiles.  Computing warp w takes every kWarps-th tile and keeps its own
+// running maximum, sums and output in registers; they are joined through
+// shared memory at the end of a pair.
+//
+// Products: mma.sync m16n8k16 with up to 16 query heads of one key head as
+// rows.  (tcgen05 needs 64 rows or more; here the tensor pipe is idle most of
+// the time either way, and the registers hold S, P and O without a trip
+// through tensor memory.)  An e4m3 cache is widened to f16 in registers,
+// exactly; Q is scaled by a power of two per row so that f16 holds it.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace tab {
+
+constexpr int kDecWarps = 4;                         // computing warps
+constexpr int kDecThreads = (kDecWarps + 1) * 32;
+constexpr int kDecRows = 16;                         // query heads per pair
+constexpr int kDecBlock = 16;                        // keys per TMA box
+constexpr int kDecCtasPerSm = 2;
+// Fewest tiles per block: one for each computing warp.
+constexpr int kDecMinTiles = kDecWarps;
+// A row's maximum moves only when a tile raises it by more than this (log2
+// units), as in the forward; P stays below 2^8.
+constexpr float kDecTau = 8.0f;
+
+struct DecodeParams {
+    CUtensorMap tm_k, tm_v;  // [pages][page_size][Hkv][D], box 16 keys of one head
+    const __nv_bfloat16 *q;  // [B][Hq][D]
+    __nv_bfloat16 *o;        // [B][Hq][D]
+    float *lse;              // [B][Hq]
+    const int *page_table;   // [B][max_pages]
+    const int *seq_lens;     // [B], the new token counted
+    int *status;
+    // Workspace: per block two partial results (a pair that begins before
+    // the block, one that ends behind it) and one record.
+    float *part_o;           // [blocks][2][16][D], relative to the partial's maximum
+    float4 *part_ml;         // [blocks][2][16]: maximum (log2), sum, sum of the rounded weights
+    int4 *record;            // [blocks]: the pair that is first cut at this block's end
+    int B, Hq, Hkv, group, hchunks;
+    int max_pages, page_size, num_pages;
+    int window_left, sinks;
+    float scale_log2;        // scale * k_descale * log2(e)
+    float v_descale;
+    float softcap_in, softcap_out;  // scale * k_descale / cap, cap * log2(e); 0: none
+    const float *alibi_slopes;
+};
+
+// The visible tiles of a sequence: ns tiles from key 0 on (first tokens),
+// then those from tile w0 on.  `lo` is the window's first key.
+struct SeqTiles {
+    int len, lo, ns, w0, n;
+};
+
+template <int kTile>
+__device__ __forceinline__ SeqTiles seq_tiles(const DecodeParams &p, int b) {
+    SeqTiles s;
+    s.len = min(max(__ldg(p.seq_lens + b), 0), p.max_pages * p.page_size);
+    s.lo = p.window_left >= 0 ? max(0, s.len - 1 - p.window_left) : 0;
+    s.w0 = s.lo / kTile;
+    s.ns = min((min(p.sinks, s.lo) + kTile - 1) / kTile, s.w0);
+    s.n = s.ns + (s.len + kTile - 1) / kTile - s.w0;
+    return s;
+}
+
+// 16-bit operand type of the products: bf16, or f16 for an e4m3 cache.
+template <bool F8>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    if constexpr (F8)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// The f16 pairs of the low and the high two e4m3 codes of a word (exact).
+__device__ __forceinline__ void widen_e4m3x4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// A pair of weights in the operand type, and the sum of the rounded values.
+template <bool F8>
+__device__ __forceinline__ uint32_t pack_weights(float p0, float p1, float &sum) {
+    if constexpr (F8) {
+        const uint32_t h = pack_f16x2(p0, p1);
+        sum += f16x2_sum(h);
+        return h;
+    } else {
+        const uint32_t h = pack_bf16x2(p0, p1);
+        sum += __uint_as_float(h << 16) + __uint_as_float(h & 0xffff0000u);
+        return h;
+    }
+}
+
+// kBlocks boxes of 16 keys per tile.
+template <int D, bool F8, int kBlocks, int kStages>
+struct DecodeSmem {
+    static constexpr int kRowBytes = D * (F8 ? 1 : 2);
+    static constexpr int kBoxBytes = kDecBlock * kRowBytes;
+    static constexpr int kTile = kDecBlock * kBlocks;
+    uint8_t k[kStages][kBlocks][kBoxBytes];
+    uint8_t v[kStages][kBlocks][kBoxBytes];
+    float o[kDecWarps][kDecRows][D + 4];  // + 4: rows start in different banks
+    float4 ml[kDecWarps][kDecRows];
+    uint64_t full[kStages], empty[kStages];
+    long long start, end, share, base;    // this block's run; tiles before sequence b0
+    int b0;
+    int abort_flag;
+};
+
+// Shared-memory byte of 16-byte piece `c` of key row `r` of a box: rows of
+// 128 bytes with the 128-byte swizzle (one chunk of the box per 128 bytes of
+// the row), or of 64 bytes with the 64-byte swizzle.
+template <int kRowBytes>
+__device__ __forceinline__ uint32_t box_offset(int r, int c) {
+    if constexpr (kRowBytes >= 128)
+        return (uint32_t)((c >> 3) * (kDecBlock * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    else
+        return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+template <int D, bool F8, int kBlocks, int kStages>
+__global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
+decode_paged_kernel(const __grid_constant__ DecodeParams p) {
+    using Smem = DecodeSmem<D, F8, kBlocks, kStages>;
+    constexpr int kTile = Smem::kTile;
+    constexpr int kPieces = Smem::kRowBytes / 16;  // 16-byte pieces of a row
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_off = smem_u32(smem_raw);
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (raw_off & 1023u)) & 1023u));
+    const int warp = warp_id(), lane = lane_id();
+    const int H = p.Hkv * p.hchunks;  // pairs per sequence
+    volatile int *abort_flag = &sm.abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        sm.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kDecWarps) {
+        if (lane == 0) {
+            prefetch_tensormap(&p.tm_k);
+            prefetch_tensormap(&p.tm_v);
+        }
+        // Tiles of all sequences, then this block's run and where it begins.
+        long long total = 0;
+        for (int b = lane; b < p.B; b += 32) total += (long long)seq_tiles<kTile>(p, b).n * H;
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        const long long share =
+            max((long long)kDecMinTiles, (total + gridDim.x - 1) / (long long)gridDim.x);
+        const long long start = min(total, share * blockIdx.x);
+        const long long end = min(total, start + share);
+        long long base = 0;
+        int b0 = 0;
+        for (int c = 0; c < p.B && start < end; c += 32) {
+            const long long n = c + lane < p.B ? (long long)seq_tiles<kTile>(p, c + lane).n * H : 0;
+            long long upto = n;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += t;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, base + upto > start);
+            if (past) {
+                const int at = __ffs(past) - 1;
+                b0 = c + at;
+                base += __shfl_sync(0xffffffffu, upto - n, at);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        if (lane == 0) {
+            sm.start = start;
+            sm.end = end;
+            sm.share = share;
+            sm.base = base;
+            sm.b0 = b0;
+        }
+    }
+    __syncthreads();
+    const long long start = sm.start, end = sm.end;
+
+    if (warp == kDecWarps) {
+        // ------------------------------------------------------------ copies
+        const uint32_t n_tiles = (uint32_t)(end - start);
+        // Each lane looks up one tile of the next 32: its pair and its pages.
+        long long base = sm.base;
+        int b = sm.b0;
+        struct Item {
+            int page[kBlocks], row[kBlocks], hkv, blocks;
+        };
+        auto look_up = [&](uint32_t g) {
+            Item it{};
+            if (g >= n_tiles) return it;
+            const long long pos = start + g;
+            SeqTiles st = seq_tiles<kTile>(p, b);
+            while (b + 1 < p.B && pos >= base + (long long)st.n * H) {
+                base += (long long)st.n * H;
+                st = seq_tiles<kTile>(p, ++b);
+            }
+            const uint32_t in_seq = (uint32_t)(pos - base);
+            const uint32_t pair = in_seq / (uint32_t)st.n;
+            const int t = (int)(in_seq - pair * (uint32_t)st.n);
+            const int key0 = (t < st.ns ? t : st.w0 + t - st.ns) * kTile;
+            it.hkv = (int)(pair / (uint32_t)p.hchunks);
+#pragma unroll
+            for (int u = 0; u < kBlocks; ++u) {
+                const int key = key0 + u * kDecBlock;
+                if (key < st.len) {
+                    it.blocks = u + 1;
+                    const int page = key / p.page_size;
+                    it.row[u] = key - page * p.page_size;
+                    int at = __ldg(p.page_table + (size_t)b * p.max_pages + page);
+                    if (at < 0 || at >= p.num_pages) {  // reported; page 0 stands in
+                        atomicCAS(p.status, 0, kStatusRange);
+                        at = 0;
+                    }
+                    it.page[u] = at;
+                }
+            }
+            return it;
+        };
+        bool ok = true;
+        uint32_t issued = 0;
+        Item next = look_up(lane);
+        for (uint32_t g0 = 0; g0 < n_tiles && ok; g0 += 32) {
+            const Item it = next;
+            next = look_up(g0 + 32 + lane);
+            const uint32_t n = min(32u, n_tiles - g0);
+            for (uint32_t i = 0; i < n && ok; ++i) {
+                const int hkv = __shfl_sync(0xffffffffu, it.hkv, i);
+                const int blocks = __shfl_sync(0xffffffffu, it.blocks, i);
+                int page[kBlocks], row[kBlocks];
+#pragma unroll
+                for (int u = 0; u < kBlocks; ++u) {
+                    page[u] = __shfl_sync(0xffffffffu, it.page[u], i);
+                    row[u] = __shfl_sync(0xffffffffu, it.row[u], i);
+                }
+                const uint32_t s = issued % kStages;
+                ok = __all_sync(0xffffffffu, wait_bounded(&sm.empty[s], ((issued / kStages) & 1u) ^ 1u,
+                                                          abort_flag, p.status));
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sm.full[s], (uint32_t)blocks * 2u * Smem::kBoxBytes);
+                    for (int u = 0; u < blocks; ++u)
+                        tma_load_5d(sm.k[s][u], &p.tm_k, &sm.full[s], 0, row[u], 0, hkv, page[u]);
+                    for (int u = 0; u < blocks; ++u)
+                        tma_load_5d(sm.v[s][u], &p.tm_v, &sm.full[s], 0, row[u], 0, hkv, page[u]);
+                }
+                __syncwarp();
+                ++issued;
+            }
+        }
+        // Copies still in flight land before the block can exit.
+        for (uint32_t g = issued > kStages ? issued - kStages : 0; g < issued; ++g)
+            wait_bounded(&sm.full[g % kStages], (g / kStages) & 1u, abort_flag, p.status, false);
+        return;
+    }
+
+    // --------------------------------------------------------------- compute
+    const int qr = lane >> 2, qc = lane & 3;  // row (and row + 8) and column pair of a fragment
+    // Sequences without a key: zeros and -inf (each block takes every
+    // gridDim.x-th sequence).
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        if (seq_tiles<kTile>(p, b).n > 0) continue;
+        for (int i = threadIdx.x; i < p.Hq * (D / 8); i += kDecWarps * 32)
+            *reinterpret_cast<uint4 *>(p.o + (size_t)b * p.Hq * D + (size_t)i * 8) = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = threadIdx.x; i < p.Hq; i += kDecWarps * 32) p.lse[(size_t)b * p.Hq + i] = -INFINITY;
+    }
+    if (blockIdx.x == 0) {  // out-of-range lengths are clamped and reported
+        for (int b = threadIdx.x; b < p.B; b += kDecWarps * 32) {
+            const int len = __ldg(p.seq_lens + b);
+            if (len < 0 || len > p.max_pages * p.page_size) atomicCAS(p.status, 0, kStatusRange);
+        }
+    }
+    if (threadIdx.x == 0) p.record[blockIdx.x] = make_int4(0, 0, 0, 0);
+
+    bool ok = true;
+    long long pos = start, base = sm.base;
+    int b = sm.b0;
+    while (pos < end && b < p.B) {
+        const SeqTiles st = seq_tiles<kTile>(p, b);
+        if (pos >= base + (long long)st.n * H) {
+            base += (long long)st.n * H;
+            ++b;
+            continue;
+        }
+        const uint32_t in_seq = (uint32_t)(pos - base);
+        const int pair = (int)(in_seq / (uint32_t)st.n);
+        const int t0 = (int)(in_seq - (uint32_t)pair * (uint32_t)st.n);
+        const int t1 = (int)min((long long)st.n, t0 + (end - pos));
+        const int hkv = pair / p.hchunks, r0 = (pair - hkv * p.hchunks) * kDecRows;
+        const int rows = min(kDecRows, p.group - r0);
+        const int hq0 = hkv * p.group + r0;
+
+        // Q as the A operand.  bf16: K index k of step ks is value 16 ks + k.
+        // e4m3: the B operand's word holds four neighbouring values, so index
+        // (2c, 2c+1, 2c+8, 2c+9) is value 16 ks + 4c + (0..3) on both sides.
+        uint32_t a[D / 16][4];
+        float c_row[2] = {p.scale_log2, p.scale_log2};
+        float cap_row[2] = {p.softcap_in * (2.0f * kLog2eF), p.softcap_in * (2.0f * kLog2eF)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = qr + 8 * h;
+            const __nv_bfloat16 *q = p.q + ((size_t)b * p.Hq + hq0 + (r < rows ? r : 0)) * D;
+            if constexpr (F8) {
+                uint2 w[D / 16];
+                float amax = 0.0f;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    w[ks] = r < rows ? *reinterpret_cast<const uint2 *>(q + 16 * ks + 4 * qc) : make_uint2(0u, 0u);
+                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(__uint_as_float(w[ks].x << 16)),
+                                                   fabsf(__uint_as_float(w[ks].x & 0xffff0000u))),
+                                             fmaxf(fabsf(__uint_as_float(w[ks].y << 16)),
+                                                   fabsf(__uint_as_float(w[ks].y & 0xffff0000u)))));
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                // 2^-e with amax in [2^e, 2^(e+1)); e within [-100, 120], and 0 for
+                // rows of zeros or with infinities (f16 keeps those).
+                int e = (int)(__float_as_uint(amax) >> 23) - 127;
+                e = amax == 0.0f || e > 127 ? 0 : min(max(e, -100), 120);
+                const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+                c_row[h] *= up;
+                cap_row[h] *= up;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    a[ks][h] = pack_f16x2(__uint_as_float(w[ks].x << 16) * down,
+                                          __uint_as_float(w[ks].x & 0xffff0000u) * down);
+                    a[ks][2 + h] = pack_f16x2(__uint_as_float(w[ks].y << 16) * down,
+                                              __uint_as_float(w[ks].y & 0xffff0000u) * down);
+                }
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    a[ks][h] = r < rows ? *reinterpret_cast<const uint32_t *>(q + 16 * ks + 2 * qc) : 0u;
+                    a[ks][2 + h] = r < rows ? *reinterpret_cast<const uint32_t *>(q + 16 * ks + 8 + 2 * qc) : 0u;
+                }
+            }
+        }
+        float slope[2] = {0.0f, 0.0f};
+        if (p.alibi_slopes) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (qr + 8 * h < rows) slope[h] = __ldg(p.alibi_slopes + hq0 + qr + 8 * h) * kLog2eF;
+        }
+
+        float acc[D / 8][4];
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, lr[2] = {0.0f, 0.0f};
+
+        // This warp's tiles of the pair.
+        const uint32_t g0 = (uint32_t)(pos - start);
+        int t = t0 + (int)((warp + kDecWarps - g0 % kDecWarps) % kDecWarps);
+        for (; t < t1; t += kDecWarps) {
+            const uint32_t g = g0 + (uint32_t)(t - t0);
+            const uint32_t s = g % kStages;
+            if (ok)
+                ok = __all_sync(0xffffffffu, wait_bounded(&sm.full[s], (g / kStages) & 1u, abort_flag, p.status));
+            if (!ok) break;
+            const int tile0 = (t < st.ns ? t : st.w0 + t - st.ns) * kTile;
+#pragma unroll
+            for (int u = 0; u < kBlocks; ++u) {
+                const int key0 = tile0 + u * kDecBlock;
+                if (key0 >= st.len) break;
+                // S of 16 keys: two column blocks, each in two chains.
+                float sacc[2][2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sacc[n][0][e] = sacc[n][1][e] = 0.0f;
+                const uint32_t kb = smem_u32(sm.k[s][u]);
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int x = 0; x < kPieces; x += 4) {
+                        uint32_t w[4];
+                        ldsm4(w, kb + box_offset<Smem::kRowBytes>(n * 8 + (lane & 7), x + (lane >> 3)));
+                        if constexpr (F8) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t b0, b1;
+                                widen_e4m3x4(w[i], b0, b1);
+                                mma16816<true>(sacc[n][i & 1], a[x + i], b0, b1);
+                            }
+                        } else {
+                            mma16816<false>(sacc[n][0], a[x / 2], w[0], w[1]);
+                            mma16816<false>(sacc[n][1], a[x / 2 + 1], w[2], w[3]);
+                        }
+                    }
+                // Log2 scores.  x[h][i]: row qr + 8 h, key key0 + 2 qc + (i & 1) + 8 (i >> 1).
+                float x[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[h][i] = sacc[i >> 1][0][2 * h + (i & 1)] + sacc[i >> 1][1][2 * h + (i & 1)];
+                if (p.softcap_out > 0.0f) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2) {
+                            float r0, r1;
+                            softcap_pair(x[h][i], x[h][i + 1], r0, r1, x[h][i], x[h][i + 1],
+                                         cap_row[h], p.softcap_out);
+                        }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[h][i] *= c_row[h];
+                }
+                if (p.alibi_slopes) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float dist = (float)(st.len - 1 - (key0 + 2 * qc + (i & 1) + 8 * (i >> 1)));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) x[h][i] = fmaf(-slope[h], dist, x[h][i]);
+                    }
+                }
+                // Keys that the mask hides: their scores become -inf and their
+                // values zero, so what lies in them (NaN too) has no part.
+                uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;
+                const bool masked = key0 + kDecBlock > st.len ||
+                                    (key0 < st.lo && key0 + kDecBlock > p.sinks);
+                if (masked) {
+                    bool see[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = key0 + 2 * qc + (i & 1) + 8 * (i >> 1);
+                        see[i] = key < st.len && (key >= st.lo || key < p.sinks);
+                        if (!see[i]) x[0][i] = x[1][i] = -INFINITY;
+                    }
+                    see0 = (see[0] ? 0xffffu : 0u) | (see[1] ? 0xffff0000u : 0u);
+                    see1 = (see[2] ? 0xffffu : 0u) | (see[3] ? 0xffff0000u : 0u);
+                }
+                uint32_t pa[4];
+                float alpha[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float mx = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    alpha[h] = 1.0f;
+                    if (mx > m[h] + kDecTau) {
+                        alpha[h] = ex2_mufu(m[h] - mx);
+                        m[h] = mx;
+                    }
+                    const float neg_m = m[h] == -INFINITY ? 0.0f : -m[h];
+                    float e[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) e[i] = ex2_mufu(x[h][i] + neg_m);
+                    l[h] = fmaf(l[h], alpha[h], (e[0] + e[1]) + (e[2] + e[3]));
+                    float rounded = 0.0f;
+                    pa[h] = pack_weights<F8>(e[0], e[1], rounded);
+                    pa[2 + h] = pack_weights<F8>(e[2], e[3], rounded);
+                    lr[h] = fmaf(lr[h], alpha[h], rounded);
+                }
+                if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j) {
+                        acc[j][0] *= alpha[0];
+                        acc[j][1] *= alpha[0];
+                        acc[j][2] *= alpha[1];
+                        acc[j][3] *= alpha[1];
+                    }
+                }
+                // O += P V.  bf16: acc[j] is values 8 j ..; e4m3: acc[2 j] the even
+                // and acc[2 j + 1] the odd values of 16 j ...
+                const uint32_t vb = smem_u32(sm.v[s][u]);
+#pragma unroll
+                for (int j = 0; j < kPieces; j += 2) {
+                    uint32_t w[4];
+                    ldsm4_trans(w, vb + box_offset<Smem::kRowBytes>((lane & 7) + ((lane >> 3) & 1) * 8,
+                                                                    j + (lane >> 4)));
+                    if (masked) {
+                        w[0] &= see0;
+                        w[1] &= see1;
+                        w[2] &= see0;
+                        w[3] &= see1;
+                    }
+                    if constexpr (F8) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t e0, o0, e1, o1;
+                            widen_e4m3x4(__byte_perm(w[2 * i], 0u, 0x3120), e0, o0);
+                            widen_e4m3x4(__byte_perm(w[2 * i + 1], 0u, 0x3120), e1, o1);
+                            mma16816<true>(acc[2 * (j + i)], pa, e0, e1);
+                            mma16816<true>(acc[2 * (j + i) + 1], pa, o0, o1);
+                        }
+                    } else {
+                        mma16816<false>(acc[j], pa, w[0], w[1]);
+                        mma16816<false>(acc[j + 1], pa, w[2], w[3]);
+                    }
+                }
+            }
+            __syncwarp();  // every lane has read the tile
+            if (lane == 0) mbar_arrive(&sm.empty[s]);
+        }
+
+        // ------------------------------------------- join the warps' results
+        // Every warp comes here for every pair, with or without a tile of it
+        // (and after a wait that ran out), so the barriers below always meet.
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            for (int o = 1; o < 4; o <<= 1) {
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+                lr[h] += __shfl_xor_sync(0xffffffffu, lr[h], o);
+            }
+            const int r = qr + 8 * h;
+            if (r < rows) {
+                if (qc == 0) sm.ml[warp][r] = make_float4(m[h], l[h], lr[h], 0.0f);
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    if constexpr (F8) {
+                        float *dst = &sm.o[warp][r][16 * (j >> 1) + 4 * qc + (j & 1)];
+                        dst[0] = acc[j][2 * h];
+                        dst[2] = acc[j][2 * h + 1];
+                    } else {
+                        *reinterpret_cast<float2 *>(&sm.o[warp][r][8 * j + 2 * qc]) =
+                            make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+                    }
+                }
+            }
+        }
+        named_bar_sync(1, kDecWarps * 32);
+        const bool whole = t0 == 0 && t1 == st.n;
+        const int which = t0 == 0 ? 1 : 0;
+        const size_t part = (size_t)blockIdx.x * 2 + which;
+        for (int i = threadIdx.x; i < rows * (D / 4); i += kDecWarps * 32) {
+            const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+            float mx = sm.ml[0][r].x;
+#pragma unroll
+            for (int w = 1; w < kDecWarps; ++w) mx = fmaxf(mx, sm.ml[w][r].x);
+            float ls = 0.0f, lrs = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w) {
+                const float4 ml = sm.ml[w][r];
+                const float f = ml.x == -INFINITY ? 0.0f : ex2_mufu(ml.x - mx);
+                const float4 ow = *reinterpret_cast<const float4 *>(&sm.o[w][r][d]);
+                ls = fmaf(ml.y, f, ls);
+                lrs = fmaf(ml.z, f, lrs);
+                o.x = fmaf(ow.x, f, o.x);
+                o.y = fmaf(ow.y, f, o.y);
+                o.z = fmaf(ow.z, f, o.z);
+                o.w = fmaf(ow.w, f, o.w);
+            }
+            if (whole) {
+                const size_t row = (size_t)b * p.Hq + hq0 + r;
+                const float inv = lrs == 0.0f ? 0.0f : p.v_descale / lrs;
+                *reinterpret_cast<uint2 *>(p.o + row * D + d) =
+                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+                if (d == 0) p.lse[row] = ls == 0.0f ? -INFINITY : (mx + log2f(ls)) * 0.69314718055994531f;
+            } else {
+                *reinterpret_cast<float4 *>(p.part_o + (part * kDecRows + r) * D + d) = o;
+                if (d == 0) p.part_ml[part * kDecRows + r] = make_float4(mx, ls, lrs, 0.0f);
+            }
+        }
+        // A pair that begins here and goes on: the join starts at this block.
+        if (t0 == 0 && t1 < st.n && threadIdx.x == 0) {
+            const long long last = pos + st.n - 1;
+            p.record[blockIdx.x] = make_int4(b, hq0, rows, (int)(last / sm.share));
+        }
+        named_bar_sync(1, kDecWarps * 32);  // the buffers are free again
+        pos += t1 - t0;
+    }
+}
+
+// Joins the partial results of the pair that is first cut at the end of block
+// blockIdx.x: row blockIdx.y of it.  The partials are those of that block
+// (its second) and of the blocks up to the recorded one (their first).
+constexpr int kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+decode_join_kernel(const DecodeParams p) {
+    constexpr int kCols = D / 4, kParts = kJoinThreads / kCols;  // float4 columns, rows of threads
+    __shared__ float red[kJoinThreads / 32];
+    __shared__ float4 sum_o[kParts][kCols];
+    __shared__ float2 sum_l[kParts];
+    const int4 rec = p.record[blockIdx.x];
+    const int row = blockIdx.y;
+    if (row >= rec.z) return;
+    const int first = blockIdx.x, n = rec.w - first + 1;
+    auto part_row = [&](int i) {
+        return ((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * kDecRows + row;
+    };
+    float mx = -INFINITY;
+    for (int i = threadIdx.x; i < n; i += kJoinThreads) mx = fmaxf(mx, p.part_ml[part_row(i)].x);
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane_id() == 0) red[warp_id()] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, red[w]);
+    const int part = threadIdx.x / kCols, c = threadIdx.x % kCols;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float2 l = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = part; i < n; i += kParts) {
+        const float4 ml = p.part_ml[part_row(i)];
+        const float4 v = *reinterpret_cast<const float4 *>(p.part_o + part_row(i) * D + 4 * c);
+        const float f = ml.x == -INFINITY ? 0.0f : ex2_mufu(ml.x - mx);
+        l.x = fmaf(ml.y, f, l.x);
+        l.y = fmaf(ml.z, f, l.y);
+        o.x = fmaf(v.x, f, o.x);
+        o.y = fmaf(v.y, f, o.y);
+        o.z = fmaf(v.z, f, o.z);
+        o.w = fmaf(v.w, f, o.w);
+    }
+    sum_o[part][c] = o;
+    if (c == 0) sum_l[part] = l;
+    __syncthreads();
+    if (part == 0) {
+        o = sum_o[0][c];
+        l = sum_l[0];
+#pragma unroll
+        for (int w = 1; w < kParts; ++w) {
+            const float4 v = sum_o[w][c];
+            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+            l.x += sum_l[w].x, l.y += sum_l[w].y;
+        }
+        const size_t out = (size_t)rec.x * p.Hq + rec.y + row;
+        const float inv = l.y == 0.0f ? 0.0f : p.v_descale / l.y;
+        *reinterpret_cast<uint2 *>(p.o + out * D + 4 * c) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (c == 0) p.lse[out] = l.x == 0.0f ? -INFINITY : (mx + log2f(l.x)) * 0.69314718055994531f;
+    }
+}
+
+}  // namespace tab
