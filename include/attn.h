@@ -144,6 +144,20 @@ ATTN_API attn_status_t attn_fwd_ex(const void *q, const void *k, const void *v, 
                           const attn_fwd_options_t *opts, void *stream);
 
 /*
+ * attn_fwd_ex for a sliding window with `sinks` first keys that stay visible
+ * (the attention pages name sliding windows; a window that loses a stream's
+ * first tokens changes every later row, so serving keeps a few of them):
+ * key j is visible for row i iff the upper ends allow it (causal,
+ * window_right) and j >= i + shift - window_left or j < sinks.  sinks >= 0;
+ * without a window's lower end (window_left = -1) they change nothing.  The
+ * other rules are those of attn_fwd_ex; there is no document mask.
+ */
+ATTN_API attn_status_t attn_fwd_sinks(const void *q, const void *k, const void *v, void *o,
+                                      float *lse, int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                                      float scale, int causal, int window_left, int window_right,
+                                      int sinks, const attn_fwd_options_t *opts, void *stream);
+
+/*
  * Low-precision forward ("Hardware-Aware FP4 FlashAttention-4", "Precisión":
  * the FP8 path that Direct-P is measured against).  q, k, v hold fp8 e4m3
  * codes (1 byte each, same [B,S,H,D] layouts, 16-byte aligned); the values
@@ -302,6 +316,19 @@ ATTN_API attn_status_t attn_bwd_ex(const void *q, const void *k, const void *v, 
                                    const int *doc_offsets, int num_docs, void *workspace,
                                    size_t workspace_bytes, const attn_bwd_options_t *opts,
                                    void *stream);
+
+/* attn_bwd_ex under the mask of attn_fwd_sinks.  The workspace holds partial
+ * sums of the first keys' gradients too: attn_bwd_sinks_workspace_size()
+ * bytes (with sinks = 0, those of attn_bwd_workspace_size()). */
+ATTN_API size_t attn_bwd_sinks_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                                              int sinks);
+
+ATTN_API attn_status_t attn_bwd_sinks(const void *q, const void *k, const void *v, const void *o,
+                                      const float *lse, const void *dout, float *dq, void *dk,
+                                      void *dv, int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                                      float scale, int causal, int window_left, int window_right,
+                                      int sinks, void *workspace, size_t workspace_bytes,
+                                      const attn_bwd_options_t *opts, void *stream);
 
 /*
  * attn_bwd without a workspace argument, for callers that cannot allocate

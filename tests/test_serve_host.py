@@ -185,3 +185,69 @@ def test_decode_binding_refuses(L, name, bad):
     with pytest.raises(TypeError):
         attn.decode_paged(*t.values(), o=stand_in(2, 4, 128), lse=stand_in(2, 4, dtype=torch.float32),
                           workspace=stand_in(1 << 23, dtype=torch.uint8), stream=0)
+
+
+# ------------------------------------------------- windows with first tokens
+
+def call_fwd_sinks(L, **kw):
+    a = dict(q=P, k=P, v=P, o=P, lse=P, B=1, Hq=2, Hkv=2, Sq=16, Sk=16, D=128, scale=0.1, causal=1, wl=7, wr=-1,
+             sinks=4, opts=None)
+    a.update(kw)
+    return L.attn_fwd_sinks(a["q"], a["k"], a["v"], a["o"], a["lse"], a["B"], a["Hq"], a["Hkv"], a["Sq"], a["Sk"],
+                            a["D"], a["scale"], a["causal"], a["wl"], a["wr"], a["sinks"],
+                            None if a["opts"] is None else ctypes.byref(a["opts"]), None)
+
+
+def call_bwd_sinks(L, **kw):
+    a = dict(q=P, k=P, v=P, o=P, lse=P, dout=P, dq=P, dk=P, dv=P, B=1, Hq=2, Hkv=2, Sq=16, Sk=16, D=128, scale=0.1,
+             causal=1, wl=7, wr=-1, sinks=4, ws=P, wsb=1 << 24, opts=None)
+    a.update(kw)
+    return L.attn_bwd_sinks(*[a[n] for n in ("q", "k", "v", "o", "lse", "dout", "dq", "dk", "dv", "B", "Hq", "Hkv",
+                                             "Sq", "Sk", "D", "scale", "causal", "wl", "wr", "sinks", "ws", "wsb")],
+                            None if a["opts"] is None else ctypes.byref(a["opts"]), None)
+
+
+@pytest.mark.parametrize("call", [call_fwd_sinks, call_bwd_sinks])
+@pytest.mark.parametrize("kw,status", [
+    (dict(sinks=-1), INV), (dict(q=0), INV), (dict(lse=0), INV), (dict(B=0), INV), (dict(Hq=3, Hkv=2), INV),
+    (dict(D=96), UNS), (dict(scale=0.0), INV), (dict(wl=-2), INV), (dict(wr=-2), INV), (dict(v=P + 8), MIS)])
+def test_sinks_refusals(L, call, kw, status):
+    assert call(L, **kw) == status
+    assert L.attn_last_error_detail().decode() != ""
+
+
+def test_sinks_workspace(L):
+    size = attn.bwd_workspace_size(2, 16, 16, 4096, 4096, 128, 4)
+    # D_i, and for the one block with first keys four parts of 8 of the 32 query blocks: fp32 dK and dV
+    assert size == 2 * 16 * 4096 * 4 + 4 * 1 * 2 * 16 * 2 * 128 * 128 * 4
+    assert attn.bwd_workspace_size(2, 16, 16, 4096, 4096, 128, 0) == 2 * 16 * 4096 * 4
+    assert L.attn_bwd_sinks_workspace_size(2, 16, 0, 4096, 4096, 128, 4) == 2 * 16 * 4096 * 4
+    assert L.attn_bwd_sinks_workspace_size(0, 16, 16, 4096, 4096, 128, 4) == 0
+    # more first keys than keys; at most 64 parts
+    assert attn.bwd_workspace_size(1, 8, 1, 1 << 16, 130, 64, 10 ** 6) == 8 * (1 << 16) * 4 + 64 * 2 * 2 * 128 * 64 * 4
+    need = attn.bwd_workspace_size(1, 2, 2, 16, 16, 128, 4)
+    assert call_bwd_sinks(L, wsb=need - 1) == INV
+
+
+def test_sinks_beside_documents_are_refused(L):
+    q, lse = stand_in(1, 16, 2, 64), stand_in(1, 2, 16, dtype=torch.float32)
+    docs = stand_in(2, dtype=torch.int32)
+    with pytest.raises(attn.AttnError) as e:
+        attn.attn_fwd(q, q, q, q, lse, scale=0.1, causal=True, window=(4, 0), doc_offsets=docs, sinks=2, stream=0)
+    assert e.value.status == attn.ATTN_ERR_UNSUPPORTED
+    dq = stand_in(1, 16, 2, 64, dtype=torch.float32)
+    with pytest.raises(attn.AttnError):
+        attn.attn_bwd(q, q, q, q, lse, q, dq, q, q, stand_in(1 << 20, dtype=torch.uint8), scale=0.1, window=(4, 0),
+                      doc_offsets=docs, sinks=2, stream=0)
+    with pytest.raises(TypeError):
+        attn.attn_fwd(q, stand_in(1, 16, 4, 64), q, q, lse, scale=0.1, window=(4, 0), sinks=2, stream=0)
+    with pytest.raises(attn.AttnError) as e:
+        attn.attn_fwd(q, q, q, q, lse, scale=0.1, window=(4, 0), sinks=-2, stream=0)
+    assert e.value.status == attn.ATTN_ERR_INVALID_ARG
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU path only")
+def test_valid_sinks_calls_without_gpu_report_cuda_error(L):
+    for sinks in (0, 4, 1000):
+        assert call_fwd_sinks(L, sinks=sinks) == attn.ATTN_ERR_CUDA
+        assert call_bwd_sinks(L, sinks=sinks) == attn.ATTN_ERR_CUDA

@@ -41,7 +41,8 @@ ATTN_KV_E4M3 = 1
 
 EXPORTED = ("attn_fwd", "attn_fwd_ex", "attn_fwd_fp8", "attn_fwd_default_options",
             "attn_fp4_default_options", "attn_fwd_fp4_workspace_size", "attn_fwd_fp4", "attn_bwd",
-            "attn_bwd_ex", "attn_bwd_workspace_size", "attn_bwd_noalloc", "attn_qk_norm_rope",
+            "attn_bwd_ex", "attn_fwd_sinks", "attn_bwd_sinks", "attn_bwd_sinks_workspace_size",
+            "attn_bwd_workspace_size", "attn_bwd_noalloc", "attn_qk_norm_rope",
             "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_size",
             "attn_qk_norm_rope_cache", "attn_decode_paged", "attn_decode_paged_workspace_size",
             "attn_get_device_status",
@@ -130,6 +131,16 @@ def lib():
             L.attn_bwd_ex.restype = ctypes.c_int
             L.attn_bwd_ex.argtypes = L.attn_bwd.argtypes[:-1] + [ctypes.POINTER(BwdOptions),
                                                                  ctypes.c_void_p]
+            L.attn_fwd_sinks.restype = ctypes.c_int
+            L.attn_fwd_sinks.argtypes = _FWD_ARGS[:-2] + [ctypes.c_int, ctypes.POINTER(FwdOptions),
+                                                          ctypes.c_void_p]
+            L.attn_bwd_sinks_workspace_size.restype = ctypes.c_size_t
+            L.attn_bwd_sinks_workspace_size.argtypes = [ctypes.c_int] * 7
+            L.attn_bwd_sinks.restype = ctypes.c_int
+            L.attn_bwd_sinks.argtypes = [ctypes.c_void_p] * 9 + [ctypes.c_int] * 6 + \
+                [ctypes.c_float] + [ctypes.c_int] * 4 + [ctypes.c_void_p, ctypes.c_size_t,
+                                                         ctypes.POINTER(BwdOptions),
+                                                         ctypes.c_void_p]
             L.attn_bwd_noalloc.restype = ctypes.c_int
             L.attn_bwd_noalloc.argtypes = [ctypes.c_void_p] * 9 + [ctypes.c_int] * 6 + \
                 [ctypes.c_float] + [ctypes.c_int] * 3 + [ctypes.c_void_p, ctypes.c_int,
@@ -196,15 +207,22 @@ def _slopes(alibi_slopes, Hq, device, stream):
     return alibi_slopes
 
 
+def _check_sinks(sinks, doc_offsets):
+    if sinks and doc_offsets is not None:
+        raise AttnError(ATTN_ERR_UNSUPPORTED, "sinks: not built beside a document mask")
+
+
 def attn_fwd(q, k, v, o, lse, *, scale, causal=False, window=None, doc_offsets=None,
-             options=None, stream=None, softcap=None, alibi_slopes=None):
+             options=None, stream=None, softcap=None, alibi_slopes=None, sinks=0):
     """Enqueue the forward on `stream` (default: torch's current stream).
 
     q, o: bf16 CUDA [B,Sq,Hq,D]; k, v: bf16 CUDA [B,Sk,Hkv,D]; lse: fp32 CUDA
     [B,Hq,Sq]; doc_offsets: int32 CUDA [num_docs+1] or None.  All contiguous.
     softcap (> 0) and alibi_slopes (fp32 [Hq]) select the score modifiers;
-    they override the same fields of `options`.
+    they override the same fields of `options`.  With `sinks` the first keys
+    stay visible beside the window (no document mask then).
     """
+    _check_sinks(sinks, doc_offsets)
     for name, t, dt in (("q", q, torch.bfloat16), ("k", k, torch.bfloat16),
                         ("v", v, torch.bfloat16), ("o", o, torch.bfloat16),
                         ("lse", lse, torch.float32)):
@@ -232,7 +250,15 @@ def attn_fwd(q, k, v, o, lse, *, scale, causal=False, window=None, doc_offsets=N
             options.softcap = float(softcap)
         if slopes is not None:
             options.alibi_slopes = slopes.data_ptr()
-    if options is None:
+    if sinks:
+        for name, t, shape in (("k", k, (B, Sk, Hkv, D)), ("v", v, (B, Sk, Hkv, D)),
+                               ("o", o, (B, Sq, Hq, D)), ("lse", lse, (B, Hq, Sq))):
+            if tuple(t.shape) != shape:
+                raise TypeError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        st = L.attn_fwd_sinks(*args[:-2], int(sinks),
+                              None if options is None else ctypes.byref(options),
+                              _stream_handle(stream))
+    elif options is None:
         st = L.attn_fwd(*args, _stream_handle(stream))
     else:
         st = L.attn_fwd_ex(*args, ctypes.byref(options), _stream_handle(stream))
@@ -240,7 +266,7 @@ def attn_fwd(q, k, v, o, lse, *, scale, causal=False, window=None, doc_offsets=N
 
 
 def attention(q, k, v, *, scale=None, causal=False, window=None, doc_offsets=None,
-              options=None, stream=None, softcap=None, alibi_slopes=None):
+              options=None, stream=None, softcap=None, alibi_slopes=None, sinks=0):
     """Allocate O and LSE with torch and run the forward.  Returns (O, LSE)."""
     B, Sq, Hq, D = q.shape
     if scale is None:
@@ -253,7 +279,7 @@ def attention(q, k, v, *, scale=None, causal=False, window=None, doc_offsets=Non
         doc_offsets = doc_offsets.to(q.device)
     attn_fwd(q, k, v, o, lse, scale=scale, causal=causal, window=window,
              doc_offsets=doc_offsets, options=options, stream=stream, softcap=softcap,
-             alibi_slopes=alibi_slopes)
+             alibi_slopes=alibi_slopes, sinks=sinks)
     return o, lse
 
 
@@ -423,17 +449,20 @@ def _docs_arg(doc_offsets):
     return _ptr(doc_offsets), doc_offsets.numel() - 1
 
 
-def bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D) -> int:
+def bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D, sinks=0) -> int:
     """Bytes of device workspace attn_bwd needs."""
+    if sinks:
+        return int(lib().attn_bwd_sinks_workspace_size(B, Hq, Hkv, Sq, Sk, D, sinks))
     return int(lib().attn_bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D))
 
 
 def attn_bwd(q, k, v, o, lse, dout, dq, dk, dv, workspace, *, scale, causal=False, window=None,
-             doc_offsets=None, stream=None, softcap=None, alibi_slopes=None):
+             doc_offsets=None, stream=None, softcap=None, alibi_slopes=None, sinks=0):
     """Enqueue the backward on `stream`.  dq fp32 [B,Sq,Hq,D]; dk, dv bf16
     [B,Sk,Hkv,D]; workspace a CUDA uint8 tensor of at least
-    bwd_workspace_size() bytes.  softcap / alibi_slopes must match the
+    bwd_workspace_size() bytes.  softcap / alibi_slopes / sinks must match the
     forward that produced o and lse."""
+    _check_sinks(sinks, doc_offsets)
     _check_bwd_tensors(q, k, v, o, lse, dout, dq, dk, dv)
     if not torch.is_tensor(workspace) or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
@@ -445,18 +474,23 @@ def attn_bwd(q, k, v, o, lse, dout, dq, dk, dv, workspace, *, scale, causal=Fals
             _ptr(dv), B, Hq, Hkv, Sq, Sk, D, float(scale), int(bool(causal)), wl, wr,
             docs_ptr, nd, _ptr(workspace), workspace.numel() * workspace.element_size()]
     slopes = _slopes(alibi_slopes, Hq, q.device, stream)
-    if softcap is None and slopes is None:
+    if softcap is None and slopes is None and not sinks:
         st = lib().attn_bwd(*args, _stream_handle(stream))
     else:
         opts = BwdOptions()
         opts.softcap = float(softcap or 0.0)
         opts.alibi_slopes = None if slopes is None else slopes.data_ptr()
+        if sinks:
+            args[-4:-2] = [int(sinks)]  # in the place of the document mask
+            st = lib().attn_bwd_sinks(*args, ctypes.byref(opts), _stream_handle(stream))
+            _check(st, "attn_bwd_sinks")
+            return
         st = lib().attn_bwd_ex(*args, ctypes.byref(opts), _stream_handle(stream))
     _check(st, "attn_bwd")
 
 
 def attention_backward(q, k, v, o, lse, dout, *, scale=None, causal=False, window=None,
-                       doc_offsets=None, stream=None, softcap=None, alibi_slopes=None):
+                       doc_offsets=None, stream=None, softcap=None, alibi_slopes=None, sinks=0):
     """Allocate dQ (fp32), dK, dV (bf16) and the workspace with torch and run
     the backward.  Returns (dQ, dK, dV)."""
     B, Sq, Hq, D = q.shape
@@ -466,14 +500,16 @@ def attention_backward(q, k, v, o, lse, dout, *, scale=None, causal=False, windo
     dq = torch.empty(q.shape, dtype=torch.float32, device=q.device)
     dk = torch.empty_like(k)
     dv = torch.empty_like(v)
-    ws = torch.empty(bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D), dtype=torch.uint8,
-                     device=q.device)
+    ws = torch.empty(bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D, max(sinks, 0)),
+                     dtype=torch.uint8, device=q.device)
     if doc_offsets is not None and not torch.is_tensor(doc_offsets):
         doc_offsets = torch.as_tensor(doc_offsets, dtype=torch.int32)
     if doc_offsets is not None and not doc_offsets.is_cuda:
         doc_offsets = doc_offsets.to(q.device)
     attn_bwd(q, k, v, o, lse, dout, dq, dk, dv, ws, scale=scale, causal=causal, window=window,
-             doc_offsets=doc_offsets, stream=stream, softcap=softcap, alibi_slopes=alibi_slopes)
+             doc_offsets=doc_offsets, stream=stream, softcap=softcap, alibi_slopes=alibi_slopes,
+             sinks=sinks)
+    _keep_for(stream, dq, dk, dv, ws)
     return dq, dk, dv
 
 

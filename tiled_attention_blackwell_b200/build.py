@@ -22,9 +22,10 @@ LIB = os.path.join(PKG, "libattn.so")
 COUNT_LIB = os.path.join(PKG, "libattn_count.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
-# attn_api.cu: the forward and backward; serve_api.cu: head norms with
-# rotation, the paged cache and its decode.
-UNITS = ("attn_api.cu", "serve_api.cu")
+# attn_api.cu: the forward and backward; sinks.cu: their variants with first
+# keys beside a window; serve_api.cu: head norms with rotation, the paged cache
+# and its decode.
+UNITS = ("attn_api.cu", "sinks.cu", "serve_api.cu")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

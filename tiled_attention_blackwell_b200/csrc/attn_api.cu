@@ -13,22 +13,16 @@
 #include <type_traits>
 
 #include "../../include/attn.h"
-#include "bwd_kernel.cuh"
 #include "fp4_dequant.cuh"
 #include "fwd_fp4_kernel.cuh"
-#include "fwd_kernel.cuh"
-#include "fwd_persistent.cuh"
 #include "host_common.h"
+#include "launch.cuh"
 
 using tab_host::aligned16;
 using tab_host::device_state;
 using tab_host::DeviceState;
 using tab_host::encode_fn;
 using tab_host::EncodeTiledFn;
-using tab_host::fail;
-using tab_host::kMaxDevices;
-using tab_host::ok;
-
 namespace {
 
 thread_local char g_detail[512] = "";
@@ -160,47 +154,6 @@ attn_status_t make_map_fp4(CUtensorMap *map, const void *base, long long inner, 
 
 // --------------------------------------------------------------- launching
 
-// PERSIST selects the persistent kernel (fwd_persistent.cuh: one CTA per SM
-// running many items), otherwise one CTA per item.
-template <int D, int NS, int EXP, int MOD = 0, int PREC = 0, bool PERSIST = false>
-attn_status_t launch_fwd(const tab::FwdParams &p, int grid, cudaStream_t stream) {
-    using Smem = std::conditional_t<PERSIST, tab::FwdSmemPersistent<D, NS, PREC == 1 ? 1 : 2>,
-                                    tab::FwdSmem<D, NS, PREC == 1 ? 1 : 2>>;
-    constexpr size_t smem = sizeof(Smem) + 1024;
-    static_assert(smem <= 232448, "shared memory budget");
-    auto kernel = []() {
-        if constexpr (PERSIST) return tab::attn_fwd_persistent_kernel<D, NS, EXP, MOD, PREC>;
-        else return tab::attn_fwd_kernel<D, NS, EXP, MOD, PREC>;
-    }();
-    static std::once_flag once[kMaxDevices];
-    static cudaError_t attr_err[kMaxDevices];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    std::call_once(once[dev], [&]() {
-        attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
-    });
-    if (attr_err[dev] != cudaSuccess)
-        return fail(ATTN_ERR_LAUNCH, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err[dev]));
-    // The kernel moves registers between warpgroups with setmaxnreg; if the
-    // compiled per-thread count does not cover the split, the increase would
-    // wait forever, so never launch such a build.
-    static cudaFuncAttributes attrs[kMaxDevices];
-    static cudaError_t attrs_err[kMaxDevices];
-    static std::once_flag attrs_once[kMaxDevices];
-    std::call_once(attrs_once[dev], [&]() { attrs_err[dev] = cudaFuncGetAttributes(&attrs[dev], kernel); });
-    if (attrs_err[dev] != cudaSuccess)
-        return fail(ATTN_ERR_LAUNCH, "cudaFuncGetAttributes: %s", cudaGetErrorString(attrs_err[dev]));
-    if (attrs[dev].numRegs < tab::kLaunchRegs)
-        return fail(ATTN_ERR_LAUNCH, "kernel compiled with %d registers per thread, %d needed",
-                    attrs[dev].numRegs, tab::kLaunchRegs);
-    kernel<<<grid, tab::kFwdThreads, smem, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
-    return ok();
-}
-
-constexpr int kStagesD128 = 4;
 // Key/value heads whose query heads' CTAs are scheduled together: 8 heads of
 // K/V at S = 8192, D = 128 are 32 MiB, well inside the 126 MiB L2.
 // Measured on B200 (causal S=8192, outlier S=4096, GQA document S=16384):
@@ -220,25 +173,7 @@ int fwd_schedule_group(int B, int Hq, int Hkv, int ctas) {
     g = (g + qpk - 1) / qpk * qpk;
     return std::min(B * Hq, g);
 }
-constexpr int kStagesD64 = 8;
 constexpr int kStagesFp8 = 8;  // fp8 K/V tiles are 16 KB at D = 128
-
-template <int D, int NS>
-attn_status_t dispatch_exp(const tab::FwdParams &p, int grid, int exp_mode, int mod,
-                           cudaStream_t s) {
-    // With a score modifier the exponentials all run on MUFU.
-    switch (mod) {
-        case 1: return launch_fwd<D, NS, 0, 1>(p, grid, s);
-        case 2: return launch_fwd<D, NS, 0, 2>(p, grid, s);
-        case 3: return launch_fwd<D, NS, 0, 3>(p, grid, s);
-        default: break;
-    }
-    switch (exp_mode) {
-        case 0: return launch_fwd<D, NS, 0>(p, grid, s);
-        case 1: return launch_fwd<D, NS, 1>(p, grid, s);
-        default: return launch_fwd<D, NS, 2>(p, grid, s);
-    }
-}
 
 // The fp8 forward runs persistent (measured 6 % faster than one CTA per item
 // at causal S=8192; for bf16 operands the persistent kernel is slower).
@@ -338,66 +273,6 @@ attn_status_t check_common(int B, int Hq, int Hkv, int Sq, int Sk, int D, float 
     return ATTN_OK;
 }
 
-template <class Kernel>
-attn_status_t prepare_kernel(Kernel kernel, size_t smem, int threads, int min_regs) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e != cudaSuccess)
-        return fail(ATTN_ERR_LAUNCH, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    cudaFuncAttributes attrs;
-    e = cudaFuncGetAttributes(&attrs, kernel);
-    if (e != cudaSuccess)
-        return fail(ATTN_ERR_LAUNCH, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
-    if (attrs.numRegs < min_regs || attrs.maxThreadsPerBlock < threads)
-        return fail(ATTN_ERR_LAUNCH, "kernel build cannot be launched (%d regs, %d threads)",
-                    attrs.numRegs, attrs.maxThreadsPerBlock);
-    return ATTN_OK;
-}
-
-constexpr int kBwdStagesQ = 2;
-// dQ kernel: K and V ring depths (224 KB of SMEM with Q and dO at D = 128).
-constexpr int bwd_k_stages(int D) { return D == 128 ? 3 : 6; }
-constexpr int bwd_v_stages(int D) { return D == 128 ? 2 : 4; }
-
-template <int D, int MOD>
-attn_status_t launch_bwd(const tab::BwdParams &p, cudaStream_t stream) {
-    using DkdvS = tab::DkdvSmem<D, kBwdStagesQ>;
-    using DqS = tab::DqSmem<D, bwd_k_stages(D), bwd_v_stages(D)>;
-    constexpr size_t smem_dkdv = sizeof(DkdvS) + 1024;
-    constexpr size_t smem_dq = sizeof(DqS) + 1024;
-    static_assert(smem_dkdv <= 232448 && smem_dq <= 232448, "shared memory budget");
-    auto k_dkdv = tab::attn_bwd_dkdv_kernel<D, kBwdStagesQ, MOD>;
-    auto k_dq = tab::attn_bwd_dq_kernel<D, bwd_k_stages(D), bwd_v_stages(D), MOD>;
-    static std::once_flag once[kMaxDevices];
-    static attn_status_t prep[kMaxDevices];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    std::call_once(once[dev], [&]() {
-        prep[dev] = prepare_kernel(k_dkdv, smem_dkdv, tab::kBwdThreads, 0);
-        if (prep[dev] == ATTN_OK) prep[dev] = prepare_kernel(k_dq, smem_dq, tab::kBwdThreads, 0);
-    });
-    if (prep[dev] != ATTN_OK) return fail(prep[dev], "backward kernels could not be prepared");
-    // dQ first: it also computes D_i into the workspace, which the dK/dV
-    // kernel reads.
-    k_dq<<<p.num_qb * p.Hq * p.B, tab::kBwdThreads, smem_dq, stream>>>(p);
-    k_dkdv<<<p.num_kb * p.Hkv * p.B, tab::kBwdThreads, smem_dkdv, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
-    return ok();
-}
-
-template <int D>
-attn_status_t dispatch_bwd(const tab::BwdParams &p, int mod, cudaStream_t stream) {
-    switch (mod) {
-        case 1: return launch_bwd<D, 1>(p, stream);
-        case 2: return launch_bwd<D, 2>(p, stream);
-        case 3: return launch_bwd<D, 3>(p, stream);
-        default: return launch_bwd<D, 0>(p, stream);
-    }
-}
-
 // Shared checks of the score-modifier fields of both option structs.
 attn_status_t check_modifiers(float softcap, int reserved0, const float *alibi_slopes,
                               const int *reserved, int n_reserved) {
@@ -471,7 +346,8 @@ static attn_status_t fwd_impl(const void *q, const void *k, const void *v, void 
                        int Hq, int Hkv, int Sq, int Sk, int D, float scale, int causal,
                        int window_left, int window_right, const int *doc_offsets,
                        int num_docs, const attn_fwd_options_t *opts, bool fp8,
-                       float q_descale, float k_descale, float v_descale, void *stream) {
+                       float q_descale, float k_descale, float v_descale, void *stream,
+                       int sinks = 0) {
     attn_fwd_options_t op;
     attn_fwd_default_options(&op);
     if (opts) op = *opts;
@@ -571,6 +447,11 @@ static attn_status_t fwd_impl(const void *q, const void *k, const void *v, void 
 #endif
 
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    // First keys matter only beside a window's lower end.
+    if (sinks > 0 && window_left >= 0) {
+        p.sinks = std::min(sinks, Sk);
+        return tab_host::dispatch_fwd_sinks(p, grid, D, op.exp2_mode, mod, cs);
+    }
     if (fp8) return dispatch_fp8(p, grid, op.exp2_mode, cs);
     if (D == 128) return dispatch_exp<128, kStagesD128>(p, grid, op.exp2_mode, mod, cs);
     return dispatch_exp<64, kStagesD64>(p, grid, op.exp2_mode, mod, cs);
@@ -583,6 +464,15 @@ attn_status_t attn_fwd_ex(const void *q, const void *k, const void *v, void *o, 
                           const attn_fwd_options_t *opts, void *stream) {
     return fwd_impl(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, scale, causal, window_left,
                     window_right, doc_offsets, num_docs, opts, false, 1.0f, 1.0f, 1.0f, stream);
+}
+
+attn_status_t attn_fwd_sinks(const void *q, const void *k, const void *v, void *o, float *lse,
+                             int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
+                             int causal, int window_left, int window_right, int sinks,
+                             const attn_fwd_options_t *opts, void *stream) {
+    if (sinks < 0) return fail(ATTN_ERR_INVALID_ARG, "sinks must be >= 0");
+    return fwd_impl(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, scale, causal, window_left,
+                    window_right, nullptr, 0, opts, false, 1.0f, 1.0f, 1.0f, stream, sinks);
 }
 
 attn_status_t attn_fwd_fp8(const void *q, const void *k, const void *v, float q_descale,
@@ -803,13 +693,26 @@ attn_status_t attn_bwd(const void *q, const void *k, const void *v, const void *
                        workspace_bytes, nullptr, stream);
 }
 
-attn_status_t attn_bwd_ex(const void *q, const void *k, const void *v, const void *o,
+// Parts that the query blocks of a key block with first keys are cut into
+// (attn_bwd_sinks): about kSinkPartItems of them each, what a key block under
+// a window of 1024 keys has.  At most kSinkMaxParts, which bounds the
+// workspace.
+constexpr int kSinkPartItems = 8;
+constexpr int kSinkMaxParts = 64;
+static int sink_parts(int Hq, int Hkv, int Sq) {
+    const long long items = (Sq + 127LL) / 128 * (Hq / Hkv);
+    return (int)std::min<long long>(kSinkMaxParts, (items + kSinkPartItems - 1) / kSinkPartItems);
+}
+
+// The backward of both entry points; sinks > 0 with window_left >= 0 selects
+// the kernels whose rows see first keys beside their window.
+static attn_status_t bwd_impl(const void *q, const void *k, const void *v, const void *o,
                           const float *lse, const void *dout, float *dq, void *dk, void *dv,
                           int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
                           int causal, int window_left, int window_right,
                           const int *doc_offsets, int num_docs, void *workspace,
                           size_t workspace_bytes, const attn_bwd_options_t *opts,
-                          void *stream) {
+                          void *stream, int sinks) {
     attn_status_t s = check_bwd_args(q, k, v, o, lse, dout, dq, dk, dv, B, Hq, Hkv, Sq, Sk, D,
                                      scale, window_left, window_right, doc_offsets, num_docs);
     if (s != ATTN_OK) return s;
@@ -820,10 +723,14 @@ attn_status_t attn_bwd_ex(const void *q, const void *k, const void *v, const voi
         return s;
     if (!workspace) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(workspace)) return fail(ATTN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
-    const size_t need = attn_bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D);
+    const size_t need = attn_bwd_sinks_workspace_size(B, Hq, Hkv, Sq, Sk, D, sinks);
     if (workspace_bytes < need)
         return fail(ATTN_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     const long long num_qb = (Sq + 127LL) / 128, num_kb = (Sk + 127LL) / 128;
+    const bool with_sinks = sinks > 0 && window_left >= 0;
+    const long long sink_blocks = with_sinks ? (std::min(sinks, Sk) + 127LL) / 128 : 0;
+    if (with_sinks && (num_kb + sink_blocks * (kSinkMaxParts - 1)) * Hkv * B > 0x7fffffffLL)
+        return fail(ATTN_ERR_UNSUPPORTED, "grid too large");
 
     DeviceState *st = nullptr;
     if ((s = device_state(&st)) != ATTN_OK) return s;
@@ -867,7 +774,46 @@ attn_status_t attn_bwd_ex(const void *q, const void *k, const void *v, const voi
     p.trace_ctas = g_trace_ctas;
 #endif
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (with_sinks) {
+        p.sinks = std::min(sinks, Sk);
+        p.sink_blocks = (int)sink_blocks;
+        p.sink_parts = sink_parts(Hq, Hkv, Sq);
+        p.sink_sums = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
+                                                attn_bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D));
+        return tab_host::dispatch_bwd_sinks(p, D, mod, cs);
+    }
     return D == 128 ? dispatch_bwd<128>(p, mod, cs) : dispatch_bwd<64>(p, mod, cs);
+}
+
+size_t attn_bwd_sinks_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int D, int sinks) {
+    const size_t rows = attn_bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D);
+    if (rows == 0 || Hkv < 1 || Sk < 1 || D < 1 || sinks < 1) return rows;
+    const size_t blocks = (std::min(sinks, Sk) + (size_t)127) / 128;
+    return rows + (size_t)sink_parts(Hq, Hkv, Sq) * blocks * B * Hkv * 2 * 128 * D * sizeof(float);
+}
+
+attn_status_t attn_bwd_ex(const void *q, const void *k, const void *v, const void *o,
+                          const float *lse, const void *dout, float *dq, void *dk, void *dv,
+                          int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
+                          int causal, int window_left, int window_right,
+                          const int *doc_offsets, int num_docs, void *workspace,
+                          size_t workspace_bytes, const attn_bwd_options_t *opts,
+                          void *stream) {
+    return bwd_impl(q, k, v, o, lse, dout, dq, dk, dv, B, Hq, Hkv, Sq, Sk, D, scale, causal,
+                    window_left, window_right, doc_offsets, num_docs, workspace, workspace_bytes,
+                    opts, stream, 0);
+}
+
+attn_status_t attn_bwd_sinks(const void *q, const void *k, const void *v, const void *o,
+                             const float *lse, const void *dout, float *dq, void *dk, void *dv,
+                             int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
+                             int causal, int window_left, int window_right, int sinks,
+                             void *workspace, size_t workspace_bytes,
+                             const attn_bwd_options_t *opts, void *stream) {
+    if (sinks < 0) return fail(ATTN_ERR_INVALID_ARG, "sinks must be >= 0");
+    return bwd_impl(q, k, v, o, lse, dout, dq, dk, dv, B, Hq, Hkv, Sq, Sk, D, scale, causal,
+                    window_left, window_right, nullptr, 0, workspace, workspace_bytes, opts,
+                    stream, sinks);
 }
 
 attn_status_t attn_bwd_noalloc(const void *q, const void *k, const void *v, const void *o,

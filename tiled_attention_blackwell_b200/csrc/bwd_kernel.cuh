@@ -92,6 +92,11 @@ struct BwdParams {
     float softcap_in;   // scale / cap
     float softcap_out;  // cap * log2(e)
     const float *alibi_slopes;
+    // SINKS kernels: first keys that stay visible beside the window, the key
+    // blocks that hold them, the parts that their query blocks are cut into,
+    // and the parts' sums (fp32 [part][block][B * Hkv][dK, dV][128][D]).
+    int sinks, sink_blocks, sink_parts;
+    float *sink_sums;
 };
 
 // Modified scores of a pair in log2 units (MOD bit 0 soft-cap, bit 1 ALiBi
@@ -154,7 +159,12 @@ struct DkdvSmem {
     int qb_lo, qb_hi;
 };
 
-template <int D, int NSQ, int MOD = 0>
+// SINKS: key blocks without a first key see what they see without SINKS; one
+// with first keys is seen by (nearly) every query block behind it, many times
+// a window's worth.  Its items are cut into sink_parts parts of a block
+// each, which come first in the grid and leave fp32 sums;
+// attn_bwd_sink_sum_kernel adds those in order.
+template <int D, int NSQ, int MOD = 0, bool SINKS = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
     using Smem = DkdvSmem<D, NSQ>;
@@ -167,8 +177,19 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
     // Work item: lowest key blocks first (under a causal mask they see the
     // most query blocks), then (batch, kv head).
     const int bh_count = p.Hkv * p.B;
-    const int kb = (int)(blockIdx.x / bh_count);
+    int kb = (int)(blockIdx.x / bh_count);
     const int bh = (int)(blockIdx.x % bh_count);
+    // SINKS: part `part` of block kb's items, or (part < 0) all of them.
+    int part = -1;
+    if constexpr (SINKS) {
+        const int sink_rows = p.sink_blocks * p.sink_parts;
+        if (kb < sink_rows) {
+            part = kb / p.sink_blocks;
+            kb -= part * p.sink_blocks;
+        } else {
+            kb += p.sink_blocks - sink_rows;
+        }
+    }
     const int hkv = bh % p.Hkv;
     const int b = bh / p.Hkv;
     const int k0 = kb * 128;
@@ -202,7 +223,7 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
             const int r1 = min(r0 + 127, p.Sq - 1);
             KeyRange a = row_key_range(p, r0);
             KeyRange z = row_key_range(p, r1);
-            const int a_lo = a.lo <= a.hi ? a.lo : -1;
+            const int a_lo = a.lo <= a.hi && !(SINKS && part >= 0) ? a.lo : -1;
             const int z_hi = z.lo <= z.hi ? z.hi : -1;
             if (a_lo <= k1 && z_hi >= k0) {
                 lo = min(lo, qb);
@@ -230,7 +251,15 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
     volatile int *abort_flag = &sm.abort_flag;
     const int qb_lo = sm.qb_lo, qb_hi = sm.qb_hi;
     const int n_qb = qb_hi >= qb_lo ? qb_hi - qb_lo + 1 : 0;
-    const int n_items = n_qb * p.group;  // (query head in group, query block)
+    const int all_items = n_qb * p.group;  // (query head in group, query block)
+    int it0 = 0, n_items = all_items;      // this block's: [it0, it0 + n_items)
+    if constexpr (SINKS) {
+        if (part >= 0) {
+            const int per = (all_items + p.sink_parts - 1) / p.sink_parts;
+            it0 = min(part * per, all_items);
+            n_items = min(per, all_items - it0);
+        }
+    }
     // TMEM columns: S^T [0,128), dP^T [128,256), dV [256,256+D), dK [256+D,256+2D)
     constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 256, kColDK = 256 + D;
 
@@ -256,8 +285,8 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
         int nlo[4], nhi[4];
         bool nfull = true;
         auto prefetch = [&](int it) {
-            const int g = it / n_qb;
-            const int qb = qb_lo + it % n_qb;
+            const int g = (it0 + it) / n_qb;
+            const int qb = qb_lo + (it0 + it) % n_qb;
             const size_t rb = ((size_t)b * p.Hq + hkv * p.group + g) * p.Sq;
             nfull = true;
 #pragma unroll
@@ -268,16 +297,17 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
                 nd[m] = ld_nc_f32(p.dval + ri);
                 const KeyRange kr = r < p.Sq ? row_key_range(p, r) : KeyRange{1, 0};
                 nlo[m] = kr.lo;
-                nhi[m] = kr.hi;
-                nfull = nfull && r < p.Sq && kr.lo <= k0 && kr.hi >= k1;
+                nhi[m] = SINKS && kr.lo > kr.hi ? -1 : kr.hi;  // no key, so no first key either
+                nfull = nfull && r < p.Sq && kr.hi >= k1 &&
+                        (kr.lo <= k0 || (SINKS && part >= 0 && k1 < p.sinks && kr.lo <= kr.hi));
             }
             nfull = __all_sync(0xffffffffu, nfull);
         };
         if (n_items > 0) prefetch(0);
         for (int it = 0; it < n_items && ok; ++it) {
             const int s = it % NSQ;
-            const int g = it / n_qb;
-            const int qb = qb_lo + it % n_qb;
+            const int g = (it0 + it) / n_qb;
+            const int qb = qb_lo + (it0 + it) % n_qb;
             const int hq = hkv * p.group + g;
             float cl[4], cd[4];
             int clo[4], chi[4];
@@ -423,6 +453,7 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
     } else {
         // ---------------------------------------------------- elementwise
         const int key = k0 + (warp & 3) * 32 + lane;
+        const bool first_key = SINKS && part >= 0 && key < p.sinks;  // lower ends do not count
         const int h = warp >> 2;  // this warpgroup's half of the columns
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_col = tmem + lane_base + kColS + h * 64;
@@ -449,8 +480,8 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
             if (MOD) {
                 // Modified scores: P from the transformed score; pv keeps
                 // P * d(modified)/d(scaled) for dS, pk the plain P for dV.
-                const int qb = qb_lo + it % n_qb;
-                const int hq = hkv * p.group + it / n_qb;
+                const int qb = qb_lo + (it0 + it) % n_qb;
+                const int hq = hkv * p.group + (it0 + it) / n_qb;
                 const float slope2 = (MOD & 2) ? __ldg(p.alibi_slopes + hq) * kLog2e : 0.0f;
                 const float dist0 = (float)(qb * 128 + h * 64 + p.Sk - p.Sq - key);
                 const int *rlo = sm.rlo[s] + h * 64;
@@ -465,8 +496,8 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
                                            dist0 + (float)(e + 1));
                     add2(x0, x1, x0, x1, -l2[e], -l2[e + 1]);
                     const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
-                    const float pr0 = (full || (rlo[e] <= key && key <= rhi[e])) ? p0 : 0.0f;
-                    const float pr1 = (full || (rlo[e + 1] <= key && key <= rhi[e + 1])) ? p1 : 0.0f;
+                    const float pr0 = (full || ((rlo[e] <= key || (SINKS && first_key)) && key <= rhi[e])) ? p0 : 0.0f;
+                    const float pr1 = (full || ((rlo[e + 1] <= key || (SINKS && first_key)) && key <= rhi[e + 1])) ? p1 : 0.0f;
                     mul2(pv[e], pv[e + 1], pr0, pr1, f0, f1);
                     pk[e >> 1] = pack_bf16x2(pr0, pr1);
                 }
@@ -490,10 +521,10 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
                     const float4 l = l4[e >> 2];
                     const int4 lo = lo4[e >> 2];
                     const int4 hi = hi4[e >> 2];
-                    pv[e + 0] = (lo.x <= key && key <= hi.x) ? ex2_mufu(fmaf(pv[e + 0], c, -l.x)) : 0.0f;
-                    pv[e + 1] = (lo.y <= key && key <= hi.y) ? ex2_mufu(fmaf(pv[e + 1], c, -l.y)) : 0.0f;
-                    pv[e + 2] = (lo.z <= key && key <= hi.z) ? ex2_mufu(fmaf(pv[e + 2], c, -l.z)) : 0.0f;
-                    pv[e + 3] = (lo.w <= key && key <= hi.w) ? ex2_mufu(fmaf(pv[e + 3], c, -l.w)) : 0.0f;
+                    pv[e + 0] = ((lo.x <= key || (SINKS && first_key)) && key <= hi.x) ? ex2_mufu(fmaf(pv[e + 0], c, -l.x)) : 0.0f;
+                    pv[e + 1] = ((lo.y <= key || (SINKS && first_key)) && key <= hi.y) ? ex2_mufu(fmaf(pv[e + 1], c, -l.y)) : 0.0f;
+                    pv[e + 2] = ((lo.z <= key || (SINKS && first_key)) && key <= hi.z) ? ex2_mufu(fmaf(pv[e + 2], c, -l.z)) : 0.0f;
+                    pv[e + 3] = ((lo.w <= key || (SINKS && first_key)) && key <= hi.w) ? ex2_mufu(fmaf(pv[e + 3], c, -l.w)) : 0.0f;
                     pk[(e >> 1) + 0] = pack_bf16x2(pv[e + 0], pv[e + 1]);
                     pk[(e >> 1) + 1] = pack_bf16x2(pv[e + 2], pv[e + 3]);
                 }
@@ -559,6 +590,19 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) r[e] = 0u;
                     }
+                    if constexpr (SINKS) {
+                        if (part >= 0) {  // fp32 sums of this part, unscaled; every row
+                            float4 *dst = reinterpret_cast<float4 *>(
+                                p.sink_sums +
+                                ((((size_t)part * p.sink_blocks + kb) * bh_count + bh) * 2 + which) * 128 * D +
+                                (size_t)(key - k0) * D + h * (D / 2) + ch * 32);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                dst[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
+                                                     __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
+                            continue;
+                        }
+                    }
                     uint4 out[4];
                     uint32_t *w = reinterpret_cast<uint32_t *>(out);
 #pragma unroll
@@ -580,6 +624,37 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
     if (warp == kBwdMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+}
+
+// dK and dV of the key blocks with first keys: the parts' sums, in order.
+// One thread per four values.
+template <int D>
+__global__ void __launch_bounds__(256)
+attn_bwd_sink_sum_kernel(const __grid_constant__ BwdParams p) {
+    const int bh_count = p.Hkv * p.B;
+    const size_t n = (size_t)p.sink_blocks * bh_count * 2 * 128 * (D / 4);
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
+        const int d = (int)(i % (D / 4)) * 4;
+        size_t r = i / (D / 4);
+        const int row = (int)(r % 128);
+        r /= 128;
+        const int which = (int)(r % 2);
+        r /= 2;
+        const int bh = (int)(r % bh_count), kb = (int)(r / bh_count);
+        const int key = kb * 128 + row;
+        if (key >= p.Sk) continue;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int part = 0; part < p.sink_parts; ++part) {
+            const float4 v = *reinterpret_cast<const float4 *>(p.sink_sums + ((size_t)part * n + i) * 4);
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        const float mul = which == 0 ? p.scale : 1.0f;
+        __nv_bfloat16 *dst = (which == 0 ? p.dk : p.dv) +
+                             (((size_t)(bh / p.Hkv) * p.Sk + key) * p.Hkv + bh % p.Hkv) * (size_t)D + d;
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(pack_bf16x2(sum.x * mul, sum.y * mul), pack_bf16x2(sum.z * mul, sum.w * mul));
     }
 }
 
@@ -606,7 +681,7 @@ struct DqSmem {
     float dpart[2][128];  // D_i of each row, per half of the columns
 };
 
-template <int D, int NK, int NV, int MOD = 0>
+template <int D, int NK, int NV, int MOD = 0, bool SINKS = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_bwd_dq_kernel(const __grid_constant__ BwdParams p) {
     using Smem = DqSmem<D, NK, NV>;
@@ -662,7 +737,10 @@ attn_bwd_dq_kernel(const __grid_constant__ BwdParams p) {
     const uint32_t tmem = sm.tmem_base;
     volatile int *abort_flag = &sm.abort_flag;
     const int lo_b = sm.range[0], hi_b = sm.range[1];
-    const int n_blocks = hi_b >= lo_b ? hi_b - lo_b + 1 : 0;
+    // SINKS: the blocks of the first keys before the window come first.
+    const int s_b = SINKS ? min((p.sinks + 127) / 128, lo_b) : 0;
+    const int n_blocks = hi_b >= lo_b ? s_b + hi_b - lo_b + 1 : 0;
+    auto block_of = [&](int t) -> int { return SINKS && t < s_b ? t : lo_b - s_b + t; };
     // TMEM columns: S of even blocks [0,128), dP [128,256), dQ [256,256+D), S of
     // odd blocks [384,512).  dS (bf16 pairs) goes over its block's S.  The
     // second S buffer lets S and dP of the next block run on the tensor
@@ -681,7 +759,7 @@ attn_bwd_dq_kernel(const __grid_constant__ BwdParams p) {
             int nk = 0, nv = 0;  // K and V copies issued
             bool ok = true;
             for (int t = 0; t < n_blocks && ok; ++t) {
-                const int key0 = (lo_b + t) * 128;
+                const int key0 = block_of(t) * 128;
                 ok = wait_bounded(&sm.k_empty[t % NK], ((uint32_t)(t / NK) & 1u) ^ 1u,
                                   abort_flag, p.status);
                 if (!ok) break;
@@ -800,7 +878,8 @@ attn_bwd_dq_kernel(const __grid_constant__ BwdParams p) {
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t dp_col = tmem + lane_base + kColDP + h * 64;
         const bool row_ok = row < p.Sq;
-        const KeyRange kr = row_ok ? row_key_range(p, row) : KeyRange{1, 0};
+        KeyRange kr = row_ok ? row_key_range(p, row) : KeyRange{1, 0};
+        if (SINKS && kr.lo > kr.hi) kr.hi = -1;  // no key, so no first key either
         const size_t ri = ((size_t)b * p.Hq + hq) * p.Sq + (row_ok ? row : 0);
         const float l2 = row_ok ? __ldg(p.lse + ri) * kLog2e : INFINITY;
         // D_i = sum_d dO_id O_id of this row: each warpgroup over its half of
@@ -834,7 +913,7 @@ attn_bwd_dq_kernel(const __grid_constant__ BwdParams p) {
         const float slope2 = (MOD & 2) ? __ldg(p.alibi_slopes + hq) * kLog2e : 0.0f;
         bool ok = true;
         for (int t = 0; t < n_blocks; ++t) {
-            const int j = lo_b + t;
+            const int j = block_of(t);
             ok = __all_sync(0xffffffffu, wait_bounded(&sm.s_full, (uint32_t)t & 1u, abort_flag,
                                                       p.status));
             if (!ok) break;
@@ -854,7 +933,11 @@ attn_bwd_dq_kernel(const __grid_constant__ BwdParams p) {
             mbar_arrive(&sm.dp_free);  // dP of the next block may overwrite it now
             float *pv = reinterpret_cast<float *>(sr);
             const int key0 = j * 128 + h * 64;
-            const bool masked = __any_sync(0xffffffffu, key0 < kr.lo || key0 + 63 > kr.hi);
+            const bool masked = __any_sync(
+                0xffffffffu, (key0 < kr.lo && (!SINKS || key0 + 64 > p.sinks)) || key0 + 63 > kr.hi);
+            auto sees = [&](int key) -> bool {
+                return (key >= kr.lo || (SINKS && key < p.sinks)) && key <= kr.hi;
+            };
             if (MOD) {
                 // pv becomes P * d(modified)/d(scaled), all dS needs.
                 const float dist0 = (float)(row + p.Sk - p.Sq - key0);
@@ -869,14 +952,14 @@ attn_bwd_dq_kernel(const __grid_constant__ BwdParams p) {
                     float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
                     mul2(p0, p1, p0, p1, f0, f1);
                     const int key = key0 + e;
-                    pv[e] = (!masked || (key >= kr.lo && key <= kr.hi)) ? p0 : 0.0f;
-                    pv[e + 1] = (!masked || (key + 1 >= kr.lo && key + 1 <= kr.hi)) ? p1 : 0.0f;
+                    pv[e] = (!masked || sees(key)) ? p0 : 0.0f;
+                    pv[e + 1] = (!masked || sees(key + 1)) ? p1 : 0.0f;
                 }
             } else if (masked) {
 #pragma unroll
                 for (int e = 0; e < 64; ++e) {
                     const int key = key0 + e;
-                    pv[e] = (key >= kr.lo && key <= kr.hi) ? ex2_mufu(fmaf(pv[e], c, -l2)) : 0.0f;
+                    pv[e] = sees(key) ? ex2_mufu(fmaf(pv[e], c, -l2)) : 0.0f;
                 }
             } else {
 #pragma unroll

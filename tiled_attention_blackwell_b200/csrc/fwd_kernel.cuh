@@ -114,6 +114,7 @@ struct FwdParams {
     // V per 128-key block; two 512-byte atoms each) and the tile counts.
     const uint8_t *sf_q, *sf_k, *sf_v;
     int nq_tiles, nk_tiles;
+    int sinks;  // SINKS kernels: first keys that stay visible beside the window
 };
 
 // Opt-in event trace (compile with -DATTN_TRACE): lane 0 of warps 0 and 4
@@ -344,10 +345,16 @@ __device__ __forceinline__ void modify_scores(float *v, float c, float k1, float
     }
 }
 
-template <int D, int NS, int EXP_MODE, int MOD = 0, int PREC = 0>
+// SINKS: beside its interval (window, causal) a row sees keys j < sinks up to
+// the interval's upper end.  The blocks of a tile are then those of the first
+// keys and those of its window, at most two runs: the kernel walks the union
+// of both tiles' blocks under "virtual" indices in which the window's blocks
+// keep their own and the sb first blocks stand directly before them.
+template <int D, int NS, int EXP_MODE, int MOD = 0, int PREC = 0, bool SINKS = false>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 attn_fwd_kernel(const __grid_constant__ FwdParams p) {
     static_assert(!(PREC && MOD), "the low-precision paths have no score modifiers");
+    static_assert(!(PREC && SINKS), "first keys beside a window: bf16 operands only");
     constexpr bool FP8 = PREC == 1;
     constexpr bool DP = PREC >= 2;  // Direct-P
     constexpr int EB = FP8 ? 1 : 2;
@@ -447,9 +454,14 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
     const int lo0 = sm.range[0][0], hi0 = sm.range[0][1];
     const int lo1 = sm.range[1][0], hi1 = sm.range[1][1];
     const bool has0 = lo0 <= hi0, has1 = lo1 <= hi1;
-    const int ulo = has0 ? (has1 ? min(lo0, lo1) : lo0) : lo1;
+    const int wlo = has0 ? (has1 ? min(lo0, lo1) : lo0) : lo1;
     const int uhi = has0 ? (has1 ? max(hi0, hi1) : hi0) : hi1;
+    // Blocks with first keys; those before both tiles' windows come first.
+    const int nsb = SINKS ? (p.sinks + kBlockN - 1) / kBlockN : 0;
+    const int ulo = SINKS ? wlo - min(nsb, wlo) : wlo;
     const int n_blocks = (has0 || has1) ? (uhi - ulo + 1) : 0;
+    // Key block of virtual index j.
+    auto block_of = [&](int j) -> int { return !SINKS || j >= wlo ? j : j - ulo; };
 
     // Registers: the softmax warpgroups hold a 128-column score row per
     // thread; the MMA / TMA warpgroup needs few.  384 x 168 at launch =
@@ -464,7 +476,7 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                 uint32_t it = 0;
                 bool ok = true;
                 for (int t = 0; t < n_blocks && ok; ++t) {
-                    const int key0 = (ulo + t) * kBlockN;
+                    const int key0 = block_of(ulo + t) * kBlockN;
                     for (int which = 0; which < 2 && ok; ++which, ++it) {
                         const uint32_t slot = it % NS;
                         ok = wait_bounded(&sm.kv_empty[slot], ((it / NS) & 1u) ^ 1u, abort_flag,
@@ -549,6 +561,11 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                     __syncwarp();
                 };
                 auto active = [&](int i, int j) -> bool {
+                    if constexpr (SINKS) {
+                        const int kb = block_of(j);
+                        return i == 0 ? (has0 && (kb >= lo0 || kb < nsb) && kb <= hi0)
+                                      : (has1 && (kb >= lo1 || kb < nsb) && kb <= hi1);
+                    }
                     return i == 0 ? (has0 && j >= lo0 && j <= hi0)
                                   : (has1 && j >= lo1 && j <= hi1);
                 };
@@ -573,10 +590,16 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                         if (active(i, j)) {
                             const int lo_i = i == 0 ? lo0 : lo1;
                             const int hi_i = i == 0 ? hi0 : hi1;
-                            const uint32_t par = (uint32_t)(j - lo_i) & 1u;
+                            // Blocks of this tile before this one.
+                            int nth = j - lo_i;
+                            if constexpr (SINKS) {
+                                const int kb = block_of(j), s_i = min(nsb, lo_i);
+                                nth = kb < s_i ? kb : kb - lo_i + s_i;
+                            }
+                            const uint32_t par = (uint32_t)nth & 1u;
                             const uint32_t o_tmem = tmem + 2 * kBlockN + i * D;
                             const uint32_t p_tmem = tmem + i * kBlockN;
-                            const uint32_t first = j > lo_i ? 1u : 0u;
+                            const uint32_t first = nth > 0 ? 1u : 0u;
                             // PV in two halves of 64 keys, each as soon as its P is in TMEM.
                             // V chunk: key rows of 128 bytes, 8-row groups 1024 B apart
                             // (SBO), 64-column chunks kChunkBytes apart (LBO).
@@ -638,9 +661,11 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_tmem = tmem + lane_base + i * kBlockN;
         const uint32_t o_tmem = tmem + lane_base + 2 * kBlockN + i * D;
-        const KeyRange kr = row_key_range(p, row);
+        KeyRange kr = row_key_range(p, row);
+        if (SINKS && kr.lo > kr.hi) kr.hi = -1;  // no key, so no first key either
         const int lo_b = i == 0 ? lo0 : lo1;
         const int hi_b = i == 0 ? hi0 : hi1;
+        const int s_b = SINKS && lo_b <= hi_b ? min(nsb, lo_b) : 0;  // blocks of first keys before the window
         const float c = p.scale_log2;
         const float tau = p.rescale_threshold;
         // With a modifier the scores are transformed into log2 units before
@@ -657,8 +682,9 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
         float l_pv = 0.0f;    // row sum of the p that PV consumes (the output's normaliser)
         bool ok = true;
 
-        for (int j = lo_b; j <= hi_b; ++j) {
-            const int t = j - lo_b;
+        for (int jj = lo_b - s_b; jj <= hi_b; ++jj) {
+            const int t = jj - (lo_b - s_b);
+            const int j = !SINKS || jj >= lo_b ? jj : t;
             if ((warp & 3) == 0) ATTN_TRACE_EVENT(i, t, 0);
             ok = wait_bounded(&sm.s_full[i], (uint32_t)t & 1u, abort_flag, p.status, true, p.timeout_ns);
             ok = __all_sync(0xffffffffu, ok);
@@ -683,7 +709,8 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
 
             const int key0 = j * kBlockN;
             const float dist0 = diag_f - (float)key0;  // distance to key0 of this block
-            const bool need_mask = key0 < kr.lo || key0 + kBlockN - 1 > kr.hi;
+            const bool need_mask = (key0 < kr.lo && (!SINKS || key0 + kBlockN > p.sinks)) ||
+                                   key0 + kBlockN - 1 > kr.hi;
             const bool masked = __any_sync(0xffffffffu, need_mask);
             float alpha = 1.0f;
             float neg_m;
@@ -716,7 +743,7 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
 #pragma unroll
                 for (int e = 0; e < kBlockN / 2; ++e) {
                     const int key = key0 + e;
-                    if (key < kr.lo || key > kr.hi) s[e] = -INFINITY;
+                    if ((key < kr.lo && (!SINKS || key >= p.sinks)) || key > kr.hi) s[e] = -INFINITY;
                 }
             }
             float mx[4];
@@ -735,7 +762,7 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
 #pragma unroll
                 for (int e = kBlockN / 2; e < kBlockN; ++e) {
                     const int key = key0 + e;
-                    if (key < kr.lo || key > kr.hi) s[e] = -INFINITY;
+                    if ((key < kr.lo && (!SINKS || key >= p.sinks)) || key > kr.hi) s[e] = -INFINITY;
                 }
             }
 #pragma unroll

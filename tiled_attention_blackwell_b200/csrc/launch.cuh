@@ -1,0 +1,157 @@
+// Launching of the forward and backward kernels, shared by the translation
+// units that hold their variants.
+#pragma once
+
+#include <algorithm>
+
+#include "bwd_kernel.cuh"
+#include "fwd_kernel.cuh"
+#include "fwd_persistent.cuh"
+#include "host_common.h"
+
+namespace tab_host {
+
+// sinks.cu: SINKS variants of the forward (one CTA per item) and the backward.
+attn_status_t dispatch_fwd_sinks(const tab::FwdParams &p, int grid, int D, int exp_mode, int mod,
+                                 cudaStream_t stream);
+attn_status_t dispatch_bwd_sinks(const tab::BwdParams &p, int D, int mod, cudaStream_t stream);
+
+}  // namespace tab_host
+
+namespace {
+
+using tab_host::fail;
+using tab_host::kMaxDevices;
+using tab_host::ok;
+
+// PERSIST selects the persistent kernel (fwd_persistent.cuh: one CTA per SM
+// running many items), otherwise one CTA per item.
+template <int D, int NS, int EXP, int MOD = 0, int PREC = 0, bool PERSIST = false,
+          bool SINKS = false>
+attn_status_t launch_fwd(const tab::FwdParams &p, int grid, cudaStream_t stream) {
+    using Smem = std::conditional_t<PERSIST, tab::FwdSmemPersistent<D, NS, PREC == 1 ? 1 : 2>,
+                                    tab::FwdSmem<D, NS, PREC == 1 ? 1 : 2>>;
+    constexpr size_t smem = sizeof(Smem) + 1024;
+    static_assert(smem <= 232448, "shared memory budget");
+    auto kernel = []() {
+        if constexpr (PERSIST) return tab::attn_fwd_persistent_kernel<D, NS, EXP, MOD, PREC>;
+        else return tab::attn_fwd_kernel<D, NS, EXP, MOD, PREC, SINKS>;
+    }();
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t attr_err[kMaxDevices];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::call_once(once[dev], [&]() {
+        attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)smem);
+    });
+    if (attr_err[dev] != cudaSuccess)
+        return fail(ATTN_ERR_LAUNCH, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err[dev]));
+    // The kernel moves registers between warpgroups with setmaxnreg; if the
+    // compiled per-thread count does not cover the split, the increase would
+    // wait forever, so never launch such a build.
+    static cudaFuncAttributes attrs[kMaxDevices];
+    static cudaError_t attrs_err[kMaxDevices];
+    static std::once_flag attrs_once[kMaxDevices];
+    std::call_once(attrs_once[dev], [&]() { attrs_err[dev] = cudaFuncGetAttributes(&attrs[dev], kernel); });
+    if (attrs_err[dev] != cudaSuccess)
+        return fail(ATTN_ERR_LAUNCH, "cudaFuncGetAttributes: %s", cudaGetErrorString(attrs_err[dev]));
+    if (attrs[dev].numRegs < tab::kLaunchRegs)
+        return fail(ATTN_ERR_LAUNCH, "kernel compiled with %d registers per thread, %d needed",
+                    attrs[dev].numRegs, tab::kLaunchRegs);
+    kernel<<<grid, tab::kFwdThreads, smem, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+constexpr int kStagesD128 = 4;
+constexpr int kStagesD64 = 8;
+
+template <int D, int NS, bool SINKS = false>
+attn_status_t dispatch_exp(const tab::FwdParams &p, int grid, int exp_mode, int mod,
+                           cudaStream_t s) {
+    // With a score modifier the exponentials all run on MUFU.
+    switch (mod) {
+        case 1: return launch_fwd<D, NS, 0, 1, 0, false, SINKS>(p, grid, s);
+        case 2: return launch_fwd<D, NS, 0, 2, 0, false, SINKS>(p, grid, s);
+        case 3: return launch_fwd<D, NS, 0, 3, 0, false, SINKS>(p, grid, s);
+        default: break;
+    }
+    switch (exp_mode) {
+        case 0: return launch_fwd<D, NS, 0, 0, 0, false, SINKS>(p, grid, s);
+        case 1: return launch_fwd<D, NS, 1, 0, 0, false, SINKS>(p, grid, s);
+        default: return launch_fwd<D, NS, 2, 0, 0, false, SINKS>(p, grid, s);
+    }
+}
+
+template <class Kernel>
+attn_status_t prepare_kernel(Kernel kernel, size_t smem, int threads, int min_regs) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e != cudaSuccess)
+        return fail(ATTN_ERR_LAUNCH, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    cudaFuncAttributes attrs;
+    e = cudaFuncGetAttributes(&attrs, kernel);
+    if (e != cudaSuccess)
+        return fail(ATTN_ERR_LAUNCH, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
+    if (attrs.numRegs < min_regs || attrs.maxThreadsPerBlock < threads)
+        return fail(ATTN_ERR_LAUNCH, "kernel build cannot be launched (%d regs, %d threads)",
+                    attrs.numRegs, attrs.maxThreadsPerBlock);
+    return ATTN_OK;
+}
+
+constexpr int kBwdStagesQ = 2;
+// dQ kernel: K and V ring depths (224 KB of SMEM with Q and dO at D = 128).
+constexpr int bwd_k_stages(int D) { return D == 128 ? 3 : 6; }
+constexpr int bwd_v_stages(int D) { return D == 128 ? 2 : 4; }
+
+template <int D, int MOD, bool SINKS>
+attn_status_t launch_bwd(const tab::BwdParams &p, cudaStream_t stream) {
+    using DkdvS = tab::DkdvSmem<D, kBwdStagesQ>;
+    using DqS = tab::DqSmem<D, bwd_k_stages(D), bwd_v_stages(D)>;
+    constexpr size_t smem_dkdv = sizeof(DkdvS) + 1024;
+    constexpr size_t smem_dq = sizeof(DqS) + 1024;
+    static_assert(smem_dkdv <= 232448 && smem_dq <= 232448, "shared memory budget");
+    auto k_dkdv = tab::attn_bwd_dkdv_kernel<D, kBwdStagesQ, MOD, SINKS>;
+    auto k_dq = tab::attn_bwd_dq_kernel<D, bwd_k_stages(D), bwd_v_stages(D), MOD, SINKS>;
+    static std::once_flag once[kMaxDevices];
+    static attn_status_t prep[kMaxDevices];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::call_once(once[dev], [&]() {
+        prep[dev] = prepare_kernel(k_dkdv, smem_dkdv, tab::kBwdThreads, 0);
+        if (prep[dev] == ATTN_OK) prep[dev] = prepare_kernel(k_dq, smem_dq, tab::kBwdThreads, 0);
+    });
+    if (prep[dev] != ATTN_OK) return fail(prep[dev], "backward kernels could not be prepared");
+    // dQ first: it also computes D_i into the workspace, which the dK/dV
+    // kernel reads.
+    k_dq<<<p.num_qb * p.Hq * p.B, tab::kBwdThreads, smem_dq, stream>>>(p);
+    if constexpr (SINKS) {
+        // Key blocks with first keys: sink_parts blocks each, and their sum.
+        const int rows = p.num_kb + p.sink_blocks * (p.sink_parts - 1);
+        k_dkdv<<<rows * p.Hkv * p.B, tab::kBwdThreads, smem_dkdv, stream>>>(p);
+        const long long n = (long long)p.sink_blocks * p.Hkv * p.B * 2 * 128 * (D / 4);
+        const int grid = (int)std::min<long long>((n + 255) / 256, 148 * 8);
+        tab::attn_bwd_sink_sum_kernel<D><<<grid, 256, 0, stream>>>(p);
+    } else {
+        k_dkdv<<<p.num_kb * p.Hkv * p.B, tab::kBwdThreads, smem_dkdv, stream>>>(p);
+    }
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+template <int D, bool SINKS = false>
+attn_status_t dispatch_bwd(const tab::BwdParams &p, int mod, cudaStream_t stream) {
+    switch (mod) {
+        case 1: return launch_bwd<D, 1, SINKS>(p, stream);
+        case 2: return launch_bwd<D, 2, SINKS>(p, stream);
+        case 3: return launch_bwd<D, 3, SINKS>(p, stream);
+        default: return launch_bwd<D, 0, SINKS>(p, stream);
+    }
+}
+
+}  // namespace
