@@ -6,7 +6,6 @@ There is no fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -184,7 +183,7 @@ def default_options(**overrides) -> FwdOptions:
 
 def _stream_handle(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -534,48 +533,62 @@ def attn_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, *, scale, causal=False, 
 
 
 # ----------------------------------------------- around the attention kernels
+#
+# These calls are short (a decoding step makes one of each per layer), so the
+# checks below take the cheap way to every fact: a call costs the host about
+# as long as its launches.
 
-def _same_device(tensors):
-    """The CUDA device of all (name, tensor) pairs; anything else raises."""
-    device = None
-    for name, t in tensors:
-        if not torch.is_tensor(t) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise TypeError(f"{name} is on {t.device}, the first tensor on {device}")
-    return device
+def _device_of(names, *tensors):
+    """Index of the CUDA device that all the tensors are on; else raises."""
+    index = None
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{names.split()[i]} must be a CUDA tensor")
+        if index is None:
+            index = t.get_device()
+        elif t.get_device() != index:
+            raise TypeError(f"{names.split()[i]} is on {t.device}, {names.split()[0]} on "
+                            f"{tensors[0].device}")
+    return index
 
 
-def _on_device(device):
-    """Makes `device` current for a call, if it is not."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _run(what, index, fn, args, stream, *allocated):
+    """fn(*args, stream) with device `index` current.  The tensors `allocated`
+    here come from the current stream's memory: where another stream uses
+    them, the allocator is told."""
+    if index >= 0 and index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _run(what, index, fn, args, stream, *allocated)
+    if stream is None:
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)), what)
+        return
+    _check(fn(*args, _stream_handle(stream)), what)
+    _keep_for(stream, *allocated)
 
 
 def _keep_for(stream, *tensors):
-    """Tells the allocator that work on `stream` uses tensors which were
-    allocated on the current stream."""
     if stream is not None and hasattr(stream, "cuda_stream") \
             and stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
         for t in tensors:
             t.record_stream(stream)
 
 
-def _token_stride(name, t, H, D, dtypes):
+_BF16 = (torch.bfloat16,)
+_BF16_FP32 = (torch.bfloat16, torch.float32)
+
+
+def _token_stride(name, t, H, D, dtypes=_BF16):
     """Distance, in values, of consecutive tokens of a [..., H, D] tensor
     whose heads are contiguous and whose tokens are evenly spaced."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    shape, strides = t.shape, t.stride()
-    if len(shape) < 3 or shape[-1] != D or shape[-2] != H:
-        raise TypeError(f"{name} must be [..., {H}, {D}], got {tuple(shape)}")
+    if t.is_contiguous():
+        return H * D
+    strides = t.stride()
     if strides[-1] != 1 or (H > 1 and strides[-2] != D):
         raise TypeError(f"{name}: the heads of a token must be contiguous")
     step, upto = None, None
-    for n, st in zip(reversed(shape[:-2]), reversed(strides[:-2])):
+    for n, st in zip(t.shape[-3::-1], strides[-3::-1]):
         if n == 1:
             continue
         if step is None:
@@ -589,24 +602,24 @@ def _token_stride(name, t, H, D, dtypes):
 def _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
     """Checked arguments that every form of the norm and rotation shares:
     (weights .. positions), (tokens .. interleaved)."""
-    if q.dim() < 3 or k.dim() != q.dim() or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
+    (*lead, Hq, D), (*lead_k, Hkv, Dk) = q.shape, k.shape
+    if not lead or lead != lead_k or D != Dk:
         raise TypeError(f"q and k must be [..., H, D] of the same tokens, got {tuple(q.shape)} "
                         f"and {tuple(k.shape)}")
-    D = q.shape[-1]
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w.dtype not in (torch.bfloat16, torch.float32) or w.dtype != q_weight.dtype \
-                or tuple(w.shape) != (D,) or not w.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous bf16 or fp32 tensor of shape ({D},), "
-                            "both weights of one type")
-    for name, t in (("cos", cos), ("sin", sin)):
-        if t.dtype != torch.float32 or t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous fp32 tensor [max_positions, rot / 2]")
-    if positions.dtype != torch.int32 or positions.shape != q.shape[:-2] or not positions.is_contiguous():
-        raise TypeError(f"positions must be a contiguous int32 tensor of shape {tuple(q.shape[:-2])}")
-    return ((q_weight.data_ptr(), k_weight.data_ptr(), int(q_weight.dtype == torch.float32),
+    dtype, one = q_weight.dtype, (D,)
+    if dtype not in _BF16_FP32 or k_weight.dtype != dtype or q_weight.shape != one \
+            or k_weight.shape != one or not q_weight.is_contiguous() or not k_weight.is_contiguous():
+        raise TypeError(f"q_weight and k_weight must be contiguous bf16 or fp32 tensors of shape {one}, "
+                        "both of one type")
+    table = cos.shape
+    if cos.dtype != torch.float32 or sin.dtype != torch.float32 or len(table) != 2 \
+            or sin.shape != table or not cos.is_contiguous() or not sin.is_contiguous():
+        raise TypeError("cos and sin must be contiguous fp32 tensors [max_positions, rot / 2]")
+    if positions.dtype != torch.int32 or [*positions.shape] != lead or not positions.is_contiguous():
+        raise TypeError(f"positions must be a contiguous int32 tensor of shape {tuple(lead)}")
+    return ((q_weight.data_ptr(), k_weight.data_ptr(), dtype == torch.float32,
              cos.data_ptr(), sin.data_ptr(), positions.data_ptr()),
-            (positions.numel(), q.shape[-2], k.shape[-2], D, 2 * cos.shape[1], cos.shape[0],
-             float(eps), int(bool(interleaved))))
+            (positions.numel(), Hq, Hkv, D, 2 * table[1], table[0], eps, bool(interleaved)))
 
 
 def rope_table(max_positions, rot, *, theta=10000.0, device="cuda"):
@@ -630,23 +643,20 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6, int
     `interleaved`, in neighbouring pairs; positions int32 [...].  q_out and
     k_out are allocated unless given; they may be q and k themselves."""
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty_like(q)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    device = _same_device((("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight),
-                           ("cos", cos), ("sin", sin), ("positions", positions),
-                           ("q_out", q_out), ("k_out", k_out)))
+        k_out = torch.empty_like(k)
+    index = _device_of("q k q_weight k_weight cos sin positions q_out k_out", q, k, q_weight,
+                       k_weight, cos, sin, positions, q_out, k_out)
     norm, sizes = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     if q_out.shape != q.shape or k_out.shape != k.shape:
         raise TypeError("q_out and k_out must have the shapes of q and k")
-    D, bf16 = q.shape[-1], (torch.bfloat16,)
-    strides = [_token_stride(n, t, t.shape[-2], D, bf16)
-               for n, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))]
-    with _on_device(device):
-        _check(lib().attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(),
-                                       k_out.data_ptr(), *strides, *norm, *sizes,
-                                       _stream_handle(stream)), "attn_qk_norm_rope")
-        _keep_for(stream, q_out, k_out)
+    _, Hq, Hkv, D = sizes[:4]
+    _run("attn_qk_norm_rope", index, lib().attn_qk_norm_rope,
+         (q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+          _token_stride("q", q, Hq, D), _token_stride("k", k, Hkv, D),
+          _token_stride("q_out", q_out, Hq, D), _token_stride("k_out", k_out, Hkv, D),
+          *norm, *sizes), stream, q_out, k_out)
     return q_out, k_out
 
 
@@ -657,41 +667,40 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos, sin, positions,
     (dq_in, dk_in, dq_weight, dk_weight): bf16 like q and k (allocated unless
     given: views of a packed gradient are fine), fp32 [D]."""
     if dq_in is None:
-        dq_in = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dq_in = torch.empty_like(q)
     if dk_in is None:
-        dk_in = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    device = _same_device((("dq", dq), ("dk", dk), ("q", q), ("k", k), ("q_weight", q_weight),
-                           ("k_weight", k_weight), ("cos", cos), ("sin", sin),
-                           ("positions", positions), ("dq_in", dq_in), ("dk_in", dk_in)))
+        dk_in = torch.empty_like(k)
+    index = _device_of("dq dk q k q_weight k_weight cos sin positions dq_in dk_in", dq, dk, q, k,
+                       q_weight, k_weight, cos, sin, positions, dq_in, dk_in)
     norm, sizes = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     if dq.shape != q.shape or dk.shape != k.shape or dq_in.shape != q.shape or dk_in.shape != k.shape:
         raise TypeError("dq, dk, dq_in and dk_in must have the shapes of q and k")
-    D, bf16, either = q.shape[-1], (torch.bfloat16,), (torch.bfloat16, torch.float32)
-    strides = [_token_stride(n, t, t.shape[-2], D, types)
-               for n, t, types in (("dq", dq, either), ("dk", dk, either), ("q", q, bf16),
-                                   ("k", k, bf16), ("dq_in", dq_in, bf16), ("dk_in", dk_in, bf16))]
+    _, Hq, Hkv, D = sizes[:4]
+    strides = (_token_stride("dq", dq, Hq, D, _BF16_FP32), _token_stride("dk", dk, Hkv, D, _BF16_FP32),
+               _token_stride("q", q, Hq, D), _token_stride("k", k, Hkv, D),
+               _token_stride("dq_in", dq_in, Hq, D), _token_stride("dk_in", dk_in, Hkv, D))
     L = lib()
-    weights = torch.empty(2, D, dtype=torch.float32, device=device)
-    ws = torch.empty(L.attn_qk_norm_rope_bwd_workspace_size(D), dtype=torch.uint8, device=device)
-    with _on_device(device):
-        _check(L.attn_qk_norm_rope_bwd(dq.data_ptr(), dk.data_ptr(), int(dq.dtype == torch.float32),
-                                       int(dk.dtype == torch.float32), q.data_ptr(), k.data_ptr(),
-                                       dq_in.data_ptr(), dk_in.data_ptr(), weights.data_ptr(),
-                                       weights.data_ptr() + 4 * D, *strides, *norm, *sizes,
-                                       ws.data_ptr(), ws.numel(), _stream_handle(stream)),
-               "attn_qk_norm_rope_bwd")
-        _keep_for(stream, dq_in, dk_in, weights, ws)
-    return dq_in, dk_in, weights[0], weights[1]
+    dq_weight = torch.empty_like(q_weight, dtype=torch.float32)
+    dk_weight = torch.empty_like(k_weight, dtype=torch.float32)
+    size = L.attn_qk_norm_rope_bwd_workspace_size(D)
+    ws = torch.empty(size, dtype=torch.uint8, device=q.device)
+    _run("attn_qk_norm_rope_bwd", index, L.attn_qk_norm_rope_bwd,
+         (dq.data_ptr(), dk.data_ptr(), dq.dtype == torch.float32, dk.dtype == torch.float32,
+          q.data_ptr(), k.data_ptr(), dq_in.data_ptr(), dk_in.data_ptr(), dq_weight.data_ptr(),
+          dk_weight.data_ptr(), *strides, *norm, *sizes, ws.data_ptr(), size),
+         stream, dq_in, dk_in, dq_weight, dk_weight, ws)
+    return dq_in, dk_in, dq_weight, dk_weight
 
 
 def _cache_type(k_cache, v_cache):
     """ATTN_KV_* of a pair of caches [num_pages, page_size, Hkv, D]."""
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or t.dim() != 4 \
-                or t.shape != k_cache.shape or t.dtype != k_cache.dtype or not t.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous bf16 or float8_e4m3fn tensor "
-                            "[num_pages, page_size, Hkv, D], both caches alike")
-    return ATTN_KV_BF16 if k_cache.dtype == torch.bfloat16 else ATTN_KV_E4M3
+    dtype, shape = k_cache.dtype, k_cache.shape
+    if dtype not in (torch.bfloat16, torch.float8_e4m3fn) or len(shape) != 4 \
+            or v_cache.dtype != dtype or v_cache.shape != shape \
+            or not k_cache.is_contiguous() or not v_cache.is_contiguous():
+        raise TypeError("k_cache and v_cache must be contiguous bf16 or float8_e4m3fn tensors "
+                        "[num_pages, page_size, Hkv, D], both alike")
+    return ATTN_KV_BF16 if dtype == torch.bfloat16 else ATTN_KV_E4M3
 
 
 def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos, sin, positions, slots, k_cache, v_cache, *,
@@ -704,27 +713,21 @@ def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos, sin, positions, slots, 
     negative slot marks padding, of which nothing is read or written (its row
     of q_out keeps what it held)."""
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    device = _same_device((("q", q), ("k", k), ("v", v), ("q_weight", q_weight),
-                           ("k_weight", k_weight), ("cos", cos), ("sin", sin),
-                           ("positions", positions), ("slots", slots), ("k_cache", k_cache),
-                           ("v_cache", v_cache), ("q_out", q_out)))
+        q_out = torch.empty_like(q)
+    index = _device_of("q k v q_weight k_weight cos sin positions slots k_cache v_cache q_out", q, k,
+                       v, q_weight, k_weight, cos, sin, positions, slots, k_cache, v_cache, q_out)
     norm, sizes = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    kv = _cache_type(k_cache, v_cache)
-    if v.shape != k.shape or q_out.shape != q.shape or k_cache.shape[2:] != k.shape[-2:]:
+    kv, cache = _cache_type(k_cache, v_cache), k_cache.shape
+    if v.shape != k.shape or q_out.shape != q.shape or cache[2:] != k.shape[-2:]:
         raise TypeError("v must have k's shape, q_out q's, and the caches k's heads")
-    if slots.dtype != torch.int32 or slots.shape != q.shape[:-2] or not slots.is_contiguous():
-        raise TypeError(f"slots must be a contiguous int32 tensor of shape {tuple(q.shape[:-2])}")
-    D, bf16 = q.shape[-1], (torch.bfloat16,)
-    strides = [_token_stride(n, t, t.shape[-2], D, bf16)
-               for n, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out))]
-    with _on_device(device):
-        _check(lib().attn_qk_norm_rope_cache(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), *strides, *norm,
-            slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv, float(k_descale),
-            float(v_descale), k_cache.shape[0] * k_cache.shape[1], *sizes, _stream_handle(stream)),
-            "attn_qk_norm_rope_cache")
-        _keep_for(stream, q_out)
+    if slots.dtype != torch.int32 or slots.shape != positions.shape or not slots.is_contiguous():
+        raise TypeError(f"slots must be a contiguous int32 tensor of shape {tuple(positions.shape)}")
+    _, Hq, Hkv, D = sizes[:4]
+    _run("attn_qk_norm_rope_cache", index, lib().attn_qk_norm_rope_cache,
+         (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
+          _token_stride("q", q, Hq, D), _token_stride("k", k, Hkv, D), _token_stride("v", v, Hkv, D),
+          _token_stride("q_out", q_out, Hq, D), *norm, slots.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), kv, k_descale, v_descale, cache[0] * cache[1], *sizes), stream, q_out)
     return q_out
 
 
@@ -745,7 +748,8 @@ def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, scale=None, windo
     = (left, right) as in attention(): the last left + 1 keys stay visible, and
     with `sinks` the first ones too.  o, lse and workspace (uint8, at least
     decode_workspace_size(D)) are allocated unless given."""
-    if not torch.is_tensor(q) or q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.dtype != torch.bfloat16 \
+            or not q.is_contiguous():
         raise TypeError("q must be a contiguous bf16 tensor [B, Hq, D]")
     B, Hq, D = q.shape
     L = lib()
@@ -756,37 +760,37 @@ def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, scale=None, windo
     if workspace is None:
         workspace = torch.empty(L.attn_decode_paged_workspace_size(D), dtype=torch.uint8,
                                 device=q.device)
-    slopes = _slopes(alibi_slopes, Hq, q.device, stream)
-    device = _same_device((("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
-                           ("page_table", page_table), ("seq_lens", seq_lens), ("o", o),
-                           ("lse", lse), ("workspace", workspace))
-                          + ((("alibi_slopes", slopes),) if slopes is not None else ()))
+    index = _device_of("q k_cache v_cache page_table seq_lens o lse workspace", q, k_cache, v_cache,
+                       page_table, seq_lens, o, lse, workspace)
+    slopes = None
+    if alibi_slopes is not None:
+        slopes = _slopes(alibi_slopes, Hq, q.device, stream)
+        _device_of("q alibi_slopes", q, slopes)
     kv = _cache_type(k_cache, v_cache)
     num_pages, page_size, Hkv, Dk = k_cache.shape
     if Dk != D:
         raise TypeError(f"the caches' heads have {Dk} values, q's {D}")
-    for name, t, dt, shape in (("page_table", page_table, torch.int32, (B, page_table.shape[-1])),
-                               ("seq_lens", seq_lens, torch.int32, (B,)),
-                               ("o", o, torch.bfloat16, (B, Hq, D)),
-                               ("lse", lse, torch.float32, (B, Hq))):
-        if t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous {dt} tensor of shape {shape}")
+    table = page_table.shape
+    if page_table.dtype != torch.int32 or len(table) != 2 or table[0] != B \
+            or not page_table.is_contiguous():
+        raise TypeError(f"page_table must be a contiguous int32 tensor [{B}, max_pages]")
+    if seq_lens.dtype != torch.int32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
+        raise TypeError(f"seq_lens must be a contiguous int32 tensor of shape ({B},)")
+    if o.dtype != torch.bfloat16 or o.shape != q.shape or not o.is_contiguous():
+        raise TypeError("o must be a contiguous bf16 tensor of q's shape")
+    if lse.dtype != torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous():
+        raise TypeError(f"lse must be a contiguous fp32 tensor of shape ({B}, {Hq})")
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous uint8 tensor")
-    wl, wr = (-1, -1) if window is None else (int(window[0]), int(window[1]))
-    if wr < -1:
+    left, right = (-1, -1) if window is None else window
+    if right < -1:
         raise ValueError("window bounds must be -1 or >= 0")
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with _on_device(device):
-        _check(L.attn_decode_paged(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv, float(k_descale),
-            float(v_descale), page_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
-            lse.data_ptr(), B, Hq, Hkv, D, num_pages, page_size, page_table.shape[1],
-            float(scale), wl, int(sinks), float(softcap or 0.0),
-            None if slopes is None else slopes.data_ptr(), workspace.data_ptr(),
-            workspace.numel(), _stream_handle(stream)), "attn_decode_paged")
-        _keep_for(stream, o, lse, workspace)
+    _run("attn_decode_paged", index, L.attn_decode_paged,
+         (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv, k_descale, v_descale,
+          page_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, D,
+          num_pages, page_size, table[1], D ** -0.5 if scale is None else scale, int(left),
+          int(sinks), softcap or 0.0, None if slopes is None else slopes.data_ptr(),
+          workspace.data_ptr(), workspace.numel()), stream, o, lse, workspace)
     return o, lse
 
 

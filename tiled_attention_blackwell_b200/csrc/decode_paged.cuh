@@ -13,13 +13,19 @@
 // unnormalised output), which decode_join_kernel joins in the order of the
 // blocks, so the result does not depend on the timing.
 //
-// Warp roles: warps 0 .. kWarps-1 compute, warp kWarps copies.  The copying
-// warp walks the block's whole run ahead of the computing ones, across the
-// ends of pairs, so the copies never pause: 16 keys of K and of V are one
-// TMA box each (a page holds a multiple of 16 keys), in a ring of kStages
-// tiles.  Computing warp w takes every kWarps-th tile and keeps its own
-// running maximum, sums and output in registers; they are joined through
-// shared memory at the end of a pair.
+// A pair here is a sequence and kHeads neighbouring key heads, whose rows in
+// the cache are adjacent: kHeads * D * bytes is 256 where the heads allow it.
+// (Read head by head, a key's 128 or 64 bytes lie 1 KB and more apart, and
+// the copies run at 67 % and 41 % of the copy rate instead of 95 %.)
+//
+// Warp roles: warps 0-3 compute, warps 4 and 5 copy, two more are idle.  Warp
+// w works on head w % kHeads, as part of team w / kHeads; team t takes the
+// tiles g = t, t + kTeams, ... of the block's run and keeps the running
+// maximum, sums and output of its head in registers.  The teams' results are
+// joined through shared memory at the end of a pair.  The copying warps walk
+// the block's whole run ahead of the computing ones, across the ends of
+// pairs, so the copies never pause: 16 keys of K and of V are one TMA box
+// each (a page holds a multiple of 16 keys), in a ring of kStages tiles.
 //
 // Products: mma.sync m16n8k16 with up to 16 query heads of one key head as
 // rows.  (tcgen05 needs 64 rows or more; here the tensor pipe is idle most of
@@ -36,12 +42,20 @@
 namespace tab {
 
 constexpr int kDecWarps = 4;                         // computing warps
-constexpr int kDecThreads = (kDecWarps + 1) * 32;
+constexpr int kDecCopyWarps = 2;
+constexpr int kDecThreads = 2 * kDecWarps * 32;
 constexpr int kDecRows = 16;                         // query heads per pair
 constexpr int kDecBlock = 16;                        // keys per TMA box
+constexpr int kDecSlice = 32;                        // values of the output joined at a time
 constexpr int kDecCtasPerSm = 2;
-// Fewest tiles per block: one for each computing warp.
-constexpr int kDecMinTiles = kDecWarps;
+// Registers: 512 threads per SM launch with 128 each; setmaxnreg moves them
+// from the copying to the computing warpgroup of a block.  The split must not
+// exceed the launch allocation (a larger request would wait forever), and the
+// host checks the compiled count.
+constexpr int kDecLaunchRegs = 128;
+constexpr int kDecComputeRegs = 200;
+constexpr int kDecCopyRegs = 56;
+static_assert(kDecComputeRegs + kDecCopyRegs <= 2 * kDecLaunchRegs, "register split exceeds the launch allocation");
 // A row's maximum moves only when a tile raises it by more than this (log2
 // units), as in the forward; P stays below 2^8.
 constexpr float kDecTau = 8.0f;
@@ -56,10 +70,10 @@ struct DecodeParams {
     int *status;
     // Workspace: per block two partial results (a pair that begins before
     // the block, one that ends behind it) and one record.
-    float *part_o;           // [blocks][2][16][D], relative to the partial's maximum
-    float4 *part_ml;         // [blocks][2][16]: maximum (log2), sum, sum of the rounded weights
+    float *part_o;           // [blocks][2][kHeads][16][D], relative to the partial's maximum
+    float4 *part_ml;         // [blocks][2][kHeads][16]: maximum (log2), sum, sum of the rounded weights
     int4 *record;            // [blocks]: the pair that is first cut at this block's end
-    int B, Hq, Hkv, group, hchunks;
+    int B, Hq, Hkv, group, hchunks;  // hchunks: parts of 16 query heads of a key head
     int max_pages, page_size, num_pages;
     int window_left, sinks;
     float scale_log2;        // scale * k_descale * log2(e)
@@ -127,29 +141,36 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// A pair of weights in the operand type, and the sum of the rounded values.
+// A pair of weights in the operand type.  bf16: with the sum of the rounded
+// values, which normalises the output, as in the forward (a row that one key
+// dominates gives that key's V).  f16 weights are off by 2^-12 at most, which
+// the output's own rounding hides: the plain sum normalises them.
 template <bool F8>
 __device__ __forceinline__ uint32_t pack_weights(float p0, float p1, float &sum) {
     if constexpr (F8) {
-        const uint32_t h = pack_f16x2(p0, p1);
-        sum += f16x2_sum(h);
-        return h;
+        return pack_f16x2(p0, p1);
     } else {
         const uint32_t h = pack_bf16x2(p0, p1);
-        sum += __uint_as_float(h << 16) + __uint_as_float(h & 0xffff0000u);
+        float other = 0.0f;
+        add_bf16x2_f32(sum, other, h);
+        sum += other;
         return h;
     }
 }
 
-// kBlocks boxes of 16 keys per tile.
-template <int D, bool F8, int kBlocks, int kStages>
+// kBlocks boxes of 16 keys of kHeads heads per tile.
+template <int D, bool F8, int kHeads, int kBlocks, int kStages>
 struct DecodeSmem {
     static constexpr int kRowBytes = D * (F8 ? 1 : 2);
-    static constexpr int kBoxBytes = kDecBlock * kRowBytes;
+    static constexpr int kHeadBytes = kDecBlock * kRowBytes;  // one head's part of a box
+    static constexpr int kBoxBytes = kHeads * kHeadBytes;
+    static constexpr int kPitch = kRowBytes < 128 ? kRowBytes : 128;  // bytes per key in a chunk
+    static constexpr int kChunkBytes = kDecBlock * kPitch;            // 128 bytes of every key
     static constexpr int kTile = kDecBlock * kBlocks;
+    static constexpr int kTeams = kDecWarps / kHeads;
     uint8_t k[kStages][kBlocks][kBoxBytes];
     uint8_t v[kStages][kBlocks][kBoxBytes];
-    float o[kDecWarps][kDecRows][D + 4];  // + 4: rows start in different banks
+    float o[kDecWarps][kDecRows][kDecSlice + 4];  // + 4: rows start in different banks
     float4 ml[kDecWarps][kDecRows];
     uint64_t full[kStages], empty[kStages];
     long long start, end, share, base;    // this block's run; tiles before sequence b0
@@ -157,34 +178,37 @@ struct DecodeSmem {
     int abort_flag;
 };
 
-// Shared-memory byte of 16-byte piece `c` of key row `r` of a box: rows of
-// 128 bytes with the 128-byte swizzle (one chunk of the box per 128 bytes of
-// the row), or of 64 bytes with the 64-byte swizzle.
+// Byte of 16-byte piece `c` of key `r` in a box's first chunk: 128 bytes per
+// key with the 128-byte swizzle, or 64 with the 64-byte swizzle.  The next 128
+// bytes of the keys are the next chunk, laid out the same.
 template <int kRowBytes>
 __device__ __forceinline__ uint32_t box_offset(int r, int c) {
     if constexpr (kRowBytes >= 128)
-        return (uint32_t)((c >> 3) * (kDecBlock * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+        return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
     else
         return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-template <int D, bool F8, int kBlocks, int kStages>
+template <int D, bool F8, int kHeads, int kBlocks, int kStages>
 __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
 decode_paged_kernel(const __grid_constant__ DecodeParams p) {
-    using Smem = DecodeSmem<D, F8, kBlocks, kStages>;
-    constexpr int kTile = Smem::kTile;
+    using Smem = DecodeSmem<D, F8, kHeads, kBlocks, kStages>;
+    constexpr int kTile = Smem::kTile, kTeams = Smem::kTeams;
     constexpr int kPieces = Smem::kRowBytes / 16;  // 16-byte pieces of a row
+    // Tile g goes to slot g % kStages, which is one team's and one copying
+    // warp's alone: no wait can be two phases behind its slot.
+    static_assert(kStages % kTeams == 0 && kStages % kDecCopyWarps == 0, "slots belong to fixed warps");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_off = smem_u32(smem_raw);
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (raw_off & 1023u)) & 1023u));
     const int warp = warp_id(), lane = lane_id();
-    const int H = p.Hkv * p.hchunks;  // pairs per sequence
+    const int H = p.Hkv / kHeads * p.hchunks;  // pairs per sequence
     volatile int *abort_flag = &sm.abort_flag;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.empty[s], 1);
+            mbar_init(&sm.full[s], 2 * kBlocks);  // one arrival per box, copied or not
+            mbar_init(&sm.empty[s], kHeads);
         }
         sm.abort_flag = 0;
         fence_mbar_init();
@@ -199,7 +223,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
         for (int b = lane; b < p.B; b += 32) total += (long long)seq_tiles<kTile>(p, b).n * H;
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         const long long share =
-            max((long long)kDecMinTiles, (total + gridDim.x - 1) / (long long)gridDim.x);
+            max((long long)kTeams, (total + gridDim.x - 1) / (long long)gridDim.x);
         const long long start = min(total, share * blockIdx.x);
         const long long end = min(total, start + share);
         long long base = 0;
@@ -231,19 +255,24 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
     __syncthreads();
     const long long start = sm.start, end = sm.end;
 
-    if (warp == kDecWarps) {
+    if (warp >= kDecWarps) {
         // ------------------------------------------------------------ copies
+        setmaxnreg_dec<kDecCopyRegs>();
         const uint32_t n_tiles = (uint32_t)(end - start);
-        // Each lane looks up one tile of the next 32: its pair and its pages.
+        // This warp's tiles are w, w + kDecCopyWarps, ...; each lane looks up one of
+        // the next 32 of them: its pair and its pages.
+        const uint32_t w = warp - kDecWarps;
+        if (w >= kDecCopyWarps) return;
+        const uint32_t n_mine = n_tiles > w ? (n_tiles - w - 1) / kDecCopyWarps + 1 : 0;
         long long base = sm.base;
         int b = sm.b0;
         struct Item {
-            int page[kBlocks], row[kBlocks], hkv, blocks;
+            int page[kBlocks], row[kBlocks], head, blocks;
         };
-        auto look_up = [&](uint32_t g) {
+        auto look_up = [&](uint32_t i) {
             Item it{};
-            if (g >= n_tiles) return it;
-            const long long pos = start + g;
+            if (i >= n_mine) return it;
+            const long long pos = start + w + (long long)i * kDecCopyWarps;
             SeqTiles st = seq_tiles<kTile>(p, b);
             while (b + 1 < p.B && pos >= base + (long long)st.n * H) {
                 base += (long long)st.n * H;
@@ -253,7 +282,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
             const uint32_t pair = in_seq / (uint32_t)st.n;
             const int t = (int)(in_seq - pair * (uint32_t)st.n);
             const int key0 = (t < st.ns ? t : st.w0 + t - st.ns) * kTile;
-            it.hkv = (int)(pair / (uint32_t)p.hchunks);
+            it.head = (int)(pair / (uint32_t)p.hchunks) * kHeads;
 #pragma unroll
             for (int u = 0; u < kBlocks; ++u) {
                 const int key = key0 + u * kDecBlock;
@@ -271,44 +300,56 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
             }
             return it;
         };
+        // Lane 2 u + v copies box u of K (v = 0) or V (v = 1).
+        const int my_u = lane >> 1;
+        const bool my_v = lane & 1;
         bool ok = true;
         uint32_t issued = 0;
         Item next = look_up(lane);
-        for (uint32_t g0 = 0; g0 < n_tiles && ok; g0 += 32) {
+        for (uint32_t i0 = 0; i0 < n_mine && ok; i0 += 32) {
             const Item it = next;
-            next = look_up(g0 + 32 + lane);
-            const uint32_t n = min(32u, n_tiles - g0);
-            for (uint32_t i = 0; i < n && ok; ++i) {
-                const int hkv = __shfl_sync(0xffffffffu, it.hkv, i);
+            next = look_up(i0 + 32 + lane);
+            const uint32_t n = min(32u, n_mine - i0);
+            for (uint32_t i = 0; i < n; ++i) {
+                const int head = __shfl_sync(0xffffffffu, it.head, i);
                 const int blocks = __shfl_sync(0xffffffffu, it.blocks, i);
-                int page[kBlocks], row[kBlocks];
+                int page = 0, row = 0;
 #pragma unroll
                 for (int u = 0; u < kBlocks; ++u) {
-                    page[u] = __shfl_sync(0xffffffffu, it.page[u], i);
-                    row[u] = __shfl_sync(0xffffffffu, it.row[u], i);
+                    const int pg = __shfl_sync(0xffffffffu, it.page[u], i);
+                    const int rw = __shfl_sync(0xffffffffu, it.row[u], i);
+                    if (my_u == u) page = pg, row = rw;
                 }
-                const uint32_t s = issued % kStages;
-                ok = __all_sync(0xffffffffu, wait_bounded(&sm.empty[s], ((issued / kStages) & 1u) ^ 1u,
+                const uint32_t g = w + issued * kDecCopyWarps;
+                const uint32_t s = g % kStages;
+                ok = __all_sync(0xffffffffu, wait_bounded(&sm.empty[s], ((g / kStages) & 1u) ^ 1u,
                                                           abort_flag, p.status));
                 if (!ok) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&sm.full[s], (uint32_t)blocks * 2u * Smem::kBoxBytes);
-                    for (int u = 0; u < blocks; ++u)
-                        tma_load_5d(sm.k[s][u], &p.tm_k, &sm.full[s], 0, row[u], 0, hkv, page[u]);
-                    for (int u = 0; u < blocks; ++u)
-                        tma_load_5d(sm.v[s][u], &p.tm_v, &sm.full[s], 0, row[u], 0, hkv, page[u]);
+                if (my_u < kBlocks) {
+                    if (my_u < blocks) {
+                        mbar_arrive_expect_tx(&sm.full[s], Smem::kBoxBytes);
+                        tma_load_5d(my_v ? sm.v[s][my_u] : sm.k[s][my_u], my_v ? &p.tm_v : &p.tm_k,
+                                    &sm.full[s], 0, row, 0, head, page);
+                    } else {
+                        mbar_arrive(&sm.full[s]);
+                    }
                 }
                 __syncwarp();
                 ++issued;
             }
         }
         // Copies still in flight land before the block can exit.
-        for (uint32_t g = issued > kStages ? issued - kStages : 0; g < issued; ++g)
+        constexpr uint32_t kMine = kStages / kDecCopyWarps;
+        for (uint32_t i = issued > kMine ? issued - kMine : 0; i < issued; ++i) {
+            const uint32_t g = w + i * kDecCopyWarps;
             wait_bounded(&sm.full[g % kStages], (g / kStages) & 1u, abort_flag, p.status, false);
+        }
         return;
     }
 
     // --------------------------------------------------------------- compute
+    setmaxnreg_inc<kDecComputeRegs>();
+    const int head = warp % kHeads, team = warp / kHeads;
     const int qr = lane >> 2, qc = lane & 3;  // row (and row + 8) and column pair of a fragment
     // Sequences without a key: zeros and -inf (each block takes every
     // gridDim.x-th sequence).
@@ -326,6 +367,16 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
     }
     if (threadIdx.x == 0) p.record[blockIdx.x] = make_int4(0, 0, 0, 0);
 
+    // Where this lane reads K (keys 0-7 of a box, four pieces) and V (16 keys,
+    // two pieces) of a chunk, for each group of pieces.
+    constexpr int kKAt = kPieces >= 8 ? 2 : 1, kVAt = kPieces >= 8 ? 4 : 2;
+    uint32_t k_at[kKAt], v_at[kVAt];
+#pragma unroll
+    for (int i = 0; i < kKAt; ++i) k_at[i] = box_offset<Smem::kRowBytes>(lane & 7, 4 * i + (lane >> 3));
+#pragma unroll
+    for (int i = 0; i < kVAt; ++i) v_at[i] = box_offset<Smem::kRowBytes>(lane & 15, 2 * i + (lane >> 4));
+    const bool modified = p.softcap_out > 0.0f || p.alibi_slopes != nullptr;
+
     bool ok = true;
     long long pos = start, base = sm.base;
     int b = sm.b0;
@@ -340,9 +391,10 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
         const int pair = (int)(in_seq / (uint32_t)st.n);
         const int t0 = (int)(in_seq - (uint32_t)pair * (uint32_t)st.n);
         const int t1 = (int)min((long long)st.n, t0 + (end - pos));
-        const int hkv = pair / p.hchunks, r0 = (pair - hkv * p.hchunks) * kDecRows;
+        const int heads = pair / p.hchunks, r0 = (pair - heads * p.hchunks) * kDecRows;
         const int rows = min(kDecRows, p.group - r0);
-        const int hq0 = hkv * p.group + r0;
+        const int hq0 = heads * kHeads * p.group + r0;  // of the pair's first key head
+        const int hq = hq0 + head * p.group;            // of this warp's
 
         // Q as the A operand.  bf16: K index k of step ks is value 16 ks + k.
         // e4m3: the B operand's word holds four neighbouring values, so index
@@ -353,7 +405,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = qr + 8 * h;
-            const __nv_bfloat16 *q = p.q + ((size_t)b * p.Hq + hq0 + (r < rows ? r : 0)) * D;
+            const __nv_bfloat16 *q = p.q + ((size_t)b * p.Hq + hq + (r < rows ? r : 0)) * D;
             if constexpr (F8) {
                 uint2 w[D / 16];
                 float amax = 0.0f;
@@ -394,7 +446,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
         if (p.alibi_slopes) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (qr + 8 * h < rows) slope[h] = __ldg(p.alibi_slopes + hq0 + qr + 8 * h) * kLog2eF;
+                if (qr + 8 * h < rows) slope[h] = __ldg(p.alibi_slopes + hq + qr + 8 * h) * kLog2eF;
         }
 
         float acc[D / 8][4];
@@ -404,135 +456,132 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
             for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, lr[2] = {0.0f, 0.0f};
 
-        // This warp's tiles of the pair.
+        // This team's tiles of the pair.
         const uint32_t g0 = (uint32_t)(pos - start);
-        int t = t0 + (int)((warp + kDecWarps - g0 % kDecWarps) % kDecWarps);
-        for (; t < t1; t += kDecWarps) {
+        int t = t0 + (int)((team + kTeams - g0 % kTeams) % kTeams);
+        for (; t < t1; t += kTeams) {
             const uint32_t g = g0 + (uint32_t)(t - t0);
             const uint32_t s = g % kStages;
             if (ok)
                 ok = __all_sync(0xffffffffu, wait_bounded(&sm.full[s], (g / kStages) & 1u, abort_flag, p.status));
             if (!ok) break;
-            const int tile0 = (t < st.ns ? t : st.w0 + t - st.ns) * kTile;
+            const int key0 = (t < st.ns ? t : st.w0 + t - st.ns) * kTile;
+            // S of the tile's keys, 8 per column block.
+            float x[kTile / 8][4];
+#pragma unroll
+            for (int n = 0; n < kTile / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[n][e] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kPieces; c += 4) {
+                uint32_t w[kTile / 8][4];
+#pragma unroll
+                for (int n = 0; n < kTile / 8; ++n)
+                    ldsm4(w[n], smem_u32(sm.k[s][n / 2]) + head * Smem::kHeadBytes + (n & 1) * 8 * Smem::kPitch +
+                                    k_at[c / 4 % kKAt] + (c / 8) * Smem::kChunkBytes);
+#pragma unroll
+                for (int i = 0; i < (F8 ? 4 : 2); ++i)
+#pragma unroll
+                    for (int n = 0; n < kTile / 8; ++n) {
+                        if constexpr (F8) {
+                            uint32_t b0, b1;
+                            widen_e4m3x4(w[n][i], b0, b1);
+                            mma16816<true>(x[n], a[c + i], b0, b1);
+                        } else {
+                            mma16816<false>(x[n], a[c / 2 + i], w[n][2 * i], w[n][2 * i + 1]);
+                        }
+                    }
+            }
+            // x[n][2 h + i]: row qr + 8 h, key key0 + 8 n + 2 qc + i.  With a score
+            // modifier the scores become log2 units here, else in the exponent.
+            if (modified) {
+#pragma unroll
+                for (int n = 0; n < kTile / 8; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float &x0 = x[n][2 * h], &x1 = x[n][2 * h + 1];
+                        if (p.softcap_out > 0.0f) {
+                            float r0, r1;
+                            softcap_pair(x0, x1, r0, r1, x0, x1, cap_row[h], p.softcap_out);
+                        } else {
+                            x0 *= c_row[h];
+                            x1 *= c_row[h];
+                        }
+                        const float dist = (float)(st.len - 1 - (key0 + 8 * n + 2 * qc));
+                        x0 = fmaf(-slope[h], dist, x0);
+                        x1 = fmaf(-slope[h], dist - 1.0f, x1);
+                    }
+            }
+            // Keys that the mask hides: their scores become -inf and their values
+            // zero, so what lies in them (NaN too) has no part.
+            uint32_t see[kTile / 8];
+            const bool masked =
+                key0 + kTile > st.len || (key0 < st.lo && key0 + kTile > p.sinks);
+            if (masked) {
+#pragma unroll
+                for (int n = 0; n < kTile / 8; ++n) {
+                    see[n] = 0u;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int key = key0 + 8 * n + 2 * qc + i;
+                        if (key < st.len && (key >= st.lo || key < p.sinks))
+                            see[n] |= i ? 0xffff0000u : 0xffffu;
+                        else
+                            x[n][i] = x[n][2 + i] = -INFINITY;
+                    }
+                }
+            }
+            uint32_t pa[kBlocks][4];
+            float alpha[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float c = modified ? 1.0f : c_row[h];
+                float mx = fmaxf(x[0][2 * h], x[0][2 * h + 1]);
+#pragma unroll
+                for (int n = 1; n < kTile / 8; ++n) mx = fmax3(mx, x[n][2 * h], x[n][2 * h + 1]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * c;
+                alpha[h] = 1.0f;
+                if (mx > m[h] + kDecTau) {
+                    alpha[h] = ex2_mufu(m[h] - mx);
+                    m[h] = mx;
+                }
+                const float neg_m = m[h] == -INFINITY ? 0.0f : -m[h];
+                float sum = 0.0f, rounded = 0.0f;
+#pragma unroll
+                for (int n = 0; n < kTile / 8; ++n) {
+                    const float e0 = ex2_mufu(fmaf(x[n][2 * h], c, neg_m));
+                    const float e1 = ex2_mufu(fmaf(x[n][2 * h + 1], c, neg_m));
+                    sum += e0 + e1;
+                    pa[n / 2][(n & 1) * 2 + h] = pack_weights<F8>(e0, e1, rounded);
+                }
+                l[h] = fmaf(l[h], alpha[h], sum);
+                lr[h] = fmaf(lr[h], alpha[h], rounded);
+            }
+            if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    acc[j][0] *= alpha[0];
+                    acc[j][1] *= alpha[0];
+                    acc[j][2] *= alpha[1];
+                    acc[j][3] *= alpha[1];
+                }
+            }
+            // O += P V.  bf16: acc[j] is values 8 j ..; e4m3: acc[2 j] the even and
+            // acc[2 j + 1] the odd values of 16 j ...  Boxes behind the sequence's
+            // end were not copied: `see` hides what is left in them.
 #pragma unroll
             for (int u = 0; u < kBlocks; ++u) {
-                const int key0 = tile0 + u * kDecBlock;
-                if (key0 >= st.len) break;
-                // S of 16 keys: two column blocks, each in two chains.
-                float sacc[2][2][4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sacc[n][0][e] = sacc[n][1][e] = 0.0f;
-                const uint32_t kb = smem_u32(sm.k[s][u]);
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int x = 0; x < kPieces; x += 4) {
-                        uint32_t w[4];
-                        ldsm4(w, kb + box_offset<Smem::kRowBytes>(n * 8 + (lane & 7), x + (lane >> 3)));
-                        if constexpr (F8) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t b0, b1;
-                                widen_e4m3x4(w[i], b0, b1);
-                                mma16816<true>(sacc[n][i & 1], a[x + i], b0, b1);
-                            }
-                        } else {
-                            mma16816<false>(sacc[n][0], a[x / 2], w[0], w[1]);
-                            mma16816<false>(sacc[n][1], a[x / 2 + 1], w[2], w[3]);
-                        }
-                    }
-                // Log2 scores.  x[h][i]: row qr + 8 h, key key0 + 2 qc + (i & 1) + 8 (i >> 1).
-                float x[2][4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[h][i] = sacc[i >> 1][0][2 * h + (i & 1)] + sacc[i >> 1][1][2 * h + (i & 1)];
-                if (p.softcap_out > 0.0f) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int i = 0; i < 4; i += 2) {
-                            float r0, r1;
-                            softcap_pair(x[h][i], x[h][i + 1], r0, r1, x[h][i], x[h][i + 1],
-                                         cap_row[h], p.softcap_out);
-                        }
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[h][i] *= c_row[h];
-                }
-                if (p.alibi_slopes) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float dist = (float)(st.len - 1 - (key0 + 2 * qc + (i & 1) + 8 * (i >> 1)));
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) x[h][i] = fmaf(-slope[h], dist, x[h][i]);
-                    }
-                }
-                // Keys that the mask hides: their scores become -inf and their
-                // values zero, so what lies in them (NaN too) has no part.
-                uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;
-                const bool masked = key0 + kDecBlock > st.len ||
-                                    (key0 < st.lo && key0 + kDecBlock > p.sinks);
-                if (masked) {
-                    bool see[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = key0 + 2 * qc + (i & 1) + 8 * (i >> 1);
-                        see[i] = key < st.len && (key >= st.lo || key < p.sinks);
-                        if (!see[i]) x[0][i] = x[1][i] = -INFINITY;
-                    }
-                    see0 = (see[0] ? 0xffffu : 0u) | (see[1] ? 0xffff0000u : 0u);
-                    see1 = (see[2] ? 0xffffu : 0u) | (see[3] ? 0xffff0000u : 0u);
-                }
-                uint32_t pa[4];
-                float alpha[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float mx = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    alpha[h] = 1.0f;
-                    if (mx > m[h] + kDecTau) {
-                        alpha[h] = ex2_mufu(m[h] - mx);
-                        m[h] = mx;
-                    }
-                    const float neg_m = m[h] == -INFINITY ? 0.0f : -m[h];
-                    float e[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) e[i] = ex2_mufu(x[h][i] + neg_m);
-                    l[h] = fmaf(l[h], alpha[h], (e[0] + e[1]) + (e[2] + e[3]));
-                    float rounded = 0.0f;
-                    pa[h] = pack_weights<F8>(e[0], e[1], rounded);
-                    pa[2 + h] = pack_weights<F8>(e[2], e[3], rounded);
-                    lr[h] = fmaf(lr[h], alpha[h], rounded);
-                }
-                if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j) {
-                        acc[j][0] *= alpha[0];
-                        acc[j][1] *= alpha[0];
-                        acc[j][2] *= alpha[1];
-                        acc[j][3] *= alpha[1];
-                    }
-                }
-                // O += P V.  bf16: acc[j] is values 8 j ..; e4m3: acc[2 j] the even
-                // and acc[2 j + 1] the odd values of 16 j ...
-                const uint32_t vb = smem_u32(sm.v[s][u]);
+                const uint32_t vb = smem_u32(sm.v[s][u]) + head * Smem::kHeadBytes;
 #pragma unroll
                 for (int j = 0; j < kPieces; j += 2) {
                     uint32_t w[4];
-                    ldsm4_trans(w, vb + box_offset<Smem::kRowBytes>((lane & 7) + ((lane >> 3) & 1) * 8,
-                                                                    j + (lane >> 4)));
+                    ldsm4_trans(w, vb + v_at[j / 2 % kVAt] + (j / 8) * Smem::kChunkBytes);
                     if (masked) {
-                        w[0] &= see0;
-                        w[1] &= see1;
-                        w[2] &= see0;
-                        w[3] &= see1;
+                        w[0] &= see[2 * u];
+                        w[1] &= see[2 * u + 1];
+                        w[2] &= see[2 * u];
+                        w[3] &= see[2 * u + 1];
                     }
                     if constexpr (F8) {
 #pragma unroll
@@ -540,12 +589,12 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
                             uint32_t e0, o0, e1, o1;
                             widen_e4m3x4(__byte_perm(w[2 * i], 0u, 0x3120), e0, o0);
                             widen_e4m3x4(__byte_perm(w[2 * i + 1], 0u, 0x3120), e1, o1);
-                            mma16816<true>(acc[2 * (j + i)], pa, e0, e1);
-                            mma16816<true>(acc[2 * (j + i) + 1], pa, o0, o1);
+                            mma16816<true>(acc[2 * (j + i)], pa[u], e0, e1);
+                            mma16816<true>(acc[2 * (j + i) + 1], pa[u], o0, o1);
                         }
                     } else {
-                        mma16816<false>(acc[j], pa, w[0], w[1]);
-                        mma16816<false>(acc[j + 1], pa, w[2], w[3]);
+                        mma16816<false>(acc[j], pa[u], w[0], w[1]);
+                        mma16816<false>(acc[j + 1], pa[u], w[2], w[3]);
                     }
                 }
             }
@@ -553,81 +602,92 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
             if (lane == 0) mbar_arrive(&sm.empty[s]);
         }
 
-        // ------------------------------------------- join the warps' results
+        // ------------------------------------------- join the teams' results
         // Every warp comes here for every pair, with or without a tile of it
         // (and after a wait that ran out), so the barriers below always meet.
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+#pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
                 l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
                 lr[h] += __shfl_xor_sync(0xffffffffu, lr[h], o);
             }
-            const int r = qr + 8 * h;
-            if (r < rows) {
-                if (qc == 0) sm.ml[warp][r] = make_float4(m[h], l[h], lr[h], 0.0f);
+            if (qr + 8 * h < rows && qc == 0)
+                sm.ml[warp][qr + 8 * h] = make_float4(m[h], l[h], F8 ? l[h] : lr[h], 0.0f);
+        }
+        const bool whole = t0 == 0 && t1 == st.n;
+        const size_t part = (size_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0);
+        // A slice of the values at a time (four accumulators).
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
+        for (int slice = 0; slice < D / kDecSlice; ++slice) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = qr + 8 * h;
+                if (r >= rows) continue;
+#pragma unroll
+                for (int jj = 0; jj < kDecSlice / 8; ++jj) {
+                    const int j = slice * (kDecSlice / 8) + jj;
                     if constexpr (F8) {
-                        float *dst = &sm.o[warp][r][16 * (j >> 1) + 4 * qc + (j & 1)];
+                        float *dst = &sm.o[warp][r][16 * (jj >> 1) + 4 * qc + (jj & 1)];
                         dst[0] = acc[j][2 * h];
                         dst[2] = acc[j][2 * h + 1];
                     } else {
-                        *reinterpret_cast<float2 *>(&sm.o[warp][r][8 * j + 2 * qc]) =
+                        *reinterpret_cast<float2 *>(&sm.o[warp][r][8 * jj + 2 * qc]) =
                             make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
                     }
                 }
             }
-        }
-        named_bar_sync(1, kDecWarps * 32);
-        const bool whole = t0 == 0 && t1 == st.n;
-        const int which = t0 == 0 ? 1 : 0;
-        const size_t part = (size_t)blockIdx.x * 2 + which;
-        for (int i = threadIdx.x; i < rows * (D / 4); i += kDecWarps * 32) {
-            const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-            float mx = sm.ml[0][r].x;
+            named_bar_sync(1, kDecWarps * 32);
+            for (int i = threadIdx.x; i < kHeads * rows * (kDecSlice / 4); i += kDecWarps * 32) {
+                const int d = (i % (kDecSlice / 4)) * 4;
+                const int k = i / (kDecSlice / 4) / rows, r = i / (kDecSlice / 4) % rows;  // head, row
+                float mx = sm.ml[k][r].x;
 #pragma unroll
-            for (int w = 1; w < kDecWarps; ++w) mx = fmaxf(mx, sm.ml[w][r].x);
-            float ls = 0.0f, lrs = 0.0f;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int w = 1; w < kTeams; ++w) mx = fmaxf(mx, sm.ml[k + w * kHeads][r].x);
+                float ls = 0.0f, lrs = 0.0f;
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int w = 0; w < kDecWarps; ++w) {
-                const float4 ml = sm.ml[w][r];
-                const float f = ml.x == -INFINITY ? 0.0f : ex2_mufu(ml.x - mx);
-                const float4 ow = *reinterpret_cast<const float4 *>(&sm.o[w][r][d]);
-                ls = fmaf(ml.y, f, ls);
-                lrs = fmaf(ml.z, f, lrs);
-                o.x = fmaf(ow.x, f, o.x);
-                o.y = fmaf(ow.y, f, o.y);
-                o.z = fmaf(ow.z, f, o.z);
-                o.w = fmaf(ow.w, f, o.w);
+                for (int w = 0; w < kTeams; ++w) {
+                    const float4 ml = sm.ml[k + w * kHeads][r];
+                    const float f = ml.x == -INFINITY ? 0.0f : ex2_mufu(ml.x - mx);
+                    const float4 ow = *reinterpret_cast<const float4 *>(&sm.o[k + w * kHeads][r][d]);
+                    ls = fmaf(ml.y, f, ls);
+                    lrs = fmaf(ml.z, f, lrs);
+                    o.x = fmaf(ow.x, f, o.x);
+                    o.y = fmaf(ow.y, f, o.y);
+                    o.z = fmaf(ow.z, f, o.z);
+                    o.w = fmaf(ow.w, f, o.w);
+                }
+                const int at = slice * kDecSlice + d;
+                if (whole) {
+                    const size_t row = (size_t)b * p.Hq + hq0 + k * p.group + r;
+                    const float inv = lrs == 0.0f ? 0.0f : p.v_descale / lrs;
+                    *reinterpret_cast<uint2 *>(p.o + row * D + at) =
+                        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+                    if (at == 0) p.lse[row] = ls == 0.0f ? -INFINITY : (mx + log2f(ls)) * 0.69314718055994531f;
+                } else {
+                    const size_t row = (part * kHeads + k) * kDecRows + r;
+                    *reinterpret_cast<float4 *>(p.part_o + row * D + at) = o;
+                    if (at == 0) p.part_ml[row] = make_float4(mx, ls, lrs, 0.0f);
+                }
             }
-            if (whole) {
-                const size_t row = (size_t)b * p.Hq + hq0 + r;
-                const float inv = lrs == 0.0f ? 0.0f : p.v_descale / lrs;
-                *reinterpret_cast<uint2 *>(p.o + row * D + d) =
-                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-                if (d == 0) p.lse[row] = ls == 0.0f ? -INFINITY : (mx + log2f(ls)) * 0.69314718055994531f;
-            } else {
-                *reinterpret_cast<float4 *>(p.part_o + (part * kDecRows + r) * D + d) = o;
-                if (d == 0) p.part_ml[part * kDecRows + r] = make_float4(mx, ls, lrs, 0.0f);
-            }
+            named_bar_sync(1, kDecWarps * 32);  // the buffer is free again
         }
         // A pair that begins here and goes on: the join starts at this block.
         if (t0 == 0 && t1 < st.n && threadIdx.x == 0) {
             const long long last = pos + st.n - 1;
             p.record[blockIdx.x] = make_int4(b, hq0, rows, (int)(last / sm.share));
         }
-        named_bar_sync(1, kDecWarps * 32);  // the buffers are free again
         pos += t1 - t0;
     }
 }
 
 // Joins the partial results of the pair that is first cut at the end of block
-// blockIdx.x: row blockIdx.y of it.  The partials are those of that block
+// blockIdx.x: row blockIdx.y of head blockIdx.z of it.  The partials are those of that block
 // (its second) and of the blocks up to the recorded one (their first).
 constexpr int kJoinThreads = 256;
 
-template <int D>
+template <int D, int kHeads>
 __global__ void __launch_bounds__(kJoinThreads)
 decode_join_kernel(const DecodeParams p) {
     constexpr int kCols = D / 4, kParts = kJoinThreads / kCols;  // float4 columns, rows of threads
@@ -635,11 +695,11 @@ decode_join_kernel(const DecodeParams p) {
     __shared__ float4 sum_o[kParts][kCols];
     __shared__ float2 sum_l[kParts];
     const int4 rec = p.record[blockIdx.x];
-    const int row = blockIdx.y;
+    const int row = blockIdx.y, head = blockIdx.z;
     if (row >= rec.z) return;
     const int first = blockIdx.x, n = rec.w - first + 1;
     auto part_row = [&](int i) {
-        return ((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * kDecRows + row;
+        return (((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * kHeads + head) * kDecRows + row;
     };
     float mx = -INFINITY;
     for (int i = threadIdx.x; i < n; i += kJoinThreads) mx = fmaxf(mx, p.part_ml[part_row(i)].x);
@@ -675,7 +735,7 @@ decode_join_kernel(const DecodeParams p) {
             o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
             l.x += sum_l[w].x, l.y += sum_l[w].y;
         }
-        const size_t out = (size_t)rec.x * p.Hq + rec.y + row;
+        const size_t out = (size_t)rec.x * p.Hq + rec.y + head * p.group + row;
         const float inv = l.y == 0.0f ? 0.0f : p.v_descale / l.y;
         *reinterpret_cast<uint2 *>(p.o + out * D + 4 * c) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));

@@ -94,17 +94,19 @@ struct DecodeLayout {
     size_t part_ml, record, total;
 };
 DecodeLayout decode_layout(int D) {
+    // Key heads of a pair: at most what makes 256 bytes of 8-bit values.
+    const size_t rows = (size_t)kDecodeMaxBlocks * 2 * std::max(1, 256 / D) * tab::kDecRows;
     DecodeLayout L;
-    L.part_ml = align256((size_t)kDecodeMaxBlocks * 2 * tab::kDecRows * D * sizeof(float));
-    L.record = L.part_ml + align256((size_t)kDecodeMaxBlocks * 2 * tab::kDecRows * sizeof(float4));
+    L.part_ml = align256(rows * D * sizeof(float));
+    L.record = L.part_ml + align256(rows * sizeof(float4));
     L.total = L.record + align256((size_t)kDecodeMaxBlocks * sizeof(int4));
     return L;
 }
 
-// Boxes of 16 keys of one head; the rows of a box are 128-byte pieces with
+// Boxes of 16 keys of `heads` heads; the rows of a box are 128-byte pieces with
 // the 128-byte swizzle (64 bytes for D = 64 in 8 bits).
 attn_status_t make_cache_map(CUtensorMap *map, const void *base, int pages, int page_size, int Hkv,
-                             int D, int eb) {
+                             int D, int eb, int heads) {
     tab_host::EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
     const int row = D * eb, piece = std::min(row, 128);
@@ -113,7 +115,7 @@ attn_status_t make_cache_map(CUtensorMap *map, const void *base, int pages, int 
     const cuuint64_t strides[4] = {(cuuint64_t)Hkv * row, (cuuint64_t)piece, (cuuint64_t)row,
                                    (cuuint64_t)page_size * Hkv * row};
     const cuuint32_t box[5] = {(cuuint32_t)(piece / eb), (cuuint32_t)tab::kDecBlock,
-                               (cuuint32_t)(row / piece), 1, 1};
+                               (cuuint32_t)(row / piece), (cuuint32_t)heads, 1};
     const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
     const CUresult r = fn(
         map, eb == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
@@ -124,28 +126,56 @@ attn_status_t make_cache_map(CUtensorMap *map, const void *base, int pages, int 
     return ATTN_OK;
 }
 
-template <int D, bool F8, int kBlocks, int kStages>
-attn_status_t launch_decode(const tab::DecodeParams &p, int blocks, cudaStream_t stream) {
-    using Smem = tab::DecodeSmem<D, F8, kBlocks, kStages>;
+template <int D, bool F8, int kHeads, int kBlocks, int kStages>
+attn_status_t launch_decode(tab::DecodeParams &p, const void *k_cache, const void *v_cache,
+                            int blocks, cudaStream_t stream) {
+    using Smem = tab::DecodeSmem<D, F8, kHeads, kBlocks, kStages>;
     constexpr size_t smem = sizeof(Smem) + 1024;
     static_assert(tab::kDecCtasPerSm * (smem + 1024) <= 233472, "shared memory budget");
-    auto kernel = tab::decode_paged_kernel<D, F8, kBlocks, kStages>;
+    auto kernel = tab::decode_paged_kernel<D, F8, kHeads, kBlocks, kStages>;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr_err[kMaxDevices];
+    static cudaFuncAttributes attrs[kMaxDevices];
     int dev = 0;
     cudaGetDevice(&dev);
     std::call_once(once[dev], [&]() {
         attr_err[dev] =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (attr_err[dev] == cudaSuccess) attr_err[dev] = cudaFuncGetAttributes(&attrs[dev], kernel);
     });
     if (attr_err[dev] != cudaSuccess)
-        return fail(ATTN_ERR_LAUNCH, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err[dev]));
+        return fail(ATTN_ERR_LAUNCH, "kernel attributes: %s", cudaGetErrorString(attr_err[dev]));
+    // The register split (setmaxnreg) counts on this allocation: with less,
+    // the increase would wait forever, so never launch such a build.
+    if (attrs[dev].numRegs < tab::kDecLaunchRegs)
+        return fail(ATTN_ERR_LAUNCH, "kernel compiled with %d registers per thread, %d needed",
+                    attrs[dev].numRegs, tab::kDecLaunchRegs);
+    attn_status_t s;
+    const int eb = F8 ? 1 : 2;
+    if ((s = make_cache_map(&p.tm_k, k_cache, p.num_pages, p.page_size, p.Hkv, D, eb, kHeads)) != ATTN_OK ||
+        (s = make_cache_map(&p.tm_v, v_cache, p.num_pages, p.page_size, p.Hkv, D, eb, kHeads)) != ATTN_OK)
+        return s;
     kernel<<<blocks, tab::kDecThreads, smem, stream>>>(p);
-    const attn_status_t s = launch_result();
-    if (s != ATTN_OK) return s;
-    tab::decode_join_kernel<D>
-        <<<dim3(blocks, std::min(p.group, tab::kDecRows)), tab::kJoinThreads, 0, stream>>>(p);
+    if ((s = launch_result()) != ATTN_OK) return s;
+    tab::decode_join_kernel<D, kHeads>
+        <<<dim3(blocks, std::min(p.group, tab::kDecRows), kHeads), tab::kJoinThreads, 0, stream>>>(p);
     return launch_result();
+}
+
+// The variant by the bytes of a key's head: pairs of as many key heads as make
+// 256 bytes and divide Hkv, tiles of 16 KB (32 keys) or, where a tile has one
+// or two heads of 256 bytes in all and so four or two teams, of 8 KB.
+attn_status_t dispatch_decode(tab::DecodeParams &p, const void *k, const void *v, int D, bool f8,
+                              int blocks, cudaStream_t s) {
+    const bool two = p.Hkv % 2 == 0, four = p.Hkv % 4 == 0;
+    if (!f8 && D == 128) return launch_decode<128, false, 1, 1, 12>(p, k, v, blocks, s);
+    if (!f8) return two ? launch_decode<64, false, 2, 2, 6>(p, k, v, blocks, s)
+                        : launch_decode<64, false, 1, 2, 12>(p, k, v, blocks, s);
+    if (D == 128) return two ? launch_decode<128, true, 2, 2, 4>(p, k, v, blocks, s)
+                             : launch_decode<128, true, 1, 2, 8>(p, k, v, blocks, s);
+    if (four) return launch_decode<64, true, 4, 2, 6>(p, k, v, blocks, s);
+    return two ? launch_decode<64, true, 2, 2, 12>(p, k, v, blocks, s)
+               : launch_decode<64, true, 1, 2, 16>(p, k, v, blocks, s);
 }
 
 }  // namespace
@@ -401,8 +431,6 @@ attn_status_t attn_decode_paged(const void *q, const void *k_cache, const void *
     const bool f8 = kv_dtype == ATTN_KV_E4M3;
     tab::DecodeParams p;
     memset(&p, 0, sizeof p);
-    if ((s = make_cache_map(&p.tm_k, k_cache, num_pages, page_size, Hkv, D, f8 ? 1 : 2)) != ATTN_OK) return s;
-    if ((s = make_cache_map(&p.tm_v, v_cache, num_pages, page_size, Hkv, D, f8 ? 1 : 2)) != ATTN_OK) return s;
     const DecodeLayout L = decode_layout(D);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -433,8 +461,7 @@ attn_status_t attn_decode_paged(const void *q, const void *k_cache, const void *
     p.alibi_slopes = alibi_slopes;
     const int blocks = std::min(kDecodeMaxBlocks, tab::kDecCtasPerSm * st->num_sms);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (D == 128) return f8 ? launch_decode<128, true, 2, 8>(p, blocks, cs) : launch_decode<128, false, 1, 8>(p, blocks, cs);
-    return f8 ? launch_decode<64, true, 2, 16>(p, blocks, cs) : launch_decode<64, false, 2, 8>(p, blocks, cs);
+    return dispatch_decode(p, k_cache, v_cache, D, f8, blocks, cs);
 }
 
 }  // extern "C"
