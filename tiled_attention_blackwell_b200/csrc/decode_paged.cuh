@@ -18,7 +18,7 @@
 // (Read head by head, a key's 128 or 64 bytes lie 1 KB and more apart, and
 // the copies run at 67 % and 41 % of the copy rate instead of 95 %.)
 //
-// Warp roles: warps 0-3 compute, warps 4 and 5 copy, two more are idle.  Warp
+// Warp roles: warps 0-3 compute, warps 4-7 copy.  Warp
 // w works on head w % kHeads, as part of team w / kHeads; team t takes the
 // tiles g = t, t + kTeams, ... of the block's run and keeps the running
 // maximum, sums and output of its head in registers.  The teams' results are
@@ -42,8 +42,8 @@
 namespace tab {
 
 constexpr int kDecWarps = 4;                         // computing warps
-constexpr int kDecCopyWarps = 2;
-constexpr int kDecThreads = 2 * kDecWarps * 32;
+constexpr int kDecCopyWarps = 4;
+constexpr int kDecThreads = (kDecWarps + kDecCopyWarps) * 32;
 constexpr int kDecRows = 16;                         // query heads per pair
 constexpr int kDecBlock = 16;                        // keys per TMA box
 constexpr int kDecSlice = 32;                        // values of the output joined at a time
@@ -199,6 +199,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
     // warp's alone: no wait can be two phases behind its slot.
     static_assert(kStages % kTeams == 0 && kStages % kDecCopyWarps == 0, "slots belong to fixed warps");
     extern __shared__ uint8_t smem_raw[];
+    launch_dependents();  // the join: its blocks wait for this grid's end
     const uint32_t raw_off = smem_u32(smem_raw);
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (raw_off & 1023u)) & 1023u));
     const int warp = warp_id(), lane = lane_id();
@@ -262,7 +263,6 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
         // This warp's tiles are w, w + kDecCopyWarps, ...; each lane looks up one of
         // the next 32 of them: its pair and its pages.
         const uint32_t w = warp - kDecWarps;
-        if (w >= kDecCopyWarps) return;
         const uint32_t n_mine = n_tiles > w ? (n_tiles - w - 1) / kDecCopyWarps + 1 : 0;
         long long base = sm.base;
         int b = sm.b0;
@@ -687,13 +687,24 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
 // (its second) and of the blocks up to the recorded one (their first).
 constexpr int kJoinThreads = 256;
 
+struct JoinParams {
+    const float *part_o;
+    const float4 *part_ml;
+    const int4 *record;
+    __nv_bfloat16 *o;
+    float *lse;
+    int Hq, group;
+    float v_descale;
+};
+
 template <int D, int kHeads>
 __global__ void __launch_bounds__(kJoinThreads)
-decode_join_kernel(const DecodeParams p) {
+decode_join_kernel(const JoinParams p) {
     constexpr int kCols = D / 4, kParts = kJoinThreads / kCols;  // float4 columns, rows of threads
     __shared__ float red[kJoinThreads / 32];
     __shared__ float4 sum_o[kParts][kCols];
     __shared__ float2 sum_l[kParts];
+    wait_for_primary();
     const int4 rec = p.record[blockIdx.x];
     const int row = blockIdx.y, head = blockIdx.z;
     if (row >= rec.z) return;

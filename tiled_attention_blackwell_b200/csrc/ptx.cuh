@@ -112,6 +112,15 @@ __device__ __forceinline__ float ld_nc_f32(const float *ptr) {
     return v;
 }
 
+// Dependent launch in one stream: the first kernel lets the next one's blocks
+// start early; they wait here until it has ended and its writes are visible.
+__device__ __forceinline__ void launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_primary() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar,

@@ -32,6 +32,27 @@ attn_status_t launch_result() {
     return ok();
 }
 
+// Launches `kernel` so that its blocks may start while the kernel before it in
+// the stream ends (it waits for that with wait_for_primary()).
+template <class... Args>
+attn_status_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 threads, cudaStream_t stream,
+                               Args... args) {
+    cudaLaunchAttribute attr;
+    memset(&attr, 0, sizeof attr);
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config;
+    memset(&config, 0, sizeof config);
+    config.gridDim = grid;
+    config.blockDim = threads;
+    config.stream = stream;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&config, kernel, args...);
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
 // ------------------------------------------------------------- norm + rope
 
 // Blocks of the backward, per SM: each leaves one share of dw.  A fixed
@@ -155,26 +176,32 @@ attn_status_t launch_decode(tab::DecodeParams &p, const void *k_cache, const voi
     if ((s = make_cache_map(&p.tm_k, k_cache, p.num_pages, p.page_size, p.Hkv, D, eb, kHeads)) != ATTN_OK ||
         (s = make_cache_map(&p.tm_v, v_cache, p.num_pages, p.page_size, p.Hkv, D, eb, kHeads)) != ATTN_OK)
         return s;
+    // No more blocks than the longest sequences allow tiles for one per team.
+    const double tiles = (double)p.B * (p.Hkv / kHeads) * p.hchunks *
+                         (((double)p.max_pages * p.page_size + Smem::kTile - 1) / Smem::kTile);
+    if (tiles / Smem::kTeams + 1 < blocks) blocks = (int)(tiles / Smem::kTeams) + 1;
     kernel<<<blocks, tab::kDecThreads, smem, stream>>>(p);
     if ((s = launch_result()) != ATTN_OK) return s;
-    tab::decode_join_kernel<D, kHeads>
-        <<<dim3(blocks, std::min(p.group, tab::kDecRows), kHeads), tab::kJoinThreads, 0, stream>>>(p);
-    return launch_result();
+    const tab::JoinParams jp = {p.part_o, p.part_ml, p.record, p.o, p.lse, p.Hq, p.group, p.v_descale};
+    return launch_dependent(tab::decode_join_kernel<D, kHeads>,
+                            dim3(blocks, std::min(p.group, tab::kDecRows), kHeads),
+                            dim3(tab::kJoinThreads), stream, jp);
 }
 
 // The variant by the bytes of a key's head: pairs of as many key heads as make
-// 256 bytes and divide Hkv, tiles of 16 KB (32 keys) or, where a tile has one
-// or two heads of 256 bytes in all and so four or two teams, of 8 KB.
+// 256 bytes and divide Hkv; rings of 64 KB per block (128 KB per SM; with 96
+// KB the bf16 cases read 5 % slower), in tiles of 32 keys, or of 16 for heads
+// of 256 bytes.
 attn_status_t dispatch_decode(tab::DecodeParams &p, const void *k, const void *v, int D, bool f8,
                               int blocks, cudaStream_t s) {
     const bool two = p.Hkv % 2 == 0, four = p.Hkv % 4 == 0;
-    if (!f8 && D == 128) return launch_decode<128, false, 1, 1, 12>(p, k, v, blocks, s);
-    if (!f8) return two ? launch_decode<64, false, 2, 2, 6>(p, k, v, blocks, s)
-                        : launch_decode<64, false, 1, 2, 12>(p, k, v, blocks, s);
+    if (!f8 && D == 128) return launch_decode<128, false, 1, 1, 8>(p, k, v, blocks, s);
+    if (!f8) return two ? launch_decode<64, false, 2, 2, 4>(p, k, v, blocks, s)
+                        : launch_decode<64, false, 1, 2, 8>(p, k, v, blocks, s);
     if (D == 128) return two ? launch_decode<128, true, 2, 2, 4>(p, k, v, blocks, s)
                              : launch_decode<128, true, 1, 2, 8>(p, k, v, blocks, s);
-    if (four) return launch_decode<64, true, 4, 2, 6>(p, k, v, blocks, s);
-    return two ? launch_decode<64, true, 2, 2, 12>(p, k, v, blocks, s)
+    if (four) return launch_decode<64, true, 4, 2, 4>(p, k, v, blocks, s);
+    return two ? launch_decode<64, true, 2, 2, 8>(p, k, v, blocks, s)
                : launch_decode<64, true, 1, 2, 16>(p, k, v, blocks, s);
 }
 
