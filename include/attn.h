@@ -424,11 +424,11 @@ ATTN_API attn_status_t attn_qk_norm_rope_bwd(
  * attn_qk_norm_rope for the new tokens of a serving step: Q goes to q_out,
  * the normed and rotated K and the plain V go to slot slots[t] of the caches
  * [num_slots][Hkv][D] (slot = page * page_size + place in the page), as bf16
- * or as e4m3 codes of value / descale (nearest even, saturating at +-448; the
- * value a code stands for is descale * code, as in attn_fwd_fp8).  For a
- * bf16 cache both descale factors are 1.  v: bf16 [tokens][Hkv][D], like k.
- * A token with a negative slot is padding: nothing of it is read or written,
- * its row of q_out included.  A slot >= num_slots is treated the same and
+ * or as e4m3 codes of value * (1 / descale) (the reciprocal in fp32, finite;
+ * nearest even, saturating at +-448; the value a code stands for is descale *
+ * code, as in attn_fwd_fp8).  For a bf16 cache both descale factors are 1.  v: bf16 [tokens][Hkv][D], like k.
+ * A token with a negative slot is padding: nothing of it is used and nothing
+ * written, its row of q_out included.  A slot >= num_slots is treated the same and
  * reports ATTN_ERR_RANGE.  Slots of one call are distinct: of two tokens with
  * one slot, either's values may be left there, K and V apart.
  * slots: int32 [tokens]; caches 16-byte aligned.

@@ -61,8 +61,8 @@ def test_norm_refusals(L, call, kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(v=0), INV), (dict(vs=128), INV), (dict(slots=0), INV), (dict(slots=P + 1), MIS), (dict(kc=0), INV),
-    (dict(vc=P + 4), MIS), (dict(kv=2), INV), (dict(n=0), INV), (dict(kd=0.5), INV), (dict(kv=1, kd=0.0), INV),
-    (dict(kv=1, vd=float("inf")), INV)])
+    (dict(vc=P + 4), MIS), (dict(kv=2), INV), (dict(n=0), INV), (dict(kd=0.5), INV), (dict(kv=1, kd=0.0), INV), (dict(kv=1, kd=1e-39), INV),
+    (dict(kv=1, vd=float("inf")), INV), (dict(kv=1, kd=1e-39), INV)])
 def test_norm_cache_refusals(L, kw, status):
     assert call_norm_cache(L, **kw) == status
 
@@ -105,7 +105,7 @@ def test_valid_calls_without_gpu_report_cuda_error(L):
 
 def test_workspace_sizes(L):
     assert attn.decode_workspace_size(128) >= 296 * 2 * 16 * 128 * 4 and attn.decode_workspace_size(0) == 0
-    assert L.attn_qk_norm_rope_bwd_workspace_size(64) >= 4 * 148 * 2 * 64 * 4
+    assert L.attn_qk_norm_rope_bwd_workspace_size(64) >= 2 * 148 * 2 * 64 * 4
 
 
 class _CudaStandIn(torch.Tensor):

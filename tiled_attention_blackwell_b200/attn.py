@@ -710,8 +710,8 @@ def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos, sin, positions, slots, 
     writes K (normed and rotated) and V of token t to slot slots[t] = page *
     page_size + place of the caches [num_pages, page_size, Hkv, D], bf16 or
     float8_e4m3fn (codes of value / descale).  slots int32 [...], distinct; a
-    negative slot marks padding, of which nothing is read or written (its row
-    of q_out keeps what it held)."""
+    negative slot marks padding, for which nothing is written (its row of
+    q_out keeps what it held)."""
     if q_out is None:
         q_out = torch.empty_like(q)
     index = _device_of("q k v q_weight k_weight cos sin positions slots k_cache v_cache q_out", q, k,

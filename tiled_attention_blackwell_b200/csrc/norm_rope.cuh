@@ -11,12 +11,15 @@
 //   dx_d = r h_d - r^3 x_d (sum_e h_e x_e) / D
 //   dw_d = sum over tokens and heads of g_d x_d r
 //
-// Bound by memory: two bytes in and two out per value (ten in all for a
+// Bound by memory: two bytes in and two out per value (eight in all for a
 // query's value in the backward, whose dy is fp32) against about ten
-// operations.  D / 8 lanes hold a head, eight values (16 bytes) per lane, so
-// the sums over a head are shuffles and every access is 16 bytes wide.  A
-// group of lanes takes kRows heads of one token at a time: their loads are
-// in flight together and the angles are read once for all of them.
+// operations.  D / 8 lanes hold a head, eight values per lane: the four first
+// and the four second members of four pairs, so that the rotation stays
+// within a lane and only the sums over the head are shuffles.  In the half
+// style those are two runs of four values, rot/2 apart; interleaved, one run
+// of eight.  A group of lanes takes kNormRows heads of one token at a time:
+// their loads are in flight together, and the angles, with the weights
+// multiplied in, serve all of them.
 #pragma once
 
 #include "common.cuh"
@@ -38,14 +41,14 @@ struct NormRopeParams {
     long long tokens;
     int Hq, Hkv, rot, max_positions;
     int chunks_q, chunks_k;   // kRows-head chunks of a token's query and key heads
-    int w_fp32, interleaved;
+    int w_fp32;
     float eps;
     // Serving form: slots [tokens] (negative: padding, left alone), caches
     // [num_slots][Hkv][D].
     const int *slots;
     void *k_cache, *v_cache;
     long long num_slots;
-    float k_descale, v_descale;
+    float k_scale, v_scale;   // e4m3: codes of value * scale
     // Backward.
     const void *dq, *dk;      // [tokens][H][D], contiguous heads, fp32 or bf16
     long long dq_stride, dk_stride;
@@ -53,97 +56,132 @@ struct NormRopeParams {
     float *partial;           // [blocks][2][D]
 };
 
-struct Lane8 {
-    float v[8];
-};
-
-// Sixteen bytes of an input that an output may overwrite in place (each
-// thread reads its values before it writes them): not the read-only path.
-__device__ __forceinline__ uint4 load16(const __nv_bfloat16 *p) {
-    return *reinterpret_cast<const uint4 *>(p);
-}
-
-__device__ __forceinline__ Lane8 unpack8(uint4 p) {
-    Lane8 r;
-    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        r.v[2 * e] = __uint_as_float(w[e] << 16);
-        r.v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
-    return r;
-}
-
-__device__ __forceinline__ uint4 pack8(const Lane8 &x) {
-    return make_uint4(pack_bf16x2(x.v[0], x.v[1]), pack_bf16x2(x.v[2], x.v[3]),
-                      pack_bf16x2(x.v[4], x.v[5]), pack_bf16x2(x.v[6], x.v[7]));
-}
-
-__device__ __forceinline__ Lane8 load8_f32(const float *p) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-}
-
-// Eight weights from d on.  The caller guarantees 16-byte alignment.
-__device__ __forceinline__ Lane8 load_weights(const void *w, int fp32, int d) {
-    if (fp32) return load8_f32(static_cast<const float *>(w) + d);
-    return unpack8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(w) + d)));
-}
-
-// Cosines and sines of a lane's eight values; `turn` is false past `rot`.
-// Half style: one pair of factors per value; interleaved: per pair (the
-// first four entries).
-struct Angles {
-    float c[8], s[8];
+// Where a lane's values of a head lie: `a` and `b` are the first values of its
+// two runs of four; `turn` says whether they are rotated (then by the angles
+// [angle, angle + 4) of the position).
+struct LanePlace {
+    int a, b, angle;
     bool turn;
 };
 
-__device__ __forceinline__ Angles load_angles(const NormRopeParams &p, int pos, int d) {
-    Angles a;
-    a.turn = d < p.rot;
-    if (!a.turn) return a;
-    const size_t row = (size_t)pos * (p.rot / 2);
-    if (p.interleaved) {
-        const float4 c = __ldg(reinterpret_cast<const float4 *>(p.cos + row + d / 2));
-        const float4 s = __ldg(reinterpret_cast<const float4 *>(p.sin + row + d / 2));
-        a.c[0] = c.x, a.c[1] = c.y, a.c[2] = c.z, a.c[3] = c.w;
-        a.s[0] = s.x, a.s[1] = s.y, a.s[2] = s.z, a.s[3] = s.w;
+template <bool INTERLEAVED>
+__device__ __forceinline__ LanePlace lane_place(int l, int rot) {
+    LanePlace at;
+    at.angle = 4 * l;
+    at.turn = 8 * l < rot;
+    if (INTERLEAVED || !at.turn) {
+        at.a = 8 * l;
+        at.b = 8 * l + 4;
     } else {
-        const int i = d < p.rot / 2 ? d : d - p.rot / 2;
-        const Lane8 c = load8_f32(p.cos + row + i), s = load8_f32(p.sin + row + i);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a.c[e] = c.v[e], a.s[e] = s.v[e];
+        at.a = 4 * l;
+        at.b = 4 * l + rot / 2;
     }
-    return a;
+    return at;
 }
 
-// R u (sign = 1) or R^T u (sign = -1) of a lane's eight values.  Whole warps
-// call it: in the half style the partner's values come from the lane rot/16
-// away.  rot is a multiple of 16, so a lane's eight values lie in one half.
-__device__ __forceinline__ Lane8 rotate8(const NormRopeParams &p, const Lane8 &u, const Angles &a,
-                                         int d, float sign) {
-    Lane8 y = u;
-    if (p.interleaved) {
-        if (a.turn) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float s = sign * a.s[e];
-                y.v[2 * e] = u.v[2 * e] * a.c[e] - u.v[2 * e + 1] * s;
-                y.v[2 * e + 1] = u.v[2 * e + 1] * a.c[e] + u.v[2 * e] * s;
-            }
-        }
+// A lane's eight values as the first members p and the second members q of
+// its four pairs (interleaved: neighbours; half style: run a and run b).
+struct Pairs {
+    float p[4], q[4];
+};
+
+template <bool INTERLEAVED>
+__device__ __forceinline__ Pairs make_pairs(const float (&a)[4], const float (&b)[4]) {
+    if (INTERLEAVED) return {{a[0], a[2], b[0], b[2]}, {a[1], a[3], b[1], b[3]}};
+    return {{a[0], a[1], a[2], a[3]}, {b[0], b[1], b[2], b[3]}};
+}
+
+__device__ __forceinline__ void unpack4(float (&v)[4], uint2 w) {
+    v[0] = __uint_as_float(w.x << 16);
+    v[1] = __uint_as_float(w.x & 0xffff0000u);
+    v[2] = __uint_as_float(w.y << 16);
+    v[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+
+// Both runs of a row of bf16 values that an output may overwrite in place
+// (each thread reads its values before it writes them): not the read-only path.
+struct Raw8 {
+    uint2 a, b;
+};
+__device__ __forceinline__ Raw8 load_raw(const __nv_bfloat16 *row, const LanePlace &at) {
+    return {*reinterpret_cast<const uint2 *>(row + at.a), *reinterpret_cast<const uint2 *>(row + at.b)};
+}
+
+template <bool INTERLEAVED>
+__device__ __forceinline__ Pairs unpack8(const Raw8 &r) {
+    float a[4], b[4];
+    unpack4(a, r.a);
+    unpack4(b, r.b);
+    return make_pairs<INTERLEAVED>(a, b);
+}
+
+template <bool INTERLEAVED>
+__device__ __forceinline__ void store_bf16(__nv_bfloat16 *row, const LanePlace &at, const Pairs &y) {
+    uint2 a, b;
+    if (INTERLEAVED) {
+        a = make_uint2(pack_bf16x2(y.p[0], y.q[0]), pack_bf16x2(y.p[1], y.q[1]));
+        b = make_uint2(pack_bf16x2(y.p[2], y.q[2]), pack_bf16x2(y.p[3], y.q[3]));
     } else {
-        const int off = p.rot / 16;
-        const bool low = d < p.rot / 2;
-        const int partner = !a.turn ? lane_id() : low ? lane_id() + off : lane_id() - off;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float o = __shfl_sync(0xffffffffu, u.v[e], partner);
-            if (a.turn) y.v[e] = u.v[e] * a.c[e] + (low ? -sign : sign) * a.s[e] * o;
-        }
+        a = make_uint2(pack_bf16x2(y.p[0], y.p[1]), pack_bf16x2(y.p[2], y.p[3]));
+        b = make_uint2(pack_bf16x2(y.q[0], y.q[1]), pack_bf16x2(y.q[2], y.q[3]));
     }
-    return y;
+    *reinterpret_cast<uint2 *>(row + at.a) = a;
+    *reinterpret_cast<uint2 *>(row + at.b) = b;
+}
+
+// e4m3 codes of x * scale (nearest even, saturating).
+template <bool INTERLEAVED>
+__device__ __forceinline__ void store_e4m3(uint8_t *row, const LanePlace &at, const Pairs &x, float scale) {
+    Pairs y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y.p[e] = x.p[e] * scale, y.q[e] = x.q[e] * scale;
+    uint32_t a, b;
+    if (INTERLEAVED) {
+        a = pack_e4m3x4(y.p[0], y.q[0], y.p[1], y.q[1]);
+        b = pack_e4m3x4(y.p[2], y.q[2], y.p[3], y.q[3]);
+    } else {
+        a = pack_e4m3x4(y.p[0], y.p[1], y.p[2], y.p[3]);
+        b = pack_e4m3x4(y.q[0], y.q[1], y.q[2], y.q[3]);
+    }
+    *reinterpret_cast<uint32_t *>(row + at.a) = a;
+    *reinterpret_cast<uint32_t *>(row + at.b) = b;
+}
+
+__device__ __forceinline__ void load4_f32(float (&v)[4], const float *p) {
+    const float4 f = __ldg(reinterpret_cast<const float4 *>(p));
+    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+}
+
+template <bool INTERLEAVED>
+__device__ __forceinline__ Pairs load_weights(const void *w, int fp32, const LanePlace &at) {
+    float a[4], b[4];
+    if (fp32) {
+        load4_f32(a, static_cast<const float *>(w) + at.a);
+        load4_f32(b, static_cast<const float *>(w) + at.b);
+    } else {
+        const __nv_bfloat16 *h = static_cast<const __nv_bfloat16 *>(w);
+        unpack4(a, __ldg(reinterpret_cast<const uint2 *>(h + at.a)));
+        unpack4(b, __ldg(reinterpret_cast<const uint2 *>(h + at.b)));
+    }
+    return make_pairs<INTERLEAVED>(a, b);
+}
+
+// Cosines and sines of a lane's four pairs (1 and 0 past `rot`) at the
+// position `pos`; one outside the table is clamped and reported.
+__device__ __forceinline__ void load_angles(float (&c)[4], float (&s)[4], const NormRopeParams &p,
+                                            int pos, const LanePlace &at) {
+    if (pos < 0 || pos >= p.max_positions) {
+        atomicCAS(p.status, 0, kStatusRange);
+        pos = pos < 0 ? 0 : p.max_positions - 1;
+    }
+    const size_t i = (size_t)pos * (p.rot / 2) + at.angle;
+    if (at.turn) {
+        load4_f32(c, p.cos + i);
+        load4_f32(s, p.sin + i);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = 1.0f, s[e] = 0.0f;
+    }
 }
 
 // Sum over the D / 8 lanes of a head.
@@ -154,177 +192,226 @@ __device__ __forceinline__ float head_sum(float x) {
     return x;
 }
 
-// Position of a token, clamped into the table (out of range: reported).
-__device__ __forceinline__ int token_position(const NormRopeParams &p, long long token) {
-    const int pos = __ldg(p.positions + token);
-    if (pos >= 0 && pos < p.max_positions) return pos;
-    atomicCAS(p.status, 0, kStatusRange);
-    return pos < 0 ? 0 : p.max_positions - 1;
-}
-
-// Eight values as e4m3 codes of x / descale (nearest even, saturating).
-__device__ __forceinline__ uint2 codes8(const Lane8 &x, float descale) {
-    return make_uint2(pack_e4m3x4(__fdiv_rn(x.v[0], descale), __fdiv_rn(x.v[1], descale),
-                                  __fdiv_rn(x.v[2], descale), __fdiv_rn(x.v[3], descale)),
-                      pack_e4m3x4(__fdiv_rn(x.v[4], descale), __fdiv_rn(x.v[5], descale),
-                                  __fdiv_rn(x.v[6], descale), __fdiv_rn(x.v[7], descale)));
+// sum_e x_e y_e of a lane's values.
+__device__ __forceinline__ float lane_dot(const Pairs &x, const Pairs &y) {
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+        fma2(s0, s1, x.p[e], x.p[e + 1], y.p[e], y.p[e + 1], s0, s1);
+        fma2(s0, s1, x.q[e], x.q[e + 1], y.q[e], y.q[e + 1], s0, s1);
+    }
+    return s0 + s1;
 }
 
 // KV: where K goes.  0: k_out, like Q; 1: a bf16 cache; 2: an e4m3 cache
 // (with V beside it in both).
 constexpr int kNormRows = 4;  // heads of a token that a group of lanes takes together
 
-template <int D, int KV>
+template <int D, int KV, bool INTERLEAVED>
 __global__ void __launch_bounds__(kNormThreads)
 norm_rope_kernel(const NormRopeParams p) {
     constexpr int kLanes = D / 8, kGroups = kNormThreads / kLanes, U = kNormRows;
-    const int group = threadIdx.x / kLanes;
-    const int d = (threadIdx.x % kLanes) * 8;
-    const int chunks = p.chunks_q + (KV ? 2 : 1) * p.chunks_k;
-    const uint32_t item = blockIdx.x * kGroups + group;  // the host bounds the items by 2^31
-    long long token = item / (uint32_t)chunks;
-    // Groups past the end, and padding tokens, read nothing and write nothing
-    // but stay for the shuffles.
-    bool live = token < p.tokens;
-    if (!live) token = 0;
-    const int chunk = (int)(item % (uint32_t)chunks);
+    const LanePlace at = lane_place<INTERLEAVED>(threadIdx.x % kLanes, p.rot);
+    const uint32_t chunks = p.chunks_q + (KV ? 2 : 1) * p.chunks_k;
+    // The host bounds the items by 2^31.
+    const uint32_t item = blockIdx.x * kGroups + threadIdx.x / kLanes;
+    // Groups past the end do the first token's work once more, for the
+    // shuffles, and write nothing.
+    bool live = item < (uint32_t)p.tokens * chunks;
+    const long long token = live ? item / chunks : 0;
+    const int chunk = live ? (int)(item % chunks) : 0;
     const int what = chunk < p.chunks_q ? 0 : chunk < p.chunks_q + p.chunks_k ? 1 : 2;  // Q, K, V
     const int h0 = U * (chunk - (what == 0 ? 0 : what == 1 ? p.chunks_q : p.chunks_q + p.chunks_k));
     const int heads = min(U, (what == 0 ? p.Hq : p.Hkv) - h0);
-    long long slot = 0;
-    if (KV && live) {
-        slot = __ldg(p.slots + token);
-        if (slot >= p.num_slots) atomicCAS(p.status, 0, kStatusRange);
-        live = slot >= 0 && slot < p.num_slots;
-    }
-    const __nv_bfloat16 *src = what == 0   ? p.q + token * p.q_stride
-                               : what == 1 ? p.k + token * p.k_stride
-                                           : p.v + token * p.v_stride;
-    uint4 raw[U];
+    const __nv_bfloat16 *src = (what == 0   ? p.q + token * p.q_stride
+                                : what == 1 ? p.k + token * p.k_stride
+                                            : p.v + token * p.v_stride) +
+                               (size_t)h0 * D;
+    const int pos = __ldg(p.positions + token);
+    const int slot = KV ? __ldg(p.slots + token) : 0;
+    Raw8 raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        raw[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (live && u < heads) raw[u] = load16(src + (h0 + u) * D + d);
+    for (int u = 0; u < U; ++u) raw[u] = load_raw(src + (u < heads ? u : 0) * D, at);
+    if (KV) {
+        // Padding tokens write nothing; a slot behind the cache is reported.
+        if (live && slot >= p.num_slots) atomicCAS(p.status, 0, kStatusRange);
+        live = live && slot >= 0 && slot < p.num_slots;
     }
-    Angles ang;
-    ang.turn = false;
-    Lane8 w{};
-    if (live && what != 2) {
-        ang = load_angles(p, token_position(p, token), d);
-        w = load_weights(what == 0 ? p.qw : p.kw, p.w_fp32, d);
+    // y_p = r (x_p wc_p - x_q ws_q),  y_q = r (x_q wc_q + x_p ws_p)
+    Pairs wc, ws;
+    {
+        float c[4], s[4];
+        const bool angles = live && what != 2;
+        Pairs w{};
+        if (angles) {
+            w = load_weights<INTERLEAVED>(what == 0 ? p.qw : p.kw, p.w_fp32, at);
+            load_angles(c, s, p, pos, at);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[e] = s[e] = 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            wc.p[e] = w.p[e] * c[e];
+            wc.q[e] = w.q[e] * c[e];
+            ws.p[e] = w.p[e] * s[e];
+            ws.q[e] = -w.q[e] * s[e];
+        }
     }
     float r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const Lane8 x = unpack8(raw[u]);
-        float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) s0 += x.v[e] * x.v[e], s1 += x.v[e + 1] * x.v[e + 1];
-        r[u] = rsqrtf(head_sum<D>(s0 + s1) * (1.0f / D) + p.eps);
+        const Pairs x = unpack8<INTERLEAVED>(raw[u]);
+        r[u] = rsqrtf(head_sum<D>(lane_dot(x, x)) * (1.0f / D) + p.eps);
     }
+    if (!live) return;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const Lane8 x = unpack8(raw[u]);
-        Lane8 y;
+        if (u >= heads) break;
+        const Pairs x = unpack8<INTERLEAVED>(raw[u]);
+        Pairs y;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y.v[e] = x.v[e] * r[u] * w.v[e];
-        y = rotate8(p, y, ang, d, 1.0f);
-        if (!live || u >= heads) continue;
-        const int at = (h0 + u) * D + d;
+        for (int e = 0; e < 4; e += 2) {
+            mul2(y.p[e], y.p[e + 1], x.q[e], x.q[e + 1], ws.q[e], ws.q[e + 1]);
+            fma2(y.p[e], y.p[e + 1], x.p[e], x.p[e + 1], wc.p[e], wc.p[e + 1], y.p[e], y.p[e + 1]);
+            mul2(y.p[e], y.p[e + 1], y.p[e], y.p[e + 1], r[u], r[u]);
+            mul2(y.q[e], y.q[e + 1], x.p[e], x.p[e + 1], ws.p[e], ws.p[e + 1]);
+            fma2(y.q[e], y.q[e + 1], x.q[e], x.q[e + 1], wc.q[e], wc.q[e + 1], y.q[e], y.q[e + 1]);
+            mul2(y.q[e], y.q[e + 1], y.q[e], y.q[e + 1], r[u], r[u]);
+        }
+        const size_t head = (size_t)(h0 + u) * D;
         if (KV == 0 || what == 0) {
-            __nv_bfloat16 *dst = what == 0 ? p.q_out + token * p.q_out_stride : p.k_out + token * p.k_out_stride;
-            *reinterpret_cast<uint4 *>(dst + at) = pack8(y);
+            store_bf16<INTERLEAVED>((what == 0 ? p.q_out + token * p.q_out_stride
+                                               : p.k_out + token * p.k_out_stride) + head, at, y);
         } else {
-            const size_t off = (size_t)slot * p.Hkv * D + at;
-            void *cache = what == 1 ? p.k_cache : p.v_cache;
-            if (KV == 1)
-                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(cache) + off) =
-                    what == 1 ? pack8(y) : raw[u];
-            else
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(cache) + off) =
-                    what == 1 ? codes8(y, p.k_descale) : codes8(x, p.v_descale);
+            const size_t off = (size_t)slot * p.Hkv * D + head;
+            if (KV == 1) {
+                __nv_bfloat16 *row = static_cast<__nv_bfloat16 *>(what == 1 ? p.k_cache : p.v_cache) + off;
+                if (what == 1) {
+                    store_bf16<INTERLEAVED>(row, at, y);
+                } else {
+                    *reinterpret_cast<uint2 *>(row + at.a) = raw[u].a;
+                    *reinterpret_cast<uint2 *>(row + at.b) = raw[u].b;
+                }
+            } else {
+                uint8_t *row = static_cast<uint8_t *>(what == 1 ? p.k_cache : p.v_cache) + off;
+                store_e4m3<INTERLEAVED>(row, at, what == 1 ? y : x, what == 1 ? p.k_scale : p.v_scale);
+            }
         }
     }
 }
 
 // ----------------------------------------------------------------- backward
 
-// A fixed number of blocks walks over the items, so that each block's share
-// of dw stays in registers until its end and the sum of the blocks' shares
-// (norm_rope_dw_kernel, in the blocks' order) does not depend on the timing.
-constexpr int kNormBwdRows = 2;
+// A fixed number of blocks walks over the items, first Q's, then K's, so that
+// each block's share of dw stays in registers until its end, and the sum of
+// the blocks' shares (norm_rope_dw_kernel, in the blocks' order) does not
+// depend on the timing.
+constexpr int kNormBwdRows = 4;
 
-template <int D>
-__global__ void __launch_bounds__(kNormThreads)
-norm_rope_bwd_kernel(const NormRopeParams p) {
-    constexpr int kLanes = D / 8, kGroups = kNormThreads / kLanes, U = kNormBwdRows;
-    __shared__ float share[kGroups][D];
-    const int group = threadIdx.x / kLanes;
-    const int d = (threadIdx.x % kLanes) * 8;
-    const int chunks = p.chunks_q + p.chunks_k;
-    const uint32_t items = (uint32_t)(p.tokens * chunks);  // below 2^31
-    const Lane8 wq = load_weights(p.qw, p.w_fp32, d), wk = load_weights(p.kw, p.w_fp32, d);
-    Lane8 dwq{}, dwk{};
+template <int D, bool INTERLEAVED>
+__device__ __forceinline__ Pairs norm_rope_bwd_side(const NormRopeParams &p, const LanePlace &at,
+                                                    bool is_q, uint32_t first_block) {
+    constexpr int kGroups = kNormThreads / (D / 8), U = kNormBwdRows;
+    const uint32_t chunks = is_q ? p.chunks_q : p.chunks_k;
+    const int H = is_q ? p.Hq : p.Hkv;
+    const uint32_t items = (uint32_t)p.tokens * chunks;  // below 2^31
+    const __nv_bfloat16 *x_base = is_q ? p.q : p.k;
+    __nv_bfloat16 *dx_base = is_q ? p.q_out : p.k_out;
+    const long long x_stride = is_q ? p.q_stride : p.k_stride;
+    const long long dx_stride = is_q ? p.q_out_stride : p.k_out_stride;
+    const long long dy_stride = is_q ? p.dq_stride : p.dk_stride;
+    const void *dy_base = is_q ? p.dq : p.dk;
+    const int fp32 = is_q ? p.dq_fp32 : p.dk_fp32;
+    const Pairs w = load_weights<INTERLEAVED>(is_q ? p.qw : p.kw, p.w_fp32, at);
+    Pairs dw{};
     // Whole warps loop together, as the shuffles need.
-    for (uint32_t base = blockIdx.x * kGroups; base < items; base += gridDim.x * kGroups) {
-        const bool live = base + group < items;
-        const uint32_t item = live ? base + group : 0;
-        const long long token = item / (uint32_t)chunks;
-        const int chunk = (int)(item % (uint32_t)chunks);
-        const bool is_q = chunk < p.chunks_q;
-        const int h0 = U * (is_q ? chunk : chunk - p.chunks_q);
-        const int heads = live ? min(U, (is_q ? p.Hq : p.Hkv) - h0) : 0;
-        const __nv_bfloat16 *src = is_q ? p.q + token * p.q_stride : p.k + token * p.k_stride;
-        const int fp32 = is_q ? p.dq_fp32 : p.dk_fp32;
-        const void *dy = is_q ? p.dq : p.dk;
-        const long long dy_at = token * (is_q ? p.dq_stride : p.dk_stride);
-        uint4 raw[U];
-        Lane8 g[U];
+    for (uint32_t base = first_block * kGroups; base < items; base += gridDim.x * kGroups) {
+        const uint32_t mine = base + threadIdx.x / (D / 8);
+        const bool live = mine < items;
+        const uint32_t item = live ? mine : 0;
+        const long long token = item / chunks;
+        const int h0 = U * (int)(item % chunks);
+        const int heads = live ? min(U, H - h0) : 0;
+        const int pos = __ldg(p.positions + token);
+        const __nv_bfloat16 *src = x_base + token * x_stride + (size_t)h0 * D;
+        const long long dy_at = token * dy_stride + (long long)h0 * D;
+        Raw8 raw[U];
+        float ga[U][4], gb[U][4];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            raw[u] = make_uint4(0u, 0u, 0u, 0u);
-            g[u] = Lane8{};
-            if (u < heads) {
-                const long long at = dy_at + (h0 + u) * D + d;
-                raw[u] = load16(src + (h0 + u) * D + d);
-                if (fp32) g[u] = load8_f32(static_cast<const float *>(dy) + at);
-                else g[u] = unpack8(ld_nc_v4(static_cast<const __nv_bfloat16 *>(dy) + at));
+            // A row that is not there is read as the chunk's first, and adds nothing.
+            const int row = u < heads ? u * D : 0;
+            raw[u] = load_raw(src + row, at);
+            if (fp32) {
+                const float *dy = static_cast<const float *>(dy_base) + dy_at + row;
+                load4_f32(ga[u], dy + at.a);
+                load4_f32(gb[u], dy + at.b);
+            } else {
+                const __nv_bfloat16 *dy = static_cast<const __nv_bfloat16 *>(dy_base) + dy_at + row;
+                unpack4(ga[u], __ldg(reinterpret_cast<const uint2 *>(dy + at.a)));
+                unpack4(gb[u], __ldg(reinterpret_cast<const uint2 *>(dy + at.b)));
             }
         }
-        Angles ang;
-        ang.turn = false;
-        if (live) ang = load_angles(p, token_position(p, token), d);
-        __nv_bfloat16 *dst = is_q ? p.q_out + token * p.q_out_stride : p.k_out + token * p.k_out_stride;
+        float c[4], s[4];
+        load_angles(c, s, p, pos, at);
+        __nv_bfloat16 *dst = dx_base + token * dx_stride + (size_t)h0 * D;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const Lane8 x = unpack8(raw[u]);
-            g[u] = rotate8(p, g[u], ang, d, -1.0f);
-            float ss = 0.0f, hx = 0.0f;
+            const Pairs x = unpack8<INTERLEAVED>(raw[u]);
+            const Pairs dy = make_pairs<INTERLEAVED>(ga[u], gb[u]);
+            Pairs g, gx;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                ss += x.v[e] * x.v[e];
-                hx += (is_q ? wq.v[e] : wk.v[e]) * g[u].v[e] * x.v[e];
+            for (int e = 0; e < 4; e += 2) {
+                mul2(g.p[e], g.p[e + 1], dy.q[e], dy.q[e + 1], s[e], s[e + 1]);
+                fma2(g.p[e], g.p[e + 1], dy.p[e], dy.p[e + 1], c[e], c[e + 1], g.p[e], g.p[e + 1]);
+                mul2(g.q[e], g.q[e + 1], dy.p[e], dy.p[e + 1], -s[e], -s[e + 1]);
+                fma2(g.q[e], g.q[e + 1], dy.q[e], dy.q[e + 1], c[e], c[e + 1], g.q[e], g.q[e + 1]);
+                mul2(gx.p[e], gx.p[e + 1], g.p[e], g.p[e + 1], x.p[e], x.p[e + 1]);
+                mul2(gx.q[e], gx.q[e + 1], g.q[e], g.q[e + 1], x.q[e], x.q[e + 1]);
             }
-            const float r = rsqrtf(head_sum<D>(ss) * (1.0f / D) + p.eps);
-            const float t = head_sum<D>(hx) * (1.0f / D) * r * r;
+            const float r = rsqrtf(head_sum<D>(lane_dot(x, x)) * (1.0f / D) + p.eps);
+            const float t = -(r * r * r) * (head_sum<D>(lane_dot(w, gx)) * (1.0f / D));
             if (u >= heads) continue;
-            Lane8 dx;
+            Pairs dx;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float gx = g[u].v[e] * (x.v[e] * r);
-                if (is_q) dwq.v[e] += gx;
-                else dwk.v[e] += gx;
-                dx.v[e] = r * ((is_q ? wq.v[e] : wk.v[e]) * g[u].v[e] - x.v[e] * t);
+            for (int e = 0; e < 4; e += 2) {
+                fma2(dw.p[e], dw.p[e + 1], gx.p[e], gx.p[e + 1], r, r, dw.p[e], dw.p[e + 1]);
+                fma2(dw.q[e], dw.q[e + 1], gx.q[e], gx.q[e + 1], r, r, dw.q[e], dw.q[e + 1]);
+                mul2(g.p[e], g.p[e + 1], g.p[e], g.p[e + 1], w.p[e], w.p[e + 1]);
+                mul2(g.q[e], g.q[e + 1], g.q[e], g.q[e + 1], w.q[e], w.q[e + 1]);
+                mul2(dx.p[e], dx.p[e + 1], x.p[e], x.p[e + 1], t, t);
+                mul2(dx.q[e], dx.q[e + 1], x.q[e], x.q[e + 1], t, t);
+                fma2(dx.p[e], dx.p[e + 1], g.p[e], g.p[e + 1], r, r, dx.p[e], dx.p[e + 1]);
+                fma2(dx.q[e], dx.q[e + 1], g.q[e], g.q[e + 1], r, r, dx.q[e], dx.q[e + 1]);
             }
-            *reinterpret_cast<uint4 *>(dst + (h0 + u) * D + d) = pack8(dx);
+            store_bf16<INTERLEAVED>(dst + u * D, at, dx);
         }
     }
-    // This block's share: the groups' sums in their order.
-#pragma unroll
+    return dw;
+}
+
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kNormThreads, 2)
+norm_rope_bwd_kernel(const NormRopeParams p) {
+    constexpr int kLanes = D / 8, kGroups = kNormThreads / kLanes;
+    __shared__ float share[kGroups][D];
+    launch_dependents();  // the sum of the shares: its blocks wait for this grid's end
+    const int group = threadIdx.x / kLanes;
+    const LanePlace at = lane_place<INTERLEAVED>(threadIdx.x % kLanes, p.rot);
+#pragma unroll 1
     for (int which = 0; which < 2; ++which) {
+        // K's items start at the other end of the grid: the blocks that had one
+        // more of Q's have one fewer.
+        const Pairs dw = norm_rope_bwd_side<D, INTERLEAVED>(
+            p, at, which == 0, which == 0 ? blockIdx.x : gridDim.x - 1 - blockIdx.x);
+        // This block's share: the groups' sums in their order.
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) share[group][d + e] = which ? dwk.v[e] : dwq.v[e];
+        for (int e = 0; e < 4; ++e) {
+            share[group][INTERLEAVED ? at.a + 2 * e : at.a + e] = dw.p[e];
+            share[group][INTERLEAVED ? at.a + 2 * e + 1 : at.b + e] = dw.q[e];
+        }
         __syncthreads();
         for (int i = threadIdx.x; i < D; i += kNormThreads) {
             float sum = 0.0f;
@@ -335,22 +422,23 @@ norm_rope_bwd_kernel(const NormRopeParams p) {
     }
 }
 
-// dw[i] = sum over blocks of partial[block][i], i < 2 D: 32 columns per
-// block, 32 rows of threads that take every 32nd partial, then their sums in
-// order.
-__global__ void __launch_bounds__(1024)
+// dw[i] = sum over blocks of partial[block][i], i < 2 D: 16 columns per block,
+// 64 rows of threads that take every 64th partial, then their sums in order.
+constexpr int kDwRows = 64, kDwCols = 16;
+__global__ void __launch_bounds__(kDwRows * kDwCols)
 norm_rope_dw_kernel(const float *partial, int blocks, int D, float *dqw, float *dkw) {
-    __shared__ float share[32][33];
-    const int i = blockIdx.x * 32 + threadIdx.x;
+    __shared__ float share[kDwRows][kDwCols + 1];
+    wait_for_primary();
+    const int i = blockIdx.x * kDwCols + threadIdx.x;
     float sum = 0.0f;
-#pragma unroll 4
-    for (int b = threadIdx.y; b < blocks; b += 32) sum += partial[(size_t)b * 2 * D + i];
+#pragma unroll 8
+    for (int b = threadIdx.y; b < blocks; b += kDwRows) sum += partial[(size_t)b * 2 * D + i];
     share[threadIdx.y][threadIdx.x] = sum;
     __syncthreads();
     if (threadIdx.y == 0) {
         sum = 0.0f;
 #pragma unroll
-        for (int r = 0; r < 32; ++r) sum += share[r][threadIdx.x];
+        for (int r = 0; r < kDwRows; ++r) sum += share[r][threadIdx.x];
         (i < D ? dqw[i] : dkw[i - D]) = sum;
     }
 }

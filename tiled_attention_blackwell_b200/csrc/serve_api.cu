@@ -57,8 +57,8 @@ attn_status_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 threads,
 
 // Blocks of the backward, per SM: each leaves one share of dw.  A fixed
 // bound, so that the workspace's size needs no device.
-constexpr int kNormBwdMaxBlocks = 1184;
-constexpr int kNormBwdBlocksPerSm = 4;
+constexpr int kNormBwdMaxBlocks = 296;
+constexpr int kNormBwdBlocksPerSm = 2;  // as many as are resident
 
 // A bf16 (or wider) [tokens][H][D] argument: a pointer and the distance of
 // its tokens.
@@ -95,14 +95,34 @@ attn_status_t check_norm(const void *qw, const void *kw, int w_fp32, const float
 
 int chunks_of(int heads, int per) { return (heads + per - 1) / per; }
 
-template <int KV>
+template <int KV, bool INTERLEAVED>
 attn_status_t launch_norm(const tab::NormRopeParams &p, int D, cudaStream_t stream) {
     const long long items = p.tokens * (p.chunks_q + (KV ? 2 : 1) * p.chunks_k);
     const int groups = tab::kNormThreads / (D / 8);
     const unsigned grid = (unsigned)((items + groups - 1) / groups);
-    if (D == 128) tab::norm_rope_kernel<128, KV><<<grid, tab::kNormThreads, 0, stream>>>(p);
-    else tab::norm_rope_kernel<64, KV><<<grid, tab::kNormThreads, 0, stream>>>(p);
+    if (D == 128) tab::norm_rope_kernel<128, KV, INTERLEAVED><<<grid, tab::kNormThreads, 0, stream>>>(p);
+    else tab::norm_rope_kernel<64, KV, INTERLEAVED><<<grid, tab::kNormThreads, 0, stream>>>(p);
     return launch_result();
+}
+
+template <int KV>
+attn_status_t dispatch_norm(const tab::NormRopeParams &p, int D, int interleaved, cudaStream_t stream) {
+    return interleaved ? launch_norm<KV, true>(p, D, stream) : launch_norm<KV, false>(p, D, stream);
+}
+
+template <int D, bool INTERLEAVED>
+attn_status_t launch_norm_bwd(const tab::NormRopeParams &p, int num_sms, float *dqw, float *dkw,
+                              cudaStream_t stream) {
+    const int groups = tab::kNormThreads / (D / 8);
+    const long long items = p.tokens * std::max(p.chunks_q, p.chunks_k);
+    const int blocks = (int)std::min<long long>(
+        (items + groups - 1) / groups, std::min(kNormBwdMaxBlocks, kNormBwdBlocksPerSm * num_sms));
+    tab::norm_rope_bwd_kernel<D, INTERLEAVED><<<blocks, tab::kNormThreads, 0, stream>>>(p);
+    const attn_status_t s = launch_result();
+    if (s != ATTN_OK) return s;
+    return launch_dependent(tab::norm_rope_dw_kernel, dim3(2 * D / tab::kDwCols),
+                            dim3(tab::kDwCols, tab::kDwRows), stream,
+                            static_cast<const float *>(p.partial), blocks, D, dqw, dkw);
 }
 
 // ------------------------------------------------------------------ decode
@@ -251,9 +271,8 @@ attn_status_t attn_qk_norm_rope(const void *q, const void *k, void *q_out, void 
     p.max_positions = max_positions;
     p.chunks_q = cq;
     p.chunks_k = ck;
-    p.interleaved = interleaved;
     p.eps = eps;
-    return launch_norm<0>(p, D, static_cast<cudaStream_t>(stream));
+    return dispatch_norm<0>(p, D, interleaved, static_cast<cudaStream_t>(stream));
 }
 
 attn_status_t attn_qk_norm_rope_cache(const void *q, const void *k, const void *v, void *q_out,
@@ -282,9 +301,10 @@ attn_status_t attn_qk_norm_rope_cache(const void *q, const void *k, const void *
     if (kv_dtype != ATTN_KV_BF16 && kv_dtype != ATTN_KV_E4M3)
         return fail(ATTN_ERR_INVALID_ARG, "kv_dtype must be ATTN_KV_BF16 or ATTN_KV_E4M3");
     for (float d : {k_descale, v_descale})
-        if (!(d > 0.0f) || !std::isfinite(d) || (kv_dtype == ATTN_KV_BF16 && d != 1.0f))
+        if (!(d > 0.0f) || !std::isfinite(d) || !std::isfinite(1.0f / d) ||
+            (kv_dtype == ATTN_KV_BF16 && d != 1.0f))
             return fail(ATTN_ERR_INVALID_ARG,
-                        "descale factors must be > 0 and finite, and 1 for a bf16 cache");
+                        "descale factors and their reciprocals must be > 0 and finite, and 1 for a bf16 cache");
     DeviceState *st = nullptr;
     if ((s = device_state(&st)) != ATTN_OK) return s;
     tab::NormRopeParams p;
@@ -311,16 +331,16 @@ attn_status_t attn_qk_norm_rope_cache(const void *q, const void *k, const void *
     p.max_positions = max_positions;
     p.chunks_q = cq;
     p.chunks_k = ck;
-    p.interleaved = interleaved;
     p.eps = eps;
     p.slots = slots;
     p.k_cache = k_cache;
     p.v_cache = v_cache;
     p.num_slots = num_slots;
-    p.k_descale = k_descale;
-    p.v_descale = v_descale;
+    p.k_scale = 1.0f / k_descale;
+    p.v_scale = 1.0f / v_descale;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    return kv_dtype == ATTN_KV_E4M3 ? launch_norm<2>(p, D, cs) : launch_norm<1>(p, D, cs);
+    return kv_dtype == ATTN_KV_E4M3 ? dispatch_norm<2>(p, D, interleaved, cs)
+                                    : dispatch_norm<1>(p, D, interleaved, cs);
 }
 
 size_t attn_qk_norm_rope_bwd_workspace_size(int D) {
@@ -383,7 +403,6 @@ attn_status_t attn_qk_norm_rope_bwd(const void *dq, const void *dk, int dq_fp32,
     p.max_positions = max_positions;
     p.chunks_q = cq;
     p.chunks_k = ck;
-    p.interleaved = interleaved;
     p.eps = eps;
     p.dq = dq;
     p.dk = dk;
@@ -393,15 +412,11 @@ attn_status_t attn_qk_norm_rope_bwd(const void *dq, const void *dk, int dq_fp32,
     p.dk_fp32 = dk_fp32;
     p.partial = static_cast<float *>(workspace);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const int groups = tab::kNormThreads / (D / 8);
-    const long long items = tokens * (cq + ck);
-    const int blocks = (int)std::min<long long>(
-        (items + groups - 1) / groups, std::min(kNormBwdMaxBlocks, kNormBwdBlocksPerSm * st->num_sms));
-    if (D == 128) tab::norm_rope_bwd_kernel<128><<<blocks, tab::kNormThreads, 0, cs>>>(p);
-    else tab::norm_rope_bwd_kernel<64><<<blocks, tab::kNormThreads, 0, cs>>>(p);
-    if ((s = launch_result()) != ATTN_OK) return s;
-    tab::norm_rope_dw_kernel<<<2 * D / 32, dim3(32, 32), 0, cs>>>(p.partial, blocks, D, dq_weight, dk_weight);
-    return launch_result();
+    if (D == 128)
+        return interleaved ? launch_norm_bwd<128, true>(p, st->num_sms, dq_weight, dk_weight, cs)
+                           : launch_norm_bwd<128, false>(p, st->num_sms, dq_weight, dk_weight, cs);
+    return interleaved ? launch_norm_bwd<64, true>(p, st->num_sms, dq_weight, dk_weight, cs)
+                       : launch_norm_bwd<64, false>(p, st->num_sms, dq_weight, dk_weight, cs);
 }
 
 size_t attn_decode_paged_workspace_size(int D) { return D < 1 ? 0 : decode_layout(D).total; }
