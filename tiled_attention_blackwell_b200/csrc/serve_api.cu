@@ -57,8 +57,8 @@ attn_status_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 threads,
 
 // Blocks of the backward, per SM: each leaves one share of dw.  A fixed
 // bound, so that the workspace's size needs no device.
-constexpr int kNormBwdMaxBlocks = 296;
-constexpr int kNormBwdBlocksPerSm = 2;  // as many as are resident
+constexpr int kNormBwdMaxBlocks = 592;
+constexpr int kNormBwdBlocksPerSm = 4;  // as many as are resident
 
 // A bf16 (or wider) [tokens][H][D] argument: a pointer and the distance of
 // its tokens.
