@@ -224,6 +224,34 @@ __device__ __forceinline__ void exp_pack_half(const float *s, float c, float neg
     sum_pv += r0s + r1s;
 }
 
+// The same for 32 scores of a masked block, all on MUFU: ex2(-inf) = 0 exactly.
+__device__ __forceinline__ void exp_pack_group(const float *s, float c, float neg_m, uint32_t *pk,
+                                               float &sum, float &sum_pv) {
+    float sum0 = 0.0f, sum1 = 0.0f, r0s = 0.0f, r1s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        float x0, x1;
+        fma2(x0, x1, s[e], s[e + 1], c, c, neg_m, neg_m);
+        const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
+        add2(sum0, sum1, sum0, sum1, p0, p1);
+        const uint32_t h = pack_bf16x2(p0, p1);
+        pk[e >> 1] = h;
+        add_bf16x2_f32(r0s, r1s, h);
+    }
+    sum += sum0 + sum1;
+    sum_pv += r0s + r1s;
+}
+
+// Bit e: a row whose interval is [lo, hi] and whose first `sinks` keys (up to
+// hi) are visible too sees key `key0 + e`.
+__device__ __forceinline__ uint32_t visible_bits(int key0, int lo, int hi, int sinks) {
+    const int h = hi - key0, l = lo - key0, f = sinks - key0;
+    const uint32_t upto_hi = h >= 31 ? ~0u : h < 0 ? 0u : (2u << h) - 1u;
+    const uint32_t from_lo = l <= 0 ? ~0u : l > 31 ? 0u : ~0u << l;
+    const uint32_t first = f >= 32 ? ~0u : f <= 0 ? 0u : (1u << f) - 1u;
+    return upto_hi & (from_lo | first);
+}
+
 // The same for 8-bit P: 64 probabilities of a row to e4m3, four per word.
 template <int EXP_MODE>
 __device__ __forceinline__ float exp_pack_half_fp8(const float *s, float c, float neg_m,
@@ -661,7 +689,8 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_tmem = tmem + lane_base + i * kBlockN;
         const uint32_t o_tmem = tmem + lane_base + 2 * kBlockN + i * D;
-        KeyRange kr = row_key_range(p, row);
+        // SINKS: rows behind the last see what it sees (their results go nowhere).
+        KeyRange kr = row_key_range(p, SINKS ? min(row, p.Sq - 1) : row);
         if (SINKS && kr.lo > kr.hi) kr.hi = -1;  // no key, so no first key either
         const int lo_b = i == 0 ? lo0 : lo1;
         const int hi_b = i == 0 ? hi0 : hi1;
@@ -715,6 +744,7 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
             float alpha = 1.0f;
             float neg_m;
             float bm[4];  // Direct-P: maxima of the four 32-key blocks
+            uint32_t unseen = 0u;  // SINKS, masked blocks: groups of 32 keys that no row sees
             if constexpr (DP) {
                 // Direct-P: the anchor m is the running max rounded up to an
                 // integer, so every rescale is an exact power of two and the
@@ -738,12 +768,36 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                 neg_m = m_run == -INFINITY ? 0.0f : p.p_offset - m_run;
                 if ((warp & 3) == 0) ATTN_TRACE_EVENT(i, t, 3);
             } else {
+            float row_max;
+            if (SINKS && masked) {
+                // By groups of 32 keys: one that no row of the warp sees is left out
+                // here and below, one that all see needs no mask.
+                row_max = -INFINITY;
+                unseen = 0u;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const uint32_t bits = visible_bits(key0 + 32 * g, kr.lo, kr.hi, p.sinks);
+                    if (!__any_sync(0xffffffffu, bits != 0u)) {
+                        unseen |= 1u << g;
+                        continue;
+                    }
+                    if (MOD)
+                        modify_scores<MOD, 32>(s + 32 * g, c, k1, p.softcap_out, slope2,
+                                               dist0 - (float)(32 * g));
+                    if (!__all_sync(0xffffffffu, bits == ~0u)) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((bits >> e) & 1u)) s[32 * g + e] = -INFINITY;
+                    }
+                    row_max = fmaxf(row_max, block_max32(s + 32 * g));
+                }
+            } else {
             if (MOD) modify_scores<MOD, kBlockN / 2>(s, c, k1, p.softcap_out, slope2, dist0);
             if (masked) {
 #pragma unroll
                 for (int e = 0; e < kBlockN / 2; ++e) {
                     const int key = key0 + e;
-                    if ((key < kr.lo && (!SINKS || key >= p.sinks)) || key > kr.hi) s[e] = -INFINITY;
+                    if (key < kr.lo || key > kr.hi) s[e] = -INFINITY;
                 }
             }
             float mx[4];
@@ -762,7 +816,7 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
 #pragma unroll
                 for (int e = kBlockN / 2; e < kBlockN; ++e) {
                     const int key = key0 + e;
-                    if ((key < kr.lo && (!SINKS || key >= p.sinks)) || key > kr.hi) s[e] = -INFINITY;
+                    if (key < kr.lo || key > kr.hi) s[e] = -INFINITY;
                 }
             }
 #pragma unroll
@@ -770,7 +824,8 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
 #pragma unroll
                 for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], s[e + u], s[e + 4 + u]);
             if ((warp & 3) == 0) ATTN_TRACE_EVENT(i, t, 2);
-            const float row_max = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+            row_max = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+            }
             const float m_cand = MOD ? row_max : row_max * c;
             ATTN_COUNT_BLOCK(t, m_cand > m_run, m_cand > m_run + tau);
             if (m_cand > m_run + tau) {
@@ -818,6 +873,17 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
             // this warp computes keys [64, 128).  Masked blocks (-inf scores)
             // use MUFU only: ex2(-inf) = 0 exactly.
             uint32_t pk[kBlockN / 2];
+            auto exp_groups = [&](int g0) {  // SINKS, masked: groups g0 and g0 + 1
+#pragma unroll
+                for (int g = g0; g < g0 + 2; ++g) {
+                    if ((unseen >> g) & 1u) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[16 * g + e] = 0u;
+                    } else {
+                        exp_pack_group(s + 32 * g, c_exp, neg_m, pk + 16 * g, l_run, l_pv);
+                    }
+                }
+            };
             if (MOD) __syncwarp();  // converged before the warp-collective TMEM store
             if constexpr (DP) {
                 l_run += direct_p_half<PREC>(s, bm, c, neg_m, pk);
@@ -829,8 +895,10 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                                 : exp_pack_half_fp8<EXP_MODE>(s, c_exp, neg_m, pk);
                 tmem_st16(s_tmem + 0, pk + 0);
             } else {
-                if (masked) exp_pack_half<0>(s, c_exp, neg_m, pk, l_run, l_pv);
+                if (SINKS && masked) exp_groups(0);
+                else if (masked) exp_pack_half<0>(s, c_exp, neg_m, pk, l_run, l_pv);
                 else exp_pack_half<EXP_MODE>(s, c_exp, neg_m, pk, l_run, l_pv);
+                if (SINKS) __syncwarp();
                 tmem_st32(s_tmem + 0, pk + 0);
             }
             tmem_wait_st();
@@ -847,9 +915,11 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                 if ((warp & 3) == 0) ATTN_TRACE_EVENT(i, t, 4);
                 tmem_st16(s_tmem + 16, pk + 16);
             } else {
-                if (masked) exp_pack_half<0>(s + 64, c_exp, neg_m, pk + 32, l_run, l_pv);
+                if (SINKS && masked) exp_groups(2);
+                else if (masked) exp_pack_half<0>(s + 64, c_exp, neg_m, pk + 32, l_run, l_pv);
                 else exp_pack_half<EXP_MODE>(s + 64, c_exp, neg_m, pk + 32, l_run, l_pv);
                 if ((warp & 3) == 0) ATTN_TRACE_EVENT(i, t, 4);
+                if (SINKS) __syncwarp();
                 tmem_st32(s_tmem + 32, pk + 32);
             }
             tmem_wait_st();
