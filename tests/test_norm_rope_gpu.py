@@ -106,6 +106,34 @@ def test_in_place_batched_and_bit_identical_again():
     assert torch.equal(rest, k.as_strided((60, 2, 128), k.stride(), k.storage_offset() + 2 * 128))
 
 
+def test_views_that_are_taken_and_refused():
+    qkv = torch.randn(2, 5, 8 * 64, device=DEV).to(torch.bfloat16)
+    qw = kw = torch.ones(64, device=DEV)
+    cos, sin = attn.rope_table(8, 64, device=DEV)
+    pos = torch.arange(5, dtype=torch.int32, device=DEV).repeat(2, 1)
+    q, k = qkv[..., :256].unflatten(-1, (4, 64)), qkv[..., 256:384].unflatten(-1, (2, 64))
+    want = attn.qk_norm_rope(q.contiguous(), k.contiguous(), qw, kw, cos, sin, pos)
+
+    def same(got, rows):
+        assert all(torch.equal(a, b[rows]) for a, b in zip(got, want))
+
+    everything = (slice(None), slice(None))
+    same(attn.qk_norm_rope(q, k, qw, kw, cos, sin, pos), everything)
+    # one token of each row, one token at all, one head, one key head of several
+    same(attn.qk_norm_rope(q[:, 2:3], k[:, 2:3], qw, kw, cos, sin, pos[:, 2:3].contiguous()), (slice(None), slice(2, 3)))
+    same(attn.qk_norm_rope(q[1:, 2:3], k[1:, 2:3], qw, kw, cos, sin, pos[1:, 2:3].contiguous()), (slice(1, 2), slice(2, 3)))
+    got = attn.qk_norm_rope(q[..., 3:, :], k[..., :1, :], qw, kw, cos, sin, pos)
+    assert torch.equal(got[0], want[0][..., 3:, :]) and torch.equal(got[1], want[1][..., :1, :])
+    for bad in (q[:, :3], q.transpose(0, 1).contiguous().transpose(0, 1)[:, :3], q[..., ::2, :], q[..., ::2]):
+        with pytest.raises((TypeError, attn.AttnError)):
+            attn.qk_norm_rope(bad, k[:, :bad.shape[1]], qw, kw, cos, sin, pos[:, :bad.shape[1]].contiguous())
+    with pytest.raises(attn.AttnError) as e:  # tokens that share one row
+        attn.qk_norm_rope(q[:1, :1].expand(2, 5, 4, 64), k, qw, kw, cos, sin, pos)
+    assert e.value.status == attn.ATTN_ERR_INVALID_ARG
+    with pytest.raises(TypeError, match="q_out"):
+        attn.qk_norm_rope(q, k, qw, kw, cos, sin, pos, q_out=q[:, :, :2])
+
+
 def test_zero_row_and_special_values():
     q, k, _, qw, kw, cos, sin, pos, _, _ = inputs(4, 2, 2, 64, 64, seed=6)
     q = q.contiguous()

@@ -120,71 +120,87 @@ def stand_in(*shape, dtype=torch.bfloat16):
     return torch.zeros(shape, dtype=dtype).as_subclass(_CudaStandIn)
 
 
-def norm_tensors():
-    f32, i32 = torch.float32, torch.int32
-    return dict(q=stand_in(5, 4, 128), k=stand_in(5, 2, 128), q_weight=stand_in(128), k_weight=stand_in(128),
-                cos=stand_in(9, 32, dtype=f32), sin=stand_in(9, 32, dtype=f32), positions=stand_in(5, dtype=i32))
+# The native binding looks at types and shapes before it looks at the device,
+# so CPU tensors reach each of its checks; a call whose tensors are all right
+# ends at the device.
+
+F32, I32, F8 = torch.float32, torch.int32, torch.float8_e4m3fn
+
+
+def cpu(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def norm_tensors(**other):
+    return {**dict(q=cpu(5, 4, 128), k=cpu(5, 2, 128), q_weight=cpu(128), k_weight=cpu(128), cos=cpu(9, 32, dtype=F32),
+                   sin=cpu(9, 32, dtype=F32), positions=cpu(5, dtype=I32)), **other}
+
+
+def norm_calls(t):
+    dq, dk = torch.zeros(t["q"].shape) if torch.is_tensor(t["q"]) else cpu(5, 4, 128), cpu(5, 2, 128)
+    yield lambda **kw: attn.qk_norm_rope(*t.values(), **kw)
+    yield lambda **kw: attn.qk_norm_rope_backward(dq, dk, *t.values(), **kw)
+    yield lambda **kw: attn.qk_norm_rope_cache(t["q"], t["k"], cpu(5, 2, 128), *list(t.values())[2:],
+                                               cpu(5, dtype=I32), cpu(3, 16, 2, 128), cpu(3, 16, 2, 128), **kw)
 
 
 @pytest.mark.parametrize("name,bad", [
-    ("q", lambda: torch.zeros(5, 4, 128, dtype=torch.bfloat16)), ("q", lambda: stand_in(5, 4, 128, dtype=torch.float16)),
-    ("q", lambda: stand_in(4, 128)), ("k", lambda: stand_in(6, 2, 128)), ("k", lambda: stand_in(5, 2, 64)),
-    ("q", lambda: stand_in(5, 128, 4).transpose(1, 2)), ("q", lambda: stand_in(4, 5, 128).transpose(0, 1)),
-    ("q_weight", lambda: stand_in(64)), ("k_weight", lambda: stand_in(128, dtype=torch.float32)),
-    ("cos", lambda: stand_in(8, 32, dtype=torch.float32)), ("sin", lambda: stand_in(9, 32)),
-    ("positions", lambda: stand_in(5, dtype=torch.int64)), ("positions", lambda: stand_in(4, dtype=torch.int32))])
+    ("q", 3), ("q", cpu(5, 4, 128, dtype=torch.float16)), ("q", cpu(4, 128)), ("k", cpu(6, 2, 128)),
+    ("k", cpu(5, 2, 64)), ("k", cpu(1, 5, 2, 128)), ("q_weight", cpu(64)), ("q_weight", cpu(128, dtype=torch.float16)),
+    ("k_weight", cpu(128, dtype=F32)), ("k_weight", cpu(256)[::2]), ("cos", cpu(9, 32)), ("cos", cpu(9, 1, 32, dtype=F32)),
+    ("sin", cpu(8, 32, dtype=F32)), ("sin", cpu(32, 9, dtype=F32).T), ("positions", cpu(5, dtype=torch.int64)),
+    ("positions", cpu(4, dtype=I32)), ("positions", cpu(10, dtype=I32)[::2])])
 def test_norm_binding_refuses(L, name, bad):
+    for call in norm_calls(norm_tensors(**{name: bad})):
+        with pytest.raises(TypeError, match=name):
+            call()
+
+
+def test_bindings_refuse_cpu_tensors(L):
+    for call in norm_calls(norm_tensors()):
+        with pytest.raises(TypeError, match="q must be a CUDA tensor"):
+            call()
+        with pytest.raises(TypeError):
+            call(eps="x")
     t = norm_tensors()
-    t[name] = bad()
-    with pytest.raises(TypeError):
-        attn.qk_norm_rope(*t.values(), stream=0)
-    with pytest.raises(TypeError):
-        attn.qk_norm_rope_backward(stand_in(5, 4, 128), stand_in(5, 2, 128), *t.values(), stream=0)
-    with pytest.raises(TypeError):
-        attn.qk_norm_rope_cache(t["q"], t["k"], stand_in(5, 2, 128), *list(t.values())[2:],
-                                stand_in(5, dtype=torch.int32), stand_in(3, 16, 2, 128), stand_in(3, 16, 2, 128), stream=0)
+    with pytest.raises(TypeError, match="dq must be a bf16 or fp32"):
+        attn.qk_norm_rope_backward(cpu(5, 4, 64), cpu(5, 2, 128), *t.values())
+    with pytest.raises(TypeError, match="dk must be a bf16 or fp32"):
+        attn.qk_norm_rope_backward(cpu(5, 4, 128), cpu(5, 2, 128, dtype=torch.float16), *t.values())
 
 
 @pytest.mark.parametrize("name,bad", [
-    ("v", lambda: stand_in(5, 4, 128)), ("slots", lambda: stand_in(5, dtype=torch.int64)),
-    ("slots", lambda: stand_in(1, 5, dtype=torch.int32)), ("k_cache", lambda: stand_in(3, 16, 2, 128, dtype=torch.float32)),
-    ("k_cache", lambda: stand_in(3, 2, 16, 128).transpose(1, 2)), ("v_cache", lambda: stand_in(3, 16, 4, 128)),
-    ("v_cache", lambda: stand_in(4, 16, 2, 128))])
+    ("v", cpu(5, 4, 128)), ("v", cpu(5, 2, 128, dtype=F32)), ("slots", cpu(5, dtype=torch.int64)),
+    ("slots", cpu(1, 5, dtype=I32)), ("k_cache", cpu(3, 16, 2, 128, dtype=F32)), ("k_cache", cpu(48, 2, 128)),
+    ("k_cache", cpu(3, 2, 16, 128).transpose(1, 2)), ("k_cache", cpu(3, 16, 4, 128)),
+    ("v_cache", cpu(3, 16, 4, 128)), ("v_cache", cpu(4, 16, 2, 128)), ("v_cache", cpu(3, 16, 2, 128, dtype=F8))])
 def test_cache_binding_refuses(L, name, bad):
     t = norm_tensors()
-    extra = dict(v=stand_in(5, 2, 128), slots=stand_in(5, dtype=torch.int32), k_cache=stand_in(3, 16, 2, 128),
-                 v_cache=stand_in(3, 16, 2, 128))
-    extra[name] = bad()
-    with pytest.raises(TypeError):
-        attn.qk_norm_rope_cache(t["q"], t["k"], extra["v"], *list(t.values())[2:], extra["slots"], extra["k_cache"],
-                                extra["v_cache"], stream=0)
-
-
-def test_packed_views_are_taken():
-    qkv = torch.zeros(2, 5, 8 * 64, dtype=torch.bfloat16)
-    q, k = qkv[..., :256].unflatten(-1, (4, 64)), qkv[..., 256:384].unflatten(-1, (2, 64))
-    assert attn._token_stride("q", q, 4, 64, (torch.bfloat16,)) == 512
-    assert attn._token_stride("k", k, 2, 64, (torch.bfloat16,)) == 512
-    assert attn._token_stride("q", q[:, :1], 4, 64, (torch.bfloat16,)) == 5 * 512  # one token a row
-    assert attn._token_stride("q", q[:1, :1], 4, 64, (torch.bfloat16,)) == 256
-    assert attn._token_stride("k", k[..., :1, :], 1, 64, (torch.bfloat16,)) == 512
-    with pytest.raises(TypeError):
-        attn._token_stride("q", q[:, :3], 4, 64, (torch.bfloat16,))
+    x = dict(v=cpu(5, 2, 128), slots=cpu(5, dtype=I32), k_cache=cpu(3, 16, 2, 128), v_cache=cpu(3, 16, 2, 128))
+    x[name] = bad
+    if name == "k_cache" and bad.shape == (3, 16, 4, 128):
+        x["v_cache"] = bad
+    with pytest.raises(TypeError, match=name):
+        attn.qk_norm_rope_cache(t["q"], t["k"], x["v"], *list(t.values())[2:], x["slots"], x["k_cache"], x["v_cache"])
 
 
 @pytest.mark.parametrize("name,bad", [
-    ("q", lambda: stand_in(2, 4, 128, dtype=torch.float16)), ("q", lambda: stand_in(2, 1, 4, 128)),
-    ("page_table", lambda: stand_in(3, 4, dtype=torch.int32)), ("page_table", lambda: stand_in(2, 4, dtype=torch.int64)),
-    ("seq_lens", lambda: torch.zeros(2, dtype=torch.int32)), ("seq_lens", lambda: stand_in(2, 1, dtype=torch.int32)),
-    ("k_cache", lambda: stand_in(8, 16, 2, 64)), ("v_cache", lambda: stand_in(8, 16, 2, 128, dtype=torch.float8_e4m3fn))])
+    ("q", cpu(2, 4, 128, dtype=torch.float16)), ("q", cpu(2, 1, 4, 128)), ("q", cpu(4, 2, 128).transpose(0, 1)),
+    ("page_table", cpu(3, 4, dtype=I32)), ("page_table", cpu(2, 4, dtype=torch.int64)), ("page_table", cpu(8, dtype=I32)),
+    ("seq_lens", cpu(2)), ("seq_lens", cpu(2, 1, dtype=I32)), ("k_cache", cpu(8, 16, 2, 64)),
+    ("v_cache", cpu(8, 16, 2, 128, dtype=F8)), ("k_cache", None)])
 def test_decode_binding_refuses(L, name, bad):
-    i32 = torch.int32
-    t = dict(q=stand_in(2, 4, 128), k_cache=stand_in(8, 16, 2, 128), v_cache=stand_in(8, 16, 2, 128),
-             page_table=stand_in(2, 4, dtype=i32), seq_lens=stand_in(2, dtype=i32))
-    t[name] = bad()
-    with pytest.raises(TypeError):
-        attn.decode_paged(*t.values(), o=stand_in(2, 4, 128), lse=stand_in(2, 4, dtype=torch.float32),
-                          workspace=stand_in(1 << 23, dtype=torch.uint8), stream=0)
+    t = dict(q=cpu(2, 4, 128), k_cache=cpu(8, 16, 2, 128), v_cache=cpu(8, 16, 2, 128), page_table=cpu(2, 4, dtype=I32),
+             seq_lens=cpu(2, dtype=I32))
+    with pytest.raises(TypeError, match="q must be a CUDA tensor"):
+        attn.decode_paged(*t.values())
+    t[name] = bad
+    if name == "k_cache" and bad is not None:
+        t["v_cache"] = bad
+    with pytest.raises(TypeError, match=name):
+        attn.decode_paged(*t.values())
+    with pytest.raises(ValueError):
+        attn.decode_paged(cpu(2, 4, 128), *list(t.values())[1:], window=(3, -2))
 
 
 # ------------------------------------------------- windows with first tokens

@@ -1,4 +1,5 @@
-"""Python binding of the C ABI in ``include/attn.h`` (ctypes).
+"""Python binding of the C ABI in ``include/attn.h`` (ctypes; the short calls
+of a decoding step through ``_binding.so``).
 
 Argument marshalling only: every step of the attention forward runs in the
 CUDA kernels of ``libattn.so``.  PyTorch supplies device memory and streams.
@@ -534,92 +535,48 @@ def attn_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, *, scale, causal=False, 
 
 # ----------------------------------------------- around the attention kernels
 #
-# These calls are short (a decoding step makes one of each per layer), so the
-# checks below take the cheap way to every fact: a call costs the host about
-# as long as its launches.
+# These calls are short (a decoding step makes one of each per layer): their
+# checks of the tensors and the allocation of outputs are native
+# (csrc/binding.cpp), since in Python they cost more than the launches.
 
-def _device_of(names, *tensors):
-    """Index of the CUDA device that all the tensors are on; else raises."""
-    index = None
-    for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{names.split()[i]} must be a CUDA tensor")
-        if index is None:
-            index = t.get_device()
-        elif t.get_device() != index:
-            raise TypeError(f"{names.split()[i]} is on {t.device}, {names.split()[0]} on "
-                            f"{tensors[0].device}")
-    return index
+_binding = None
+_bound = None  # the library whose functions the binding calls
+_BOUND_FUNCTIONS = ("attn_qk_norm_rope", "attn_qk_norm_rope_cache", "attn_qk_norm_rope_bwd",
+                    "attn_qk_norm_rope_bwd_workspace_size", "attn_decode_paged",
+                    "attn_decode_paged_workspace_size")
 
 
-def _run(what, index, fn, args, stream, *allocated):
-    """fn(*args, stream) with device `index` current.  The tensors `allocated`
-    here come from the current stream's memory: where another stream uses
-    them, the allocator is told."""
-    if index >= 0 and index != torch.cuda.current_device():
-        with torch.cuda.device(index):
-            return _run(what, index, fn, args, stream, *allocated)
-    if stream is None:
-        _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)), what)
-        return
-    _check(fn(*args, _stream_handle(stream)), what)
-    _keep_for(stream, *allocated)
+def _native():
+    """The native binding, calling the loaded library."""
+    global _binding, _bound
+    L = _lib or lib()
+    if _bound is not L:
+        with _lock:
+            if _binding is None:
+                try:
+                    from . import _binding as module
+                except ImportError as e:
+                    raise RuntimeError("the binding is not built or does not fit this torch; run "
+                                       "`python -m tiled_attention_blackwell_b200.build --force`") from e
+                _binding = module
+            _binding.bind(_check, *[ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+                                    for name in _BOUND_FUNCTIONS])
+            _bound = L
+    return _binding
+
+
+def _handle(stream):
+    """A stream argument as an integer handle."""
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _keep_for(stream, *tensors):
+    """Tells the allocator that work on `stream` uses tensors which were
+    allocated on the current stream."""
     if stream is not None and hasattr(stream, "cuda_stream") \
             and stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
         for t in tensors:
             t.record_stream(stream)
-
-
-_BF16 = (torch.bfloat16,)
-_BF16_FP32 = (torch.bfloat16, torch.float32)
-
-
-def _token_stride(name, t, H, D, dtypes=_BF16):
-    """Distance, in values, of consecutive tokens of a [..., H, D] tensor
-    whose heads are contiguous and whose tokens are evenly spaced."""
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.is_contiguous():
-        return H * D
-    strides = t.stride()
-    if strides[-1] != 1 or (H > 1 and strides[-2] != D):
-        raise TypeError(f"{name}: the heads of a token must be contiguous")
-    step, upto = None, None
-    for n, st in zip(t.shape[-3::-1], strides[-3::-1]):
-        if n == 1:
-            continue
-        if step is None:
-            step = upto = st
-        elif st != upto:
-            raise TypeError(f"{name}: the tokens must be evenly spaced")
-        upto *= n
-    return H * D if step is None else step
-
-
-def _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
-    """Checked arguments that every form of the norm and rotation shares:
-    (weights .. positions), (tokens .. interleaved)."""
-    (*lead, Hq, D), (*lead_k, Hkv, Dk) = q.shape, k.shape
-    if not lead or lead != lead_k or D != Dk:
-        raise TypeError(f"q and k must be [..., H, D] of the same tokens, got {tuple(q.shape)} "
-                        f"and {tuple(k.shape)}")
-    dtype, one = q_weight.dtype, (D,)
-    if dtype not in _BF16_FP32 or k_weight.dtype != dtype or q_weight.shape != one \
-            or k_weight.shape != one or not q_weight.is_contiguous() or not k_weight.is_contiguous():
-        raise TypeError(f"q_weight and k_weight must be contiguous bf16 or fp32 tensors of shape {one}, "
-                        "both of one type")
-    table = cos.shape
-    if cos.dtype != torch.float32 or sin.dtype != torch.float32 or len(table) != 2 \
-            or sin.shape != table or not cos.is_contiguous() or not sin.is_contiguous():
-        raise TypeError("cos and sin must be contiguous fp32 tensors [max_positions, rot / 2]")
-    if positions.dtype != torch.int32 or [*positions.shape] != lead or not positions.is_contiguous():
-        raise TypeError(f"positions must be a contiguous int32 tensor of shape {tuple(lead)}")
-    return ((q_weight.data_ptr(), k_weight.data_ptr(), dtype == torch.float32,
-             cos.data_ptr(), sin.data_ptr(), positions.data_ptr()),
-            (positions.numel(), Hq, Hkv, D, 2 * table[1], table[0], eps, bool(interleaved)))
 
 
 def rope_table(max_positions, rot, *, theta=10000.0, device="cuda"):
@@ -642,22 +599,13 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6, int
     first `rot` values of a head are rotated, in halves or, with
     `interleaved`, in neighbouring pairs; positions int32 [...].  q_out and
     k_out are allocated unless given; they may be q and k themselves."""
-    if q_out is None:
-        q_out = torch.empty_like(q)
-    if k_out is None:
-        k_out = torch.empty_like(k)
-    index = _device_of("q k q_weight k_weight cos sin positions q_out k_out", q, k, q_weight,
-                       k_weight, cos, sin, positions, q_out, k_out)
-    norm, sizes = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
-        raise TypeError("q_out and k_out must have the shapes of q and k")
-    _, Hq, Hkv, D = sizes[:4]
-    _run("attn_qk_norm_rope", index, lib().attn_qk_norm_rope,
-         (q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-          _token_stride("q", q, Hq, D), _token_stride("k", k, Hkv, D),
-          _token_stride("q_out", q_out, Hq, D), _token_stride("k_out", k_out, Hkv, D),
-          *norm, *sizes), stream, q_out, k_out)
-    return q_out, k_out
+    if stream is None:
+        return _native().norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
+                                   q_out, k_out, None)
+    out = _native().norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out,
+                              k_out, _handle(stream))
+    _keep_for(stream, *out)
+    return out
 
 
 def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6,
@@ -666,41 +614,15 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos, sin, positions,
     bf16, such as attention_backward returns) and its inputs.  Returns
     (dq_in, dk_in, dq_weight, dk_weight): bf16 like q and k (allocated unless
     given: views of a packed gradient are fine), fp32 [D]."""
-    if dq_in is None:
-        dq_in = torch.empty_like(q)
-    if dk_in is None:
-        dk_in = torch.empty_like(k)
-    index = _device_of("dq dk q k q_weight k_weight cos sin positions dq_in dk_in", dq, dk, q, k,
-                       q_weight, k_weight, cos, sin, positions, dq_in, dk_in)
-    norm, sizes = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    if dq.shape != q.shape or dk.shape != k.shape or dq_in.shape != q.shape or dk_in.shape != k.shape:
-        raise TypeError("dq, dk, dq_in and dk_in must have the shapes of q and k")
-    _, Hq, Hkv, D = sizes[:4]
-    strides = (_token_stride("dq", dq, Hq, D, _BF16_FP32), _token_stride("dk", dk, Hkv, D, _BF16_FP32),
-               _token_stride("q", q, Hq, D), _token_stride("k", k, Hkv, D),
-               _token_stride("dq_in", dq_in, Hq, D), _token_stride("dk_in", dk_in, Hkv, D))
-    L = lib()
-    dq_weight = torch.empty_like(q_weight, dtype=torch.float32)
-    dk_weight = torch.empty_like(k_weight, dtype=torch.float32)
-    size = L.attn_qk_norm_rope_bwd_workspace_size(D)
-    ws = torch.empty(size, dtype=torch.uint8, device=q.device)
-    _run("attn_qk_norm_rope_bwd", index, L.attn_qk_norm_rope_bwd,
-         (dq.data_ptr(), dk.data_ptr(), dq.dtype == torch.float32, dk.dtype == torch.float32,
-          q.data_ptr(), k.data_ptr(), dq_in.data_ptr(), dk_in.data_ptr(), dq_weight.data_ptr(),
-          dk_weight.data_ptr(), *strides, *norm, *sizes, ws.data_ptr(), size),
-         stream, dq_in, dk_in, dq_weight, dk_weight, ws)
-    return dq_in, dk_in, dq_weight, dk_weight
-
-
-def _cache_type(k_cache, v_cache):
-    """ATTN_KV_* of a pair of caches [num_pages, page_size, Hkv, D]."""
-    dtype, shape = k_cache.dtype, k_cache.shape
-    if dtype not in (torch.bfloat16, torch.float8_e4m3fn) or len(shape) != 4 \
-            or v_cache.dtype != dtype or v_cache.shape != shape \
-            or not k_cache.is_contiguous() or not v_cache.is_contiguous():
-        raise TypeError("k_cache and v_cache must be contiguous bf16 or float8_e4m3fn tensors "
-                        "[num_pages, page_size, Hkv, D], both alike")
-    return ATTN_KV_BF16 if dtype == torch.bfloat16 else ATTN_KV_E4M3
+    if stream is None:
+        return _native().norm_rope_backward(q, k, q_weight, k_weight, cos, sin, positions, eps,
+                                            interleaved, dq, dk, dq_in, dk_in, None, None)
+    ws = torch.empty(lib().attn_qk_norm_rope_bwd_workspace_size(q.shape[-1]), dtype=torch.uint8,
+                     device=q.device)
+    out = _native().norm_rope_backward(q, k, q_weight, k_weight, cos, sin, positions, eps,
+                                       interleaved, dq, dk, dq_in, dk_in, ws, _handle(stream))
+    _keep_for(stream, ws, *out)
+    return out
 
 
 def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos, sin, positions, slots, k_cache, v_cache, *,
@@ -712,23 +634,15 @@ def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos, sin, positions, slots, 
     float8_e4m3fn (codes of value / descale).  slots int32 [...], distinct; a
     negative slot marks padding, for which nothing is written (its row of
     q_out keeps what it held)."""
-    if q_out is None:
-        q_out = torch.empty_like(q)
-    index = _device_of("q k v q_weight k_weight cos sin positions slots k_cache v_cache q_out", q, k,
-                       v, q_weight, k_weight, cos, sin, positions, slots, k_cache, v_cache, q_out)
-    norm, sizes = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    kv, cache = _cache_type(k_cache, v_cache), k_cache.shape
-    if v.shape != k.shape or q_out.shape != q.shape or cache[2:] != k.shape[-2:]:
-        raise TypeError("v must have k's shape, q_out q's, and the caches k's heads")
-    if slots.dtype != torch.int32 or slots.shape != positions.shape or not slots.is_contiguous():
-        raise TypeError(f"slots must be a contiguous int32 tensor of shape {tuple(positions.shape)}")
-    _, Hq, Hkv, D = sizes[:4]
-    _run("attn_qk_norm_rope_cache", index, lib().attn_qk_norm_rope_cache,
-         (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
-          _token_stride("q", q, Hq, D), _token_stride("k", k, Hkv, D), _token_stride("v", v, Hkv, D),
-          _token_stride("q_out", q_out, Hq, D), *norm, slots.data_ptr(), k_cache.data_ptr(),
-          v_cache.data_ptr(), kv, k_descale, v_descale, cache[0] * cache[1], *sizes), stream, q_out)
-    return q_out
+    if stream is None:
+        return _native().norm_rope_cache(q, k, q_weight, k_weight, cos, sin, positions, eps,
+                                         interleaved, v, slots, k_cache, v_cache, k_descale,
+                                         v_descale, q_out, None)
+    out = _native().norm_rope_cache(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
+                                    v, slots, k_cache, v_cache, k_descale, v_descale, q_out,
+                                    _handle(stream))
+    _keep_for(stream, out)
+    return out
 
 
 def decode_workspace_size(D) -> int:
@@ -748,50 +662,25 @@ def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, scale=None, windo
     = (left, right) as in attention(): the last left + 1 keys stay visible, and
     with `sinks` the first ones too.  o, lse and workspace (uint8, at least
     decode_workspace_size(D)) are allocated unless given."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.dtype != torch.bfloat16 \
-            or not q.is_contiguous():
-        raise TypeError("q must be a contiguous bf16 tensor [B, Hq, D]")
-    B, Hq, D = q.shape
-    L = lib()
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(L.attn_decode_paged_workspace_size(D), dtype=torch.uint8,
-                                device=q.device)
-    index = _device_of("q k_cache v_cache page_table seq_lens o lse workspace", q, k_cache, v_cache,
-                       page_table, seq_lens, o, lse, workspace)
-    slopes = None
-    if alibi_slopes is not None:
-        slopes = _slopes(alibi_slopes, Hq, q.device, stream)
-        _device_of("q alibi_slopes", q, slopes)
-    kv = _cache_type(k_cache, v_cache)
-    num_pages, page_size, Hkv, Dk = k_cache.shape
-    if Dk != D:
-        raise TypeError(f"the caches' heads have {Dk} values, q's {D}")
-    table = page_table.shape
-    if page_table.dtype != torch.int32 or len(table) != 2 or table[0] != B \
-            or not page_table.is_contiguous():
-        raise TypeError(f"page_table must be a contiguous int32 tensor [{B}, max_pages]")
-    if seq_lens.dtype != torch.int32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
-        raise TypeError(f"seq_lens must be a contiguous int32 tensor of shape ({B},)")
-    if o.dtype != torch.bfloat16 or o.shape != q.shape or not o.is_contiguous():
-        raise TypeError("o must be a contiguous bf16 tensor of q's shape")
-    if lse.dtype != torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous():
-        raise TypeError(f"lse must be a contiguous fp32 tensor of shape ({B}, {Hq})")
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous uint8 tensor")
     left, right = (-1, -1) if window is None else window
     if right < -1:
         raise ValueError("window bounds must be -1 or >= 0")
-    _run("attn_decode_paged", index, L.attn_decode_paged,
-         (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv, k_descale, v_descale,
-          page_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, D,
-          num_pages, page_size, table[1], D ** -0.5 if scale is None else scale, int(left),
-          int(sinks), softcap or 0.0, None if slopes is None else slopes.data_ptr(),
-          workspace.data_ptr(), workspace.numel()), stream, o, lse, workspace)
-    return o, lse
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if alibi_slopes is not None:
+        alibi_slopes = _slopes(alibi_slopes, q.shape[-2], q.device, stream)
+    if stream is None:
+        return _native().decode(q, k_cache, v_cache, page_table, seq_lens, scale, left, sinks,
+                                softcap or 0.0, alibi_slopes, k_descale, v_descale, o, lse,
+                                workspace, None)
+    if workspace is None:
+        workspace = torch.empty(decode_workspace_size(q.shape[-1]), dtype=torch.uint8,
+                                device=q.device)
+    out = _native().decode(q, k_cache, v_cache, page_table, seq_lens, scale, left, sinks,
+                           softcap or 0.0, alibi_slopes, k_descale, v_descale, o, lse, workspace,
+                           _handle(stream))
+    _keep_for(stream, workspace, *out)
+    return out
 
 
 def device_status(stream=None) -> int:
