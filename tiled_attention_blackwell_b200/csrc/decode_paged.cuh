@@ -46,7 +46,6 @@ constexpr int kDecCopyWarps = 4;
 constexpr int kDecThreads = (kDecWarps + kDecCopyWarps) * 32;
 constexpr int kDecRows = 16;                         // query heads per pair
 constexpr int kDecBlock = 16;                        // keys per TMA box
-constexpr int kDecSlice = 32;                        // values of the output joined at a time
 constexpr int kDecCtasPerSm = 2;
 // Registers: 512 threads per SM launch with 128 each; setmaxnreg moves them
 // from the copying to the computing warpgroup of a block.  The split must not
@@ -170,7 +169,7 @@ struct DecodeSmem {
     static constexpr int kTeams = kDecWarps / kHeads;
     uint8_t k[kStages][kBlocks][kBoxBytes];
     uint8_t v[kStages][kBlocks][kBoxBytes];
-    float o[kDecWarps][kDecRows][kDecSlice + 4];  // + 4: rows start in different banks
+    float o[kDecWarps][kDecRows][D + 4];  // + 4: rows start in different banks
     float4 ml[kDecWarps][kDecRows];
     uint64_t full[kStages], empty[kStages];
     long long start, end, share, base;    // this block's run; tiles before sequence b0
@@ -220,11 +219,21 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
             prefetch_tensormap(&p.tm_v);
         }
         // Tiles of all sequences, then this block's run and where it begins.
+        // A run has a tile for each team, or the longest pair's if that has fewer:
+        // blocks that are there anyway take short pairs one each.
         long long total = 0;
-        for (int b = lane; b < p.B; b += 32) total += (long long)seq_tiles<kTile>(p, b).n * H;
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        int longest = 0;
+        for (int b = lane; b < p.B; b += 32) {
+            const int n = seq_tiles<kTile>(p, b).n;
+            total += (long long)n * H;
+            longest = max(longest, n);
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            total += __shfl_xor_sync(0xffffffffu, total, o);
+            longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+        }
         const long long share =
-            max((long long)kTeams, (total + gridDim.x - 1) / (long long)gridDim.x);
+            max((long long)min(kTeams, longest), (total + gridDim.x - 1) / (long long)gridDim.x);
         const long long start = min(total, share * blockIdx.x);
         const long long end = min(total, start + share);
         long long base = 0;
@@ -617,62 +626,56 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
         }
         const bool whole = t0 == 0 && t1 == st.n;
         const size_t part = (size_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0);
-        // A slice of the values at a time (four accumulators).
 #pragma unroll
-        for (int slice = 0; slice < D / kDecSlice; ++slice) {
+        for (int h = 0; h < 2; ++h) {
+            const int r = qr + 8 * h;
+            if (r >= rows) continue;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = qr + 8 * h;
-                if (r >= rows) continue;
-#pragma unroll
-                for (int jj = 0; jj < kDecSlice / 8; ++jj) {
-                    const int j = slice * (kDecSlice / 8) + jj;
-                    if constexpr (F8) {
-                        float *dst = &sm.o[warp][r][16 * (jj >> 1) + 4 * qc + (jj & 1)];
-                        dst[0] = acc[j][2 * h];
-                        dst[2] = acc[j][2 * h + 1];
-                    } else {
-                        *reinterpret_cast<float2 *>(&sm.o[warp][r][8 * jj + 2 * qc]) =
-                            make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
-                    }
-                }
-            }
-            named_bar_sync(1, kDecWarps * 32);
-            for (int i = threadIdx.x; i < kHeads * rows * (kDecSlice / 4); i += kDecWarps * 32) {
-                const int d = (i % (kDecSlice / 4)) * 4;
-                const int k = i / (kDecSlice / 4) / rows, r = i / (kDecSlice / 4) % rows;  // head, row
-                float mx = sm.ml[k][r].x;
-#pragma unroll
-                for (int w = 1; w < kTeams; ++w) mx = fmaxf(mx, sm.ml[k + w * kHeads][r].x);
-                float ls = 0.0f, lrs = 0.0f;
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int w = 0; w < kTeams; ++w) {
-                    const float4 ml = sm.ml[k + w * kHeads][r];
-                    const float f = ml.x == -INFINITY ? 0.0f : ex2_mufu(ml.x - mx);
-                    const float4 ow = *reinterpret_cast<const float4 *>(&sm.o[k + w * kHeads][r][d]);
-                    ls = fmaf(ml.y, f, ls);
-                    lrs = fmaf(ml.z, f, lrs);
-                    o.x = fmaf(ow.x, f, o.x);
-                    o.y = fmaf(ow.y, f, o.y);
-                    o.z = fmaf(ow.z, f, o.z);
-                    o.w = fmaf(ow.w, f, o.w);
-                }
-                const int at = slice * kDecSlice + d;
-                if (whole) {
-                    const size_t row = (size_t)b * p.Hq + hq0 + k * p.group + r;
-                    const float inv = lrs == 0.0f ? 0.0f : p.v_descale / lrs;
-                    *reinterpret_cast<uint2 *>(p.o + row * D + at) =
-                        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-                    if (at == 0) p.lse[row] = ls == 0.0f ? -INFINITY : (mx + log2f(ls)) * 0.69314718055994531f;
+            for (int j = 0; j < D / 8; ++j) {
+                if constexpr (F8) {
+                    float *dst = &sm.o[warp][r][16 * (j >> 1) + 4 * qc + (j & 1)];
+                    dst[0] = acc[j][2 * h];
+                    dst[2] = acc[j][2 * h + 1];
                 } else {
-                    const size_t row = (part * kHeads + k) * kDecRows + r;
-                    *reinterpret_cast<float4 *>(p.part_o + row * D + at) = o;
-                    if (at == 0) p.part_ml[row] = make_float4(mx, ls, lrs, 0.0f);
+                    *reinterpret_cast<float2 *>(&sm.o[warp][r][8 * j + 2 * qc]) =
+                        make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
                 }
             }
-            named_bar_sync(1, kDecWarps * 32);  // the buffer is free again
         }
+        named_bar_sync(1, kDecWarps * 32);
+        for (int i = threadIdx.x; i < kHeads * rows * (D / 4); i += kDecWarps * 32) {
+            const int d = (i % (D / 4)) * 4;
+            const int k = i / (D / 4) / rows, r = i / (D / 4) % rows;  // head, row
+            float mx = sm.ml[k][r].x;
+#pragma unroll
+            for (int w = 1; w < kTeams; ++w) mx = fmaxf(mx, sm.ml[k + w * kHeads][r].x);
+            float ls = 0.0f, lrs = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kTeams; ++w) {
+                const float4 ml = sm.ml[k + w * kHeads][r];
+                const float f = ml.x == -INFINITY ? 0.0f : ex2_mufu(ml.x - mx);
+                const float4 ow = *reinterpret_cast<const float4 *>(&sm.o[k + w * kHeads][r][d]);
+                ls = fmaf(ml.y, f, ls);
+                lrs = fmaf(ml.z, f, lrs);
+                o.x = fmaf(ow.x, f, o.x);
+                o.y = fmaf(ow.y, f, o.y);
+                o.z = fmaf(ow.z, f, o.z);
+                o.w = fmaf(ow.w, f, o.w);
+            }
+            if (whole) {
+                const size_t row = (size_t)b * p.Hq + hq0 + k * p.group + r;
+                const float inv = lrs == 0.0f ? 0.0f : p.v_descale / lrs;
+                *reinterpret_cast<uint2 *>(p.o + row * D + d) =
+                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+                if (d == 0) p.lse[row] = ls == 0.0f ? -INFINITY : (mx + log2f(ls)) * 0.69314718055994531f;
+            } else {
+                const size_t row = (part * kHeads + k) * kDecRows + r;
+                *reinterpret_cast<float4 *>(p.part_o + row * D + d) = o;
+                if (d == 0) p.part_ml[row] = make_float4(mx, ls, lrs, 0.0f);
+            }
+        }
+        named_bar_sync(1, kDecWarps * 32);  // the buffers are free again
         // A pair that begins here and goes on: the join starts at this block.
         if (t0 == 0 && t1 < st.n && threadIdx.x == 0) {
             const long long last = pos + st.n - 1;

@@ -196,10 +196,10 @@ attn_status_t launch_decode(tab::DecodeParams &p, const void *k_cache, const voi
     if ((s = make_cache_map(&p.tm_k, k_cache, p.num_pages, p.page_size, p.Hkv, D, eb, kHeads)) != ATTN_OK ||
         (s = make_cache_map(&p.tm_v, v_cache, p.num_pages, p.page_size, p.Hkv, D, eb, kHeads)) != ATTN_OK)
         return s;
-    // No more blocks than the longest sequences allow tiles for one per team.
-    const double tiles = (double)p.B * (p.Hkv / kHeads) * p.hchunks *
-                         (((double)p.max_pages * p.page_size + Smem::kTile - 1) / Smem::kTile);
-    if (tiles / Smem::kTeams + 1 < blocks) blocks = (int)(tiles / Smem::kTeams) + 1;
+    // No more blocks than runs: pairs of one tile, or a team's tiles each.
+    const double pairs = (double)p.B * (p.Hkv / kHeads) * p.hchunks;
+    const double tiles = ((double)p.max_pages * p.page_size + Smem::kTile - 1) / Smem::kTile;
+    blocks = (int)std::min<double>(blocks, pairs * std::max(1.0, std::ceil(tiles / Smem::kTeams)));
     kernel<<<blocks, tab::kDecThreads, smem, stream>>>(p);
     if ((s = launch_result()) != ATTN_OK) return s;
     const tab::JoinParams jp = {p.part_o, p.part_ml, p.record, p.o, p.lse, p.Hq, p.group, p.v_descale};
