@@ -198,7 +198,6 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
     // warp's alone: no wait can be two phases behind its slot.
     static_assert(kStages % kTeams == 0 && kStages % kDecCopyWarps == 0, "slots belong to fixed warps");
     extern __shared__ uint8_t smem_raw[];
-    launch_dependents();  // the join: its blocks wait for this grid's end
     const uint32_t raw_off = smem_u32(smem_raw);
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (raw_off & 1023u)) & 1023u));
     const int warp = warp_id(), lane = lane_id();
@@ -213,11 +212,16 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
         sm.abort_flag = 0;
         fence_mbar_init();
     }
+    if (warp == kDecWarps && lane == 0) {
+        prefetch_tensormap(&p.tm_k);
+        prefetch_tensormap(&p.tm_v);
+    }
+    // What stands before this launch in the stream may still be ending; from
+    // here on its results are read.  The join may begin to start: its blocks
+    // wait in turn for this grid's end.
+    wait_for_primary();
+    launch_dependents();
     if (warp == kDecWarps) {
-        if (lane == 0) {
-            prefetch_tensormap(&p.tm_k);
-            prefetch_tensormap(&p.tm_v);
-        }
         // Tiles of all sequences, then this block's run and where it begins.
         // A run has a tile for each team, or the longest pair's if that has fewer:
         // blocks that are there anyway take short pairs one each.

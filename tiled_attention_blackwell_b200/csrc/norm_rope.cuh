@@ -216,6 +216,8 @@ constexpr int kNormRows = 4;  // heads of a token that a group of lanes takes to
 template <int D, int KV, bool INTERLEAVED>
 __global__ void __launch_bounds__(kNormThreads, 8)
 norm_rope_kernel(const NormRopeParams p) {
+    wait_for_primary();
+    launch_dependents();
     constexpr int kLanes = D / 8, kGroups = kNormThreads / kLanes, U = kNormRows;
     const LanePlace at = lane_place<INTERLEAVED>(threadIdx.x % kLanes, p.rot);
     const uint32_t chunks = p.chunks_q + (KV ? 2 : 1) * p.chunks_k;
@@ -404,6 +406,7 @@ __global__ void __launch_bounds__(kNormThreads, 4)
 norm_rope_bwd_kernel(const NormRopeParams p) {
     constexpr int kLanes = D / 8, kGroups = kNormThreads / kLanes;
     __shared__ float share[kGroups][D];
+    wait_for_primary();
     launch_dependents();  // the sum of the shares: its blocks wait for this grid's end
     const int group = threadIdx.x / kLanes;
     const LanePlace at = lane_place<INTERLEAVED>(threadIdx.x % kLanes, p.rot);

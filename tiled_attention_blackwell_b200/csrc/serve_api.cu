@@ -26,17 +26,12 @@ namespace {
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-attn_status_t launch_result() {
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
-    return ok();
-}
-
-// Launches `kernel` so that its blocks may start while the kernel before it in
-// the stream ends (it waits for that with wait_for_primary()).
+// Launches `kernel` so that its blocks may start while what stands before it in
+// the stream ends; the kernel waits for that end (wait_for_primary()) before
+// it touches memory.
 template <class... Args>
 attn_status_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 threads, cudaStream_t stream,
-                               Args... args) {
+                               size_t smem, const Args &...args) {
     cudaLaunchAttribute attr;
     memset(&attr, 0, sizeof attr);
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -45,6 +40,7 @@ attn_status_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 threads,
     memset(&config, 0, sizeof config);
     config.gridDim = grid;
     config.blockDim = threads;
+    config.dynamicSmemBytes = smem;
     config.stream = stream;
     config.attrs = &attr;
     config.numAttrs = 1;
@@ -100,9 +96,9 @@ attn_status_t launch_norm(const tab::NormRopeParams &p, int D, cudaStream_t stre
     const long long items = p.tokens * (p.chunks_q + (KV ? 2 : 1) * p.chunks_k);
     const int groups = tab::kNormThreads / (D / 8);
     const unsigned grid = (unsigned)((items + groups - 1) / groups);
-    if (D == 128) tab::norm_rope_kernel<128, KV, INTERLEAVED><<<grid, tab::kNormThreads, 0, stream>>>(p);
-    else tab::norm_rope_kernel<64, KV, INTERLEAVED><<<grid, tab::kNormThreads, 0, stream>>>(p);
-    return launch_result();
+    return launch_dependent(D == 128 ? tab::norm_rope_kernel<128, KV, INTERLEAVED>
+                                     : tab::norm_rope_kernel<64, KV, INTERLEAVED>,
+                            dim3(grid), dim3(tab::kNormThreads), stream, 0, p);
 }
 
 template <int KV>
@@ -117,11 +113,11 @@ attn_status_t launch_norm_bwd(const tab::NormRopeParams &p, int num_sms, float *
     const long long items = p.tokens * std::max(p.chunks_q, p.chunks_k);
     const int blocks = (int)std::min<long long>(
         (items + groups - 1) / groups, std::min(kNormBwdMaxBlocks, kNormBwdBlocksPerSm * num_sms));
-    tab::norm_rope_bwd_kernel<D, INTERLEAVED><<<blocks, tab::kNormThreads, 0, stream>>>(p);
-    const attn_status_t s = launch_result();
+    const attn_status_t s = launch_dependent(tab::norm_rope_bwd_kernel<D, INTERLEAVED>, dim3(blocks),
+                                             dim3(tab::kNormThreads), stream, 0, p);
     if (s != ATTN_OK) return s;
     return launch_dependent(tab::norm_rope_dw_kernel, dim3(2 * D / tab::kDwCols),
-                            dim3(tab::kDwCols, tab::kDwRows), stream,
+                            dim3(tab::kDwCols, tab::kDwRows), stream, 0,
                             static_cast<const float *>(p.partial), blocks, D, dqw, dkw);
 }
 
@@ -200,12 +196,12 @@ attn_status_t launch_decode(tab::DecodeParams &p, const void *k_cache, const voi
     const double pairs = (double)p.B * (p.Hkv / kHeads) * p.hchunks;
     const double tiles = ((double)p.max_pages * p.page_size + Smem::kTile - 1) / Smem::kTile;
     blocks = (int)std::min<double>(blocks, pairs * std::max(1.0, std::ceil(tiles / Smem::kTeams)));
-    kernel<<<blocks, tab::kDecThreads, smem, stream>>>(p);
-    if ((s = launch_result()) != ATTN_OK) return s;
+    if ((s = launch_dependent(kernel, dim3(blocks), dim3(tab::kDecThreads), stream, smem, p)) != ATTN_OK)
+        return s;
     const tab::JoinParams jp = {p.part_o, p.part_ml, p.record, p.o, p.lse, p.Hq, p.group, p.v_descale};
     return launch_dependent(tab::decode_join_kernel<D, kHeads>,
                             dim3(blocks, std::min(p.group, tab::kDecRows), kHeads),
-                            dim3(tab::kJoinThreads), stream, jp);
+                            dim3(tab::kJoinThreads), stream, 0, jp);
 }
 
 // The variant by the bytes of a key's head: pairs of as many key heads as make
