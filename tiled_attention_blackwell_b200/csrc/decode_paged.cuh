@@ -390,46 +390,85 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
     for (int i = 0; i < kVAt; ++i) v_at[i] = box_offset<Smem::kRowBytes>(lane & 15, 2 * i + (lane >> 4));
     const bool modified = p.softcap_out > 0.0f || p.alibi_slopes != nullptr;
 
-    bool ok = true;
+    // The block's run, pair by pair.
+    struct Segment {
+        SeqTiles st;
+        int b, t0, t1;  // tiles [t0, t1) of the pair
+        int rows, hq0;  // query heads of a key head, the first of the pair's first key head
+        uint32_t g0;    // the block's tiles before it
+    };
     long long pos = start, base = sm.base;
-    int b = sm.b0;
-    while (pos < end && b < p.B) {
-        const SeqTiles st = seq_tiles<kTile>(p, b);
-        if (pos >= base + (long long)st.n * H) {
-            base += (long long)st.n * H;
-            ++b;
-            continue;
+    int next_b = sm.b0;
+    auto next_segment = [&](Segment &s) -> bool {
+        while (pos < end && next_b < p.B) {
+            s.st = seq_tiles<kTile>(p, next_b);
+            if (pos >= base + (long long)s.st.n * H) {
+                base += (long long)s.st.n * H;
+                ++next_b;
+                continue;
+            }
+            const uint32_t in_seq = (uint32_t)(pos - base);
+            const int pair = (int)(in_seq / (uint32_t)s.st.n);
+            s.b = next_b;
+            s.t0 = (int)(in_seq - (uint32_t)pair * (uint32_t)s.st.n);
+            s.t1 = (int)min((long long)s.st.n, s.t0 + (end - pos));
+            const int heads = pair / p.hchunks, r0 = (pair - heads * p.hchunks) * kDecRows;
+            s.rows = min(kDecRows, p.group - r0);
+            s.hq0 = heads * kHeads * p.group + r0;
+            s.g0 = (uint32_t)(pos - start);
+            pos += s.t1 - s.t0;
+            return true;
         }
-        const uint32_t in_seq = (uint32_t)(pos - base);
-        const int pair = (int)(in_seq / (uint32_t)st.n);
-        const int t0 = (int)(in_seq - (uint32_t)pair * (uint32_t)st.n);
-        const int t1 = (int)min((long long)st.n, t0 + (end - pos));
-        const int heads = pair / p.hchunks, r0 = (pair - heads * p.hchunks) * kDecRows;
-        const int rows = min(kDecRows, p.group - r0);
-        const int hq0 = heads * kHeads * p.group + r0;  // of the pair's first key head
-        const int hq = hq0 + head * p.group;            // of this warp's
-
-        // Q as the A operand.  bf16: K index k of step ks is value 16 ks + k.
-        // e4m3: the B operand's word holds four neighbouring values, so index
-        // (2c, 2c+1, 2c+8, 2c+9) is value 16 ks + 4c + (0..3) on both sides.
-        uint32_t a[D / 16][4];
-        float c_row[2] = {p.scale_log2, p.scale_log2};
-        float cap_row[2] = {p.softcap_in * (2.0f * kLog2eF), p.softcap_in * (2.0f * kLog2eF)};
+        return false;
+    };
+    // Q of a pair, loaded while the pair before it is joined.  bf16: the words are
+    // the A operand, K index k of step ks being value 16 ks + k.  e4m3: the B
+    // operand's word holds four neighbouring values, so index (2c, 2c+1, 2c+8,
+    // 2c+9) is value 16 ks + 4c + (0..3) on both sides.
+    uint32_t a[D / 16][4];
+    auto load_q = [&](const Segment &s) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = qr + 8 * h;
-            const __nv_bfloat16 *q = p.q + ((size_t)b * p.Hq + hq + (r < rows ? r : 0)) * D;
-            if constexpr (F8) {
-                uint2 w[D / 16];
+            const bool there = r < s.rows;
+            const __nv_bfloat16 *q =
+                p.q + ((size_t)s.b * p.Hq + s.hq0 + head * p.group + (there ? r : 0)) * D;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                if constexpr (F8) {
+                    const uint2 w = there ? *reinterpret_cast<const uint2 *>(q + 16 * ks + 4 * qc) : make_uint2(0u, 0u);
+                    a[ks][h] = w.x;
+                    a[ks][2 + h] = w.y;
+                } else {
+                    a[ks][h] = there ? *reinterpret_cast<const uint32_t *>(q + 16 * ks + 2 * qc) : 0u;
+                    a[ks][2 + h] = there ? *reinterpret_cast<const uint32_t *>(q + 16 * ks + 8 + 2 * qc) : 0u;
+                }
+            }
+        }
+    };
+
+    bool ok = true;
+    Segment seg, next;
+    bool more = next_segment(next);
+    if (more) load_q(next);
+    while (more) {
+        seg = next;
+        const SeqTiles &st = seg.st;
+        const int rows = seg.rows, t0 = seg.t0, t1 = seg.t1;
+        const int hq = seg.hq0 + head * p.group;  // of this warp's head
+        float c_row[2] = {p.scale_log2, p.scale_log2};
+        float cap_row[2] = {p.softcap_in * (2.0f * kLog2eF), p.softcap_in * (2.0f * kLog2eF)};
+        if constexpr (F8) {
+            // To f16, by a power of two per row.
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
                 float amax = 0.0f;
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    w[ks] = r < rows ? *reinterpret_cast<const uint2 *>(q + 16 * ks + 4 * qc) : make_uint2(0u, 0u);
-                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(__uint_as_float(w[ks].x << 16)),
-                                                   fabsf(__uint_as_float(w[ks].x & 0xffff0000u))),
-                                             fmaxf(fabsf(__uint_as_float(w[ks].y << 16)),
-                                                   fabsf(__uint_as_float(w[ks].y & 0xffff0000u)))));
-                }
+                for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                    for (int i = h; i < 4; i += 2)
+                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(a[ks][i] << 16)),
+                                                 fabsf(__uint_as_float(a[ks][i] & 0xffff0000u))));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 // 2^-e with amax in [2^e, 2^(e+1)); e within [-100, 120], and 0 for
@@ -441,18 +480,11 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
                 c_row[h] *= up;
                 cap_row[h] *= up;
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    a[ks][h] = pack_f16x2(__uint_as_float(w[ks].x << 16) * down,
-                                          __uint_as_float(w[ks].x & 0xffff0000u) * down);
-                    a[ks][2 + h] = pack_f16x2(__uint_as_float(w[ks].y << 16) * down,
-                                              __uint_as_float(w[ks].y & 0xffff0000u) * down);
-                }
-            } else {
+                for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    a[ks][h] = r < rows ? *reinterpret_cast<const uint32_t *>(q + 16 * ks + 2 * qc) : 0u;
-                    a[ks][2 + h] = r < rows ? *reinterpret_cast<const uint32_t *>(q + 16 * ks + 8 + 2 * qc) : 0u;
-                }
+                    for (int i = h; i < 4; i += 2)
+                        a[ks][i] = pack_f16x2(__uint_as_float(a[ks][i] << 16) * down,
+                                              __uint_as_float(a[ks][i] & 0xffff0000u) * down);
             }
         }
         float slope[2] = {0.0f, 0.0f};
@@ -470,7 +502,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, lr[2] = {0.0f, 0.0f};
 
         // This team's tiles of the pair.
-        const uint32_t g0 = (uint32_t)(pos - start);
+        const uint32_t g0 = seg.g0;
         int t = t0 + (int)((team + kTeams - g0 % kTeams) % kTeams);
         for (; t < t1; t += kTeams) {
             const uint32_t g = g0 + (uint32_t)(t - t0);
@@ -615,25 +647,55 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
             if (lane == 0) mbar_arrive(&sm.empty[s]);
         }
 
-        // ------------------------------------------- join the teams' results
-        // Every warp comes here for every pair, with or without a tile of it
-        // (and after a wait that ran out), so the barriers below always meet.
+        more = next_segment(next);
+        if (more) load_q(next);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
                 l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
                 lr[h] += __shfl_xor_sync(0xffffffffu, lr[h], o);
             }
-            if (qr + 8 * h < rows && qc == 0)
-                sm.ml[warp][qr + 8 * h] = make_float4(m[h], l[h], F8 ? l[h] : lr[h], 0.0f);
-        }
         const bool whole = t0 == 0 && t1 == st.n;
-        const size_t part = (size_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0);
+        if (whole && t1 == 1) {
+            // A pair of one tile is its team's alone: the team writes the output, and
+            // the others are already at their next pair.
+            if (team == (int)(g0 % kTeams)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = qr + 8 * h;
+                    if (r >= rows) continue;
+                    const size_t row = (size_t)seg.b * p.Hq + hq + r;
+                    const float sum = F8 ? l[h] : lr[h];
+                    const float inv = sum == 0.0f ? 0.0f : p.v_descale / sum;
+#pragma unroll
+                    for (int j = 0; j < D / 8; j += 2) {
+                        const float v0 = acc[j][2 * h] * inv, v1 = acc[j][2 * h + 1] * inv;
+                        const float v2 = acc[j + 1][2 * h] * inv, v3 = acc[j + 1][2 * h + 1] * inv;
+                        __nv_bfloat16 *o = p.o + row * D;
+                        if constexpr (F8) {
+                            *reinterpret_cast<uint2 *>(o + 8 * j + 4 * qc) =
+                                make_uint2(pack_bf16x2(v0, v2), pack_bf16x2(v1, v3));
+                        } else {
+                            *reinterpret_cast<uint32_t *>(o + 8 * j + 2 * qc) = pack_bf16x2(v0, v1);
+                            *reinterpret_cast<uint32_t *>(o + 8 * j + 8 + 2 * qc) = pack_bf16x2(v2, v3);
+                        }
+                    }
+                    if (qc == 0)
+                        p.lse[row] = l[h] == 0.0f ? -INFINITY : (m[h] + log2f(l[h])) * 0.69314718055994531f;
+                }
+            }
+            continue;
+        }
+
+        // ------------------------------------------- join the teams' results
+        // Every warp comes here for every other pair, with or without a tile of it
+        // (and after a wait that ran out), so the barriers below always meet.
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = qr + 8 * h;
             if (r >= rows) continue;
+            if (qc == 0) sm.ml[warp][r] = make_float4(m[h], l[h], F8 ? l[h] : lr[h], 0.0f);
 #pragma unroll
             for (int j = 0; j < D / 8; ++j) {
                 if constexpr (F8) {
@@ -646,6 +708,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
                 }
             }
         }
+        const size_t part = (size_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0);
         named_bar_sync(1, kDecWarps * 32);
         for (int i = threadIdx.x; i < kHeads * rows * (D / 4); i += kDecWarps * 32) {
             const int d = (i % (D / 4)) * 4;
@@ -668,7 +731,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
                 o.w = fmaf(ow.w, f, o.w);
             }
             if (whole) {
-                const size_t row = (size_t)b * p.Hq + hq0 + k * p.group + r;
+                const size_t row = (size_t)seg.b * p.Hq + seg.hq0 + k * p.group + r;
                 const float inv = lrs == 0.0f ? 0.0f : p.v_descale / lrs;
                 *reinterpret_cast<uint2 *>(p.o + row * D + d) =
                     make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -682,10 +745,9 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
         named_bar_sync(1, kDecWarps * 32);  // the buffers are free again
         // A pair that begins here and goes on: the join starts at this block.
         if (t0 == 0 && t1 < st.n && threadIdx.x == 0) {
-            const long long last = pos + st.n - 1;
-            p.record[blockIdx.x] = make_int4(b, hq0, rows, (int)(last / sm.share));
+            const long long last = start + g0 + st.n - 1;
+            p.record[blockIdx.x] = make_int4(seg.b, seg.hq0, rows, (int)(last / sm.share));
         }
-        pos += t1 - t0;
     }
 }
 
