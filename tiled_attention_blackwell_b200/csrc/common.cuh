@@ -69,6 +69,16 @@ __device__ __forceinline__ KeyRange tile_key_range(const Params &p, int r0, int 
     return {lo, hi};
 }
 
+// Bit e: a row whose interval is [lo, hi] and whose first `sinks` keys (up to
+// hi) are visible too sees key `key0 + e`.
+__device__ __forceinline__ uint32_t visible_bits(int key0, int lo, int hi, int sinks) {
+    const int h = hi - key0, l = lo - key0, f = sinks - key0;
+    const uint32_t upto_hi = h >= 31 ? ~0u : h < 0 ? 0u : (2u << h) - 1u;
+    const uint32_t from_lo = l <= 0 ? ~0u : l > 31 ? 0u : ~0u << l;
+    const uint32_t first = f >= 32 ? ~0u : f <= 0 ? 0u : (1u << f) - 1u;
+    return upto_hi & (from_lo | first);
+}
+
 // Bounded wait.  Returns false when the CTA is aborting (own timeout or
 // another role's); `honor_abort` = false keeps waiting until the timeout only.
 template <bool kHint = false>

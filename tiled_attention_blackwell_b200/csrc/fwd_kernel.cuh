@@ -242,16 +242,6 @@ __device__ __forceinline__ void exp_pack_group(const float *s, float c, float ne
     sum_pv += r0s + r1s;
 }
 
-// Bit e: a row whose interval is [lo, hi] and whose first `sinks` keys (up to
-// hi) are visible too sees key `key0 + e`.
-__device__ __forceinline__ uint32_t visible_bits(int key0, int lo, int hi, int sinks) {
-    const int h = hi - key0, l = lo - key0, f = sinks - key0;
-    const uint32_t upto_hi = h >= 31 ? ~0u : h < 0 ? 0u : (2u << h) - 1u;
-    const uint32_t from_lo = l <= 0 ? ~0u : l > 31 ? 0u : ~0u << l;
-    const uint32_t first = f >= 32 ? ~0u : f <= 0 ? 0u : (1u << f) - 1u;
-    return upto_hi & (from_lo | first);
-}
-
 // The same for 8-bit P: 64 probabilities of a row to e4m3, four per word.
 template <int EXP_MODE>
 __device__ __forceinline__ float exp_pack_half_fp8(const float *s, float c, float neg_m,
