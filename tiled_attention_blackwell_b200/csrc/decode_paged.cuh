@@ -27,11 +27,14 @@
 // pairs, so the copies never pause: 16 keys of K and of V are one TMA box
 // each (a page holds a multiple of 16 keys), in a ring of kStages tiles.
 //
-// Products: mma.sync m16n8k16 with up to 16 query heads of one key head as
-// rows.  (tcgen05 needs 64 rows or more; here the tensor pipe is idle most of
-// the time either way, and the registers hold S, P and O without a trip
+// Products: mma.sync m16n8k16 with 16 keys (S^T = K Q^T), then 16 values (O^T =
+// V^T P^T) as rows and the query heads of one key head as columns, in blocks of
+// 8: eight heads or fewer waste nothing.  P goes from the layout of a result to
+// that of an operand by a transposition within the warp.  (tcgen05 needs 64
+// rows or more of the other operand's heads; here the tensor pipe is idle most
+// of the time either way, and the registers hold S, P and O without a trip
 // through tensor memory.)  An e4m3 cache is widened to f16 in registers,
-// exactly; Q is scaled by a power of two per row so that f16 holds it.
+// exactly; Q is scaled by a power of two per head so that f16 holds it.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -44,7 +47,7 @@ namespace tab {
 constexpr int kDecWarps = 4;                         // computing warps
 constexpr int kDecCopyWarps = 4;
 constexpr int kDecThreads = (kDecWarps + kDecCopyWarps) * 32;
-constexpr int kDecRows = 16;                         // query heads per pair
+constexpr int kDecRows = 16;                         // query heads of a key head per pair, at most
 constexpr int kDecBlock = 16;                        // keys per TMA box
 constexpr int kDecCtasPerSm = 2;
 // Registers: 512 threads per SM launch with 128 each; setmaxnreg moves them
@@ -72,7 +75,7 @@ struct DecodeParams {
     float *part_o;           // [blocks][2][kHeads][16][D], relative to the partial's maximum
     float4 *part_ml;         // [blocks][2][kHeads][16]: maximum (log2), sum, sum of the rounded weights
     int4 *record;            // [blocks]: the pair that is first cut at this block's end
-    int B, Hq, Hkv, group, hchunks;  // hchunks: parts of 16 query heads of a key head
+    int B, Hq, Hkv, group, hchunks;  // hchunks: parts of a key head's query heads
     int max_pages, page_size, num_pages;
     int window_left, sinks;
     float scale_log2;        // scale * k_descale * log2(e)
@@ -140,25 +143,30 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// A pair of weights in the operand type.  bf16: with the sum of the rounded
-// values, which normalises the output, as in the forward (a row that one key
+// Transposes an 8 x 8 matrix of 16-bit values held as lane (row, column pair).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+// Weights of two heads in the operand type.  bf16: with the sums of the rounded
+// values, which normalise the output, as in the forward (a row that one key
 // dominates gives that key's V).  f16 weights are off by 2^-12 at most, which
 // the output's own rounding hides: the plain sum normalises them.
 template <bool F8>
-__device__ __forceinline__ uint32_t pack_weights(float p0, float p1, float &sum) {
+__device__ __forceinline__ uint32_t pack_weights(float p0, float p1, float &sum0, float &sum1) {
     if constexpr (F8) {
         return pack_f16x2(p0, p1);
     } else {
         const uint32_t h = pack_bf16x2(p0, p1);
-        float other = 0.0f;
-        add_bf16x2_f32(sum, other, h);
-        sum += other;
+        add_bf16x2_f32(sum0, sum1, h);
         return h;
     }
 }
 
-// kBlocks boxes of 16 keys of kHeads heads per tile.
-template <int D, bool F8, int kHeads, int kBlocks, int kStages>
+// kBlocks boxes of 16 keys of kHeads heads per tile; NB blocks of 8 query heads.
+template <int D, bool F8, int kHeads, int NB, int kBlocks, int kStages>
 struct DecodeSmem {
     static constexpr int kRowBytes = D * (F8 ? 1 : 2);
     static constexpr int kHeadBytes = kDecBlock * kRowBytes;  // one head's part of a box
@@ -169,8 +177,9 @@ struct DecodeSmem {
     static constexpr int kTeams = kDecWarps / kHeads;
     uint8_t k[kStages][kBlocks][kBoxBytes];
     uint8_t v[kStages][kBlocks][kBoxBytes];
-    float o[kDecWarps][kDecRows][D + 4];  // + 4: rows start in different banks
-    float4 ml[kDecWarps][kDecRows];
+    static constexpr int kRows = 8 * NB;
+    float o[kDecWarps][kRows][D + 4];  // + 4: rows start in different banks
+    float4 ml[kDecWarps][kRows];
     uint64_t full[kStages], empty[kStages];
     long long start, end, share, base;    // this block's run; tiles before sequence b0
     int b0;
@@ -188,10 +197,10 @@ __device__ __forceinline__ uint32_t box_offset(int r, int c) {
         return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-template <int D, bool F8, int kHeads, int kBlocks, int kStages>
+template <int D, bool F8, int kHeads, int NB, int kBlocks, int kStages>
 __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
 decode_paged_kernel(const __grid_constant__ DecodeParams p) {
-    using Smem = DecodeSmem<D, F8, kHeads, kBlocks, kStages>;
+    using Smem = DecodeSmem<D, F8, kHeads, NB, kBlocks, kStages>;
     constexpr int kTile = Smem::kTile, kTeams = Smem::kTeams;
     constexpr int kPieces = Smem::kRowBytes / 16;  // 16-byte pieces of a row
     // Tile g goes to slot g % kStages, which is one team's and one copying
@@ -363,7 +372,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
     // --------------------------------------------------------------- compute
     setmaxnreg_inc<kDecComputeRegs>();
     const int head = warp % kHeads, team = warp / kHeads;
-    const int qr = lane >> 2, qc = lane & 3;  // row (and row + 8) and column pair of a fragment
+    const int fr = lane >> 2, fc = lane & 3;  // row (and row + 8) and column pair of a fragment
     // Sequences without a key: zeros and -inf (each block takes every
     // gridDim.x-th sequence).
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -380,14 +389,11 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
     }
     if (threadIdx.x == 0) p.record[blockIdx.x] = make_int4(0, 0, 0, 0);
 
-    // Where this lane reads K (keys 0-7 of a box, four pieces) and V (16 keys,
-    // two pieces) of a chunk, for each group of pieces.
-    constexpr int kKAt = kPieces >= 8 ? 2 : 1, kVAt = kPieces >= 8 ? 4 : 2;
-    uint32_t k_at[kKAt], v_at[kVAt];
+    // Where this lane reads K and V (16 keys, two pieces of a chunk at a time).
+    constexpr int kAt = kPieces >= 8 ? 4 : 2;
+    uint32_t at[kAt];
 #pragma unroll
-    for (int i = 0; i < kKAt; ++i) k_at[i] = box_offset<Smem::kRowBytes>(lane & 7, 4 * i + (lane >> 3));
-#pragma unroll
-    for (int i = 0; i < kVAt; ++i) v_at[i] = box_offset<Smem::kRowBytes>(lane & 15, 2 * i + (lane >> 4));
+    for (int i = 0; i < kAt; ++i) at[i] = box_offset<Smem::kRowBytes>(lane & 15, 2 * i + (lane >> 4));
     const bool modified = p.softcap_out > 0.0f || p.alibi_slopes != nullptr;
 
     // The block's run, pair by pair.
@@ -412,8 +418,8 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
             s.b = next_b;
             s.t0 = (int)(in_seq - (uint32_t)pair * (uint32_t)s.st.n);
             s.t1 = (int)min((long long)s.st.n, s.t0 + (end - pos));
-            const int heads = pair / p.hchunks, r0 = (pair - heads * p.hchunks) * kDecRows;
-            s.rows = min(kDecRows, p.group - r0);
+            const int heads = pair / p.hchunks, r0 = (pair - heads * p.hchunks) * Smem::kRows;
+            s.rows = min(Smem::kRows, p.group - r0);
             s.hq0 = heads * kHeads * p.group + r0;
             s.g0 = (uint32_t)(pos - start);
             pos += s.t1 - s.t0;
@@ -421,27 +427,27 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
         }
         return false;
     };
-    // Q of a pair, loaded while the pair before it is joined.  bf16: the words are
-    // the A operand, K index k of step ks being value 16 ks + k.  e4m3: the B
-    // operand's word holds four neighbouring values, so index (2c, 2c+1, 2c+8,
-    // 2c+9) is value 16 ks + 4c + (0..3) on both sides.
-    uint32_t a[D / 16][4];
+    // Q of a pair as the B operand (this lane: head 8 nb + fr), loaded while the
+    // pair before it is joined.  bf16: K index k of step ks is value 16 ks + k.
+    // e4m3: the A operand's word holds four neighbouring values, so index (2c,
+    // 2c+1, 2c+8, 2c+9) is value 16 ks + 4c + (0..3) on both sides.
+    uint32_t qb[NB][D / 16][2];
     auto load_q = [&](const Segment &s) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = qr + 8 * h;
+        for (int nb = 0; nb < NB; ++nb) {
+            const int r = 8 * nb + fr;
             const bool there = r < s.rows;
             const __nv_bfloat16 *q =
                 p.q + ((size_t)s.b * p.Hq + s.hq0 + head * p.group + (there ? r : 0)) * D;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 if constexpr (F8) {
-                    const uint2 w = there ? *reinterpret_cast<const uint2 *>(q + 16 * ks + 4 * qc) : make_uint2(0u, 0u);
-                    a[ks][h] = w.x;
-                    a[ks][2 + h] = w.y;
+                    const uint2 w = there ? *reinterpret_cast<const uint2 *>(q + 16 * ks + 4 * fc) : make_uint2(0u, 0u);
+                    qb[nb][ks][0] = w.x;
+                    qb[nb][ks][1] = w.y;
                 } else {
-                    a[ks][h] = there ? *reinterpret_cast<const uint32_t *>(q + 16 * ks + 2 * qc) : 0u;
-                    a[ks][2 + h] = there ? *reinterpret_cast<const uint32_t *>(q + 16 * ks + 8 + 2 * qc) : 0u;
+                    qb[nb][ks][0] = there ? *reinterpret_cast<const uint32_t *>(q + 16 * ks + 2 * fc) : 0u;
+                    qb[nb][ks][1] = there ? *reinterpret_cast<const uint32_t *>(q + 16 * ks + 8 + 2 * fc) : 0u;
                 }
             }
         }
@@ -456,50 +462,59 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
         const SeqTiles &st = seg.st;
         const int rows = seg.rows, t0 = seg.t0, t1 = seg.t1;
         const int hq = seg.hq0 + head * p.group;  // of this warp's head
-        float c_row[2] = {p.scale_log2, p.scale_log2};
-        float cap_row[2] = {p.softcap_in * (2.0f * kLog2eF), p.softcap_in * (2.0f * kLog2eF)};
-        if constexpr (F8) {
-            // To f16, by a power of two per row.
+        // Per head 8 nb + 2 fc + i, which is column i of this lane's results: factor
+        // of the scores, soft-cap's, slope.
+        float c_head[NB][2], cap_head[NB][2], slope[NB][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+        for (int nb = 0; nb < NB; ++nb) {
+            float up = 1.0f;
+            if constexpr (F8) {
+                // To f16, by a power of two per head.
                 float amax = 0.0f;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-                    for (int i = h; i < 4; i += 2)
-                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(a[ks][i] << 16)),
-                                                 fabsf(__uint_as_float(a[ks][i] & 0xffff0000u))));
+                    for (int i = 0; i < 2; ++i)
+                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(qb[nb][ks][i] << 16)),
+                                                 fabsf(__uint_as_float(qb[nb][ks][i] & 0xffff0000u))));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 // 2^-e with amax in [2^e, 2^(e+1)); e within [-100, 120], and 0 for
-                // rows of zeros or with infinities (f16 keeps those).
+                // heads of zeros or with infinities (f16 keeps those).
                 int e = (int)(__float_as_uint(amax) >> 23) - 127;
                 e = amax == 0.0f || e > 127 ? 0 : min(max(e, -100), 120);
                 const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-                c_row[h] *= up;
-                cap_row[h] *= up;
+                up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-                    for (int i = h; i < 4; i += 2)
-                        a[ks][i] = pack_f16x2(__uint_as_float(a[ks][i] << 16) * down,
-                                              __uint_as_float(a[ks][i] & 0xffff0000u) * down);
+                    for (int i = 0; i < 2; ++i)
+                        qb[nb][ks][i] = pack_f16x2(__uint_as_float(qb[nb][ks][i] << 16) * down,
+                                                   __uint_as_float(qb[nb][ks][i] & 0xffff0000u) * down);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float f = F8 ? __shfl_sync(0xffffffffu, up, (2 * fc + i) * 4) : 1.0f;
+                c_head[nb][i] = p.scale_log2 * f;
+                cap_head[nb][i] = p.softcap_in * (2.0f * kLog2eF) * f;
+                const int r = 8 * nb + 2 * fc + i;
+                slope[nb][i] =
+                    p.alibi_slopes && r < rows ? __ldg(p.alibi_slopes + hq + r) * kLog2eF : 0.0f;
             }
         }
-        float slope[2] = {0.0f, 0.0f};
-        if (p.alibi_slopes) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (qr + 8 * h < rows) slope[h] = __ldg(p.alibi_slopes + hq + qr + 8 * h) * kLog2eF;
-        }
 
-        float acc[D / 8][4];
+        float acc[D / 16][NB][4];
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
+        for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, lr[2] = {0.0f, 0.0f};
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][nb][e] = 0.0f;
+        float m[NB][2], l[NB][2], lr[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) m[nb][i] = -INFINITY, l[nb][i] = lr[nb][i] = 0.0f;
 
         // This team's tiles of the pair.
         const uint32_t g0 = seg.g0;
@@ -511,135 +526,174 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
                 ok = __all_sync(0xffffffffu, wait_bounded(&sm.full[s], (g / kStages) & 1u, abort_flag, p.status));
             if (!ok) break;
             const int key0 = (t < st.ns ? t : st.w0 + t - st.ns) * kTile;
-            // S of the tile's keys, 8 per column block.
-            float x[kTile / 8][4];
+            // S^T of the tile: x[u][nb][2 h + i] is key key0 + 16 u + 8 h + fr, head
+            // 8 nb + 2 fc + i.  With one block of heads two chains per block of keys.
+            constexpr int kChains = NB == 1 ? 2 : 1;
+            float x[kBlocks][NB * kChains][4];
 #pragma unroll
-            for (int n = 0; n < kTile / 8; ++n)
+            for (int u = 0; u < kBlocks; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[n][e] = 0.0f;
+                for (int nb = 0; nb < NB * kChains; ++nb)
 #pragma unroll
-            for (int c = 0; c < kPieces; c += 4) {
-                uint32_t w[kTile / 8][4];
+                    for (int e = 0; e < 4; ++e) x[u][nb][e] = 0.0f;
 #pragma unroll
-                for (int n = 0; n < kTile / 8; ++n)
-                    ldsm4(w[n], smem_u32(sm.k[s][n / 2]) + head * Smem::kHeadBytes + (n & 1) * 8 * Smem::kPitch +
-                                    k_at[c / 4 % kKAt] + (c / 8) * Smem::kChunkBytes);
+            for (int c = 0; c < kPieces; c += 2) {
+                uint32_t w[kBlocks][4];
 #pragma unroll
-                for (int i = 0; i < (F8 ? 4 : 2); ++i)
+                for (int u = 0; u < kBlocks; ++u)
+                    ldsm4(w[u], smem_u32(sm.k[s][u]) + head * Smem::kHeadBytes + at[c / 2 % kAt] +
+                                    (c / 8) * Smem::kChunkBytes);
 #pragma unroll
-                    for (int n = 0; n < kTile / 8; ++n) {
-                        if constexpr (F8) {
-                            uint32_t b0, b1;
-                            widen_e4m3x4(w[n][i], b0, b1);
-                            mma16816<true>(x[n], a[c + i], b0, b1);
-                        } else {
-                            mma16816<false>(x[n], a[c / 2 + i], w[n][2 * i], w[n][2 * i + 1]);
+                for (int u = 0; u < kBlocks; ++u) {
+                    if constexpr (F8) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t a[4];
+                            widen_e4m3x4(w[u][2 * i], a[0], a[2]);
+                            widen_e4m3x4(w[u][2 * i + 1], a[1], a[3]);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+                                mma16816<true>(x[u][NB == 1 ? i : nb], a, qb[nb][c + i][0], qb[nb][c + i][1]);
                         }
+                    } else {
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+                            mma16816<false>(x[u][NB == 1 ? (c / 2) & 1 : nb], w[u], qb[nb][c / 2][0],
+                                            qb[nb][c / 2][1]);
                     }
+                }
             }
-            // x[n][2 h + i]: row qr + 8 h, key key0 + 8 n + 2 qc + i.  With a score
-            // modifier the scores become log2 units here, else in the exponent.
+            if constexpr (NB == 1) {
+#pragma unroll
+                for (int u = 0; u < kBlocks; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[u][0][e] += x[u][1][e];
+            }
+            // With a score modifier the scores become log2 units here, else in the
+            // exponent.
             if (modified) {
 #pragma unroll
-                for (int n = 0; n < kTile / 8; ++n)
+                for (int u = 0; u < kBlocks; ++u)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float &x0 = x[n][2 * h], &x1 = x[n][2 * h + 1];
-                        if (p.softcap_out > 0.0f) {
-                            float r0, r1;
-                            softcap_pair(x0, x1, r0, r1, x0, x1, cap_row[h], p.softcap_out);
-                        } else {
-                            x0 *= c_row[h];
-                            x1 *= c_row[h];
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float &x0 = x[u][nb][i], &x1 = x[u][nb][2 + i];
+                            if (p.softcap_out > 0.0f) {
+                                float r0, r1;
+                                softcap_pair(x0, x1, r0, r1, x0, x1, cap_head[nb][i], p.softcap_out);
+                            } else {
+                                x0 *= c_head[nb][i];
+                                x1 *= c_head[nb][i];
+                            }
+                            const float dist = (float)(st.len - 1 - (key0 + 16 * u + fr));
+                            x0 = fmaf(-slope[nb][i], dist, x0);
+                            x1 = fmaf(-slope[nb][i], dist - 8.0f, x1);
                         }
-                        const float dist = (float)(st.len - 1 - (key0 + 8 * n + 2 * qc));
-                        x0 = fmaf(-slope[h], dist, x0);
-                        x1 = fmaf(-slope[h], dist - 1.0f, x1);
-                    }
             }
             // Keys that the mask hides: their scores become -inf and their values
-            // zero, so what lies in them (NaN too) has no part.
-            uint32_t see[kTile / 8];
+            // zero, so what lies in them (NaN too) has no part.  see: the keys 16 u +
+            // 8 h + 2 fc + (0, 1), whose values this lane holds, as halves of a word.
+            uint32_t see[kBlocks][2];
             const bool masked =
                 key0 + kTile > st.len || (key0 < st.lo && key0 + kTile > p.sinks);
             if (masked) {
+                auto visible = [&](int key) {
+                    return key < st.len && (key >= st.lo || key < p.sinks);
+                };
 #pragma unroll
-                for (int n = 0; n < kTile / 8; ++n) {
-                    see[n] = 0u;
+                for (int u = 0; u < kBlocks; ++u)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int key = key0 + 8 * n + 2 * qc + i;
-                        if (key < st.len && (key >= st.lo || key < p.sinks))
-                            see[n] |= i ? 0xffff0000u : 0xffffu;
-                        else
-                            x[n][i] = x[n][2 + i] = -INFINITY;
+                    for (int h = 0; h < 2; ++h) {
+                        const int first = key0 + 16 * u + 8 * h;
+                        see[u][h] = (visible(first + 2 * fc) ? 0xffffu : 0u) |
+                                    (visible(first + 2 * fc + 1) ? 0xffff0000u : 0u);
+                        if (!visible(first + fr)) {
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) x[u][nb][2 * h] = x[u][nb][2 * h + 1] = -INFINITY;
+                        }
                     }
+            }
+            uint32_t pt[kBlocks][NB][2];  // P^T as the B operand
+            float alpha[NB][2];
+            bool moved = false;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                float neg_m[2], c[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    c[i] = modified ? 1.0f : c_head[nb][i];
+                    float mx = fmaxf(x[0][nb][i], x[0][nb][2 + i]);
+#pragma unroll
+                    for (int u = 1; u < kBlocks; ++u) mx = fmax3(mx, x[u][nb][i], x[u][nb][2 + i]);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    mx *= c[i];
+                    alpha[nb][i] = 1.0f;
+                    if (mx > m[nb][i] + kDecTau) {
+                        alpha[nb][i] = ex2_mufu(m[nb][i] - mx);
+                        m[nb][i] = mx;
+                        moved = true;
+                    }
+                    neg_m[i] = m[nb][i] == -INFINITY ? 0.0f : -m[nb][i];
+                }
+                float sum[2] = {0.0f, 0.0f}, rounded[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int u = 0; u < kBlocks; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float e0 = ex2_mufu(fmaf(x[u][nb][2 * h], c[0], neg_m[0]));
+                        const float e1 = ex2_mufu(fmaf(x[u][nb][2 * h + 1], c[1], neg_m[1]));
+                        sum[0] += e0;
+                        sum[1] += e1;
+                        pt[u][nb][h] = transpose8x8(pack_weights<F8>(e0, e1, rounded[0], rounded[1]));
+                    }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    l[nb][i] = fmaf(l[nb][i], alpha[nb][i], sum[i]);
+                    lr[nb][i] = fmaf(lr[nb][i], alpha[nb][i], rounded[i]);
                 }
             }
-            uint32_t pa[kBlocks][4];
-            float alpha[2];
+            if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float c = modified ? 1.0f : c_row[h];
-                float mx = fmaxf(x[0][2 * h], x[0][2 * h + 1]);
+                for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-                for (int n = 1; n < kTile / 8; ++n) mx = fmax3(mx, x[n][2 * h], x[n][2 * h + 1]);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * c;
-                alpha[h] = 1.0f;
-                if (mx > m[h] + kDecTau) {
-                    alpha[h] = ex2_mufu(m[h] - mx);
-                    m[h] = mx;
-                }
-                const float neg_m = m[h] == -INFINITY ? 0.0f : -m[h];
-                float sum = 0.0f, rounded = 0.0f;
+                    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int n = 0; n < kTile / 8; ++n) {
-                    const float e0 = ex2_mufu(fmaf(x[n][2 * h], c, neg_m));
-                    const float e1 = ex2_mufu(fmaf(x[n][2 * h + 1], c, neg_m));
-                    sum += e0 + e1;
-                    pa[n / 2][(n & 1) * 2 + h] = pack_weights<F8>(e0, e1, rounded);
-                }
-                l[h] = fmaf(l[h], alpha[h], sum);
-                lr[h] = fmaf(lr[h], alpha[h], rounded);
+                        for (int e = 0; e < 4; ++e) acc[j][nb][e] *= alpha[nb][e & 1];
             }
-            if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    acc[j][0] *= alpha[0];
-                    acc[j][1] *= alpha[0];
-                    acc[j][2] *= alpha[1];
-                    acc[j][3] *= alpha[1];
-                }
-            }
-            // O += P V.  bf16: acc[j] is values 8 j ..; e4m3: acc[2 j] the even and
-            // acc[2 j + 1] the odd values of 16 j ...  Boxes behind the sequence's
-            // end were not copied: `see` hides what is left in them.
+            // O^T += V^T P^T.  acc[j][nb][i] and [2 + i]: head 8 nb + 2 fc + i, values
+            // (bf16) 16 j + fr and 16 j + 8 + fr, or (e4m3, whose words hold value
+            // pairs) 16 j + 2 fr and 16 j + 2 fr + 1.  Boxes behind the sequence's end
+            // were not copied: `see` hides what is left in them.
 #pragma unroll
             for (int u = 0; u < kBlocks; ++u) {
                 const uint32_t vb = smem_u32(sm.v[s][u]) + head * Smem::kHeadBytes;
 #pragma unroll
                 for (int j = 0; j < kPieces; j += 2) {
                     uint32_t w[4];
-                    ldsm4_trans(w, vb + v_at[j / 2 % kVAt] + (j / 8) * Smem::kChunkBytes);
+                    ldsm4_trans(w, vb + at[j / 2 % kAt] + (j / 8) * Smem::kChunkBytes);
                     if (masked) {
-                        w[0] &= see[2 * u];
-                        w[1] &= see[2 * u + 1];
-                        w[2] &= see[2 * u];
-                        w[3] &= see[2 * u + 1];
+                        w[0] &= see[u][0];
+                        w[1] &= see[u][1];
+                        w[2] &= see[u][0];
+                        w[3] &= see[u][1];
                     }
                     if constexpr (F8) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            uint32_t e0, o0, e1, o1;
-                            widen_e4m3x4(__byte_perm(w[2 * i], 0u, 0x3120), e0, o0);
-                            widen_e4m3x4(__byte_perm(w[2 * i + 1], 0u, 0x3120), e1, o1);
-                            mma16816<true>(acc[2 * (j + i)], pa[u], e0, e1);
-                            mma16816<true>(acc[2 * (j + i) + 1], pa[u], o0, o1);
+                            uint32_t a[4];
+                            widen_e4m3x4(__byte_perm(w[2 * i], 0u, 0x3120), a[0], a[1]);
+                            widen_e4m3x4(__byte_perm(w[2 * i + 1], 0u, 0x3120), a[2], a[3]);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+                                mma16816<true>(acc[j + i][nb], a, pt[u][nb][0], pt[u][nb][1]);
                         }
                     } else {
-                        mma16816<false>(acc[j], pa[u], w[0], w[1]);
-                        mma16816<false>(acc[j + 1], pa[u], w[2], w[3]);
+                        const uint32_t a[4] = {w[0], w[2], w[1], w[3]};
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+                            mma16816<false>(acc[j / 2][nb], a, pt[u][nb][0], pt[u][nb][1]);
                     }
                 }
             }
@@ -650,40 +704,44 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
         more = next_segment(next);
         if (more) load_q(next);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-                lr[h] += __shfl_xor_sync(0xffffffffu, lr[h], o);
-            }
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], o);
+                    lr[nb][i] += __shfl_xor_sync(0xffffffffu, lr[nb][i], o);
+                }
         const bool whole = t0 == 0 && t1 == st.n;
         if (whole && t1 == 1) {
             // A pair of one tile is its team's alone: the team writes the output, and
             // the others are already at their next pair.
             if (team == (int)(g0 % kTeams)) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = qr + 8 * h;
-                    if (r >= rows) continue;
-                    const size_t row = (size_t)seg.b * p.Hq + hq + r;
-                    const float sum = F8 ? l[h] : lr[h];
-                    const float inv = sum == 0.0f ? 0.0f : p.v_descale / sum;
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int j = 0; j < D / 8; j += 2) {
-                        const float v0 = acc[j][2 * h] * inv, v1 = acc[j][2 * h + 1] * inv;
-                        const float v2 = acc[j + 1][2 * h] * inv, v3 = acc[j + 1][2 * h + 1] * inv;
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = 8 * nb + 2 * fc + i;
+                        if (r >= rows) continue;
+                        const size_t row = (size_t)seg.b * p.Hq + hq + r;
+                        const float sum = F8 ? l[nb][i] : lr[nb][i];
+                        const float inv = sum == 0.0f ? 0.0f : p.v_descale / sum;
                         __nv_bfloat16 *o = p.o + row * D;
-                        if constexpr (F8) {
-                            *reinterpret_cast<uint2 *>(o + 8 * j + 4 * qc) =
-                                make_uint2(pack_bf16x2(v0, v2), pack_bf16x2(v1, v3));
-                        } else {
-                            *reinterpret_cast<uint32_t *>(o + 8 * j + 2 * qc) = pack_bf16x2(v0, v1);
-                            *reinterpret_cast<uint32_t *>(o + 8 * j + 8 + 2 * qc) = pack_bf16x2(v2, v3);
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            const float v0 = acc[j][nb][i] * inv, v1 = acc[j][nb][2 + i] * inv;
+                            if constexpr (F8) {
+                                *reinterpret_cast<uint32_t *>(o + 16 * j + 2 * fr) = pack_bf16x2(v0, v1);
+                            } else {
+                                o[16 * j + fr] = __float2bfloat16_rn(v0);
+                                o[16 * j + 8 + fr] = __float2bfloat16_rn(v1);
+                            }
                         }
+                        if (fr == 0)
+                            p.lse[row] = l[nb][i] == 0.0f
+                                             ? -INFINITY
+                                             : (m[nb][i] + log2f(l[nb][i])) * 0.69314718055994531f;
                     }
-                    if (qc == 0)
-                        p.lse[row] = l[h] == 0.0f ? -INFINITY : (m[h] + log2f(l[h])) * 0.69314718055994531f;
-                }
             }
             continue;
         }
@@ -692,22 +750,24 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
         // Every warp comes here for every other pair, with or without a tile of it
         // (and after a wait that ran out), so the barriers below always meet.
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = qr + 8 * h;
-            if (r >= rows) continue;
-            if (qc == 0) sm.ml[warp][r] = make_float4(m[h], l[h], F8 ? l[h] : lr[h], 0.0f);
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-                if constexpr (F8) {
-                    float *dst = &sm.o[warp][r][16 * (j >> 1) + 4 * qc + (j & 1)];
-                    dst[0] = acc[j][2 * h];
-                    dst[2] = acc[j][2 * h + 1];
-                } else {
-                    *reinterpret_cast<float2 *>(&sm.o[warp][r][8 * j + 2 * qc]) =
-                        make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * nb + 2 * fc + i;
+                if (r >= rows) continue;
+                if (fr == 0)
+                    sm.ml[warp][r] = make_float4(m[nb][i], l[nb][i], F8 ? l[nb][i] : lr[nb][i], 0.0f);
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    if constexpr (F8) {
+                        *reinterpret_cast<float2 *>(&sm.o[warp][r][16 * j + 2 * fr]) =
+                            make_float2(acc[j][nb][i], acc[j][nb][2 + i]);
+                    } else {
+                        sm.o[warp][r][16 * j + fr] = acc[j][nb][i];
+                        sm.o[warp][r][16 * j + 8 + fr] = acc[j][nb][2 + i];
+                    }
                 }
             }
-        }
         const size_t part = (size_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0);
         named_bar_sync(1, kDecWarps * 32);
         for (int i = threadIdx.x; i < kHeads * rows * (D / 4); i += kDecWarps * 32) {

@@ -163,13 +163,13 @@ attn_status_t make_cache_map(CUtensorMap *map, const void *base, int pages, int 
     return ATTN_OK;
 }
 
-template <int D, bool F8, int kHeads, int kBlocks, int kStages>
-attn_status_t launch_decode(tab::DecodeParams &p, const void *k_cache, const void *v_cache,
+template <int D, bool F8, int kHeads, int NB, int kBlocks, int kStages>
+attn_status_t launch_decode_nb(tab::DecodeParams &p, const void *k_cache, const void *v_cache,
                             int blocks, cudaStream_t stream) {
-    using Smem = tab::DecodeSmem<D, F8, kHeads, kBlocks, kStages>;
+    using Smem = tab::DecodeSmem<D, F8, kHeads, NB, kBlocks, kStages>;
     constexpr size_t smem = sizeof(Smem) + 1024;
     static_assert(tab::kDecCtasPerSm * (smem + 1024) <= 233472, "shared memory budget");
-    auto kernel = tab::decode_paged_kernel<D, F8, kHeads, kBlocks, kStages>;
+    auto kernel = tab::decode_paged_kernel<D, F8, kHeads, NB, kBlocks, kStages>;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr_err[kMaxDevices];
     static cudaFuncAttributes attrs[kMaxDevices];
@@ -200,8 +200,16 @@ attn_status_t launch_decode(tab::DecodeParams &p, const void *k_cache, const voi
         return s;
     const tab::JoinParams jp = {p.part_o, p.part_ml, p.record, p.o, p.lse, p.Hq, p.group, p.v_descale};
     return launch_dependent(tab::decode_join_kernel<D, kHeads>,
-                            dim3(blocks, std::min(p.group, tab::kDecRows), kHeads),
+                            dim3(blocks, std::min(p.group, Smem::kRows), kHeads),
                             dim3(tab::kJoinThreads), stream, 0, jp);
+}
+
+// One block of 8 query heads where that holds a key head's, else two.
+template <int D, bool F8, int kHeads, int kBlocks, int kStages>
+attn_status_t launch_decode(tab::DecodeParams &p, const void *k_cache, const void *v_cache,
+                            int blocks, cudaStream_t stream) {
+    return p.group <= 8 ? launch_decode_nb<D, F8, kHeads, 1, kBlocks, kStages>(p, k_cache, v_cache, blocks, stream)
+                        : launch_decode_nb<D, F8, kHeads, 2, kBlocks, kStages>(p, k_cache, v_cache, blocks, stream);
 }
 
 // The variant by the bytes of a key's head: pairs of as many key heads as make
