@@ -443,13 +443,14 @@ ATTN_API attn_status_t attn_qk_norm_rope_cache(
 
 /*
  * Decode: attention of one new token per sequence over a paged cache.
- *   q, o      bf16 [B][Hq][D]
+ *   q, o      bf16 [B][Hq][D], not overlapping
  *   k_cache, v_cache  [num_pages][page_size][Hkv][D], kv_dtype as above
  *   seq_lens  int32 [B]: keys of each sequence, the new token's own (already
  *             in the cache) counted; may be 0
  *   page_table int32 [B][max_pages]: key j of sequence b is in page
  *             page_table[b][j / page_size], place j % page_size; entries
- *             behind the sequence's last page are not read
+ *             of pages without a visible key (behind the sequence's end, or
+ *             outside a window) are not used
  *   lse       fp32 [B][Hq]
  * With i = seq_lens[b] - 1, key j <= i is visible iff window_left is -1, or
  * j >= i - window_left, or j < sinks (first tokens that stay visible).
@@ -458,8 +459,8 @@ ATTN_API attn_status_t attn_qk_norm_rope_cache(
  * O = 0 and LSE = -inf.  What lies in the caches at hidden places (behind a
  * sequence's end, in pages of others) has no part in the result, NaN
  * included.  page_size is a multiple of 16; Hq % Hkv == 0; D is 64 or 128.
- * A length outside [0, max_pages * page_size] is clamped, a page outside
- * [0, num_pages) is replaced by page 0 (that sequence's results are then
+ * A length outside [0, max_pages * page_size] is clamped, a page (of
+ * visible keys) outside [0, num_pages) is replaced by page 0 (that sequence's results are then
  * unspecified); both report ATTN_ERR_RANGE.  workspace: at least
  * attn_decode_paged_workspace_size(D) bytes, 16-byte aligned (contents on
  * entry ignored; calls that may run at the same time need one each).  The

@@ -146,6 +146,27 @@ def test_windows_and_sinks(window, sinks, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_pages_outside_a_window_may_be_given_away(dtype, D):
+    """Entries of pages without a visible key are out of range: unused and not
+    reported; the pages' old places hold NaN."""
+    for heads in ((4, 1), (8, 4)):
+        lens, window, sinks, page = [1000, 330, 95, 16, 47], 70, 18, 16
+        t = problem(lens, *heads, D, page, dtype, seed=D)
+        for b, n in enumerate(lens):
+            for i in range(-(-n // page)):
+                if i * page >= sinks and i * page + page <= n - 1 - window:
+                    old = int(t["table"][b, i])
+                    for c in ("kc", "vc"):
+                        t[c][old] = torch.full_like(t[c][old].float(), float("nan")).to(dtype)
+                    t["table"][b, i] = -1 - i
+        got = run(t, window=(window, 0), sinks=sinks)
+        assert attn.device_status() == attn.ATTN_OK
+        t["table"] = t["table"].clamp_min(0)  # (the reference never looks at those keys)
+        check(t, got, scale=D ** -0.5, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
 def test_score_modifiers_and_scale(dtype):
     slopes = 2.0 ** -torch.arange(1, 9).float()
     t = problem([1, 300, 77], 8, 2, 128, 16, dtype, seed=40, q_std=3.0)

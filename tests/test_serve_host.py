@@ -75,7 +75,7 @@ def test_norm_bwd_refusals(L, kw, status):
 
 
 def call_decode(L, **kw):
-    a = dict(q=P, kc=P, vc=P, kv=0, kd=1.0, vd=1.0, table=P, lens=P, o=P, lse=P, B=2, Hq=4, Hkv=2, D=128, pages=8,
+    a = dict(q=P, kc=P, vc=P, kv=0, kd=1.0, vd=1.0, table=P, lens=P, o=2 * P, lse=P, B=2, Hq=4, Hkv=2, D=128, pages=8,
              page=16, width=4, scale=0.1, wl=-1, sinks=0, cap=0.0, slopes=None, ws=P, wsb=1 << 24)
     a.update(kw)
     return L.attn_decode_paged(a["q"], a["kc"], a["vc"], a["kv"], a["kd"], a["vd"], a["table"], a["lens"], a["o"],
@@ -86,7 +86,7 @@ def call_decode(L, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(q=0), INV), (dict(kc=0), INV), (dict(table=0), INV), (dict(lens=0), INV), (dict(lse=0), INV),
     (dict(ws=0), INV), (dict(wsb=100), INV), (dict(q=P + 8), MIS), (dict(vc=P + 4), MIS), (dict(table=P + 2), MIS),
-    (dict(slopes=P + 2), MIS), (dict(B=0), INV), (dict(Hq=3), INV), (dict(pages=0), INV), (dict(width=0), INV),
+    (dict(o=P), INV), (dict(slopes=P + 2), MIS), (dict(B=0), INV), (dict(Hq=3), INV), (dict(pages=0), INV), (dict(width=0), INV),
     (dict(D=96), UNS), (dict(page=8), UNS), (dict(page=24), UNS), (dict(page=0), UNS), (dict(kv=3), INV),
     (dict(kd=2.0), INV), (dict(kv=1, vd=-1.0), INV), (dict(scale=0.0), INV), (dict(scale=float("nan")), INV),
     (dict(wl=-2), INV), (dict(sinks=-1), INV), (dict(cap=-1.0), INV), (dict(cap=float("inf")), INV),

@@ -223,6 +223,7 @@ def attn_fwd(q, k, v, o, lse, *, scale, causal=False, window=None, doc_offsets=N
     stay visible beside the window (no document mask then).
     """
     _check_sinks(sinks, doc_offsets)
+    sinks = min(sinks, k.shape[1])
     for name, t, dt in (("q", q, torch.bfloat16), ("k", k, torch.bfloat16),
                         ("v", v, torch.bfloat16), ("o", o, torch.bfloat16),
                         ("lse", lse, torch.float32)):
@@ -463,6 +464,7 @@ def attn_bwd(q, k, v, o, lse, dout, dq, dk, dv, workspace, *, scale, causal=Fals
     bwd_workspace_size() bytes.  softcap / alibi_slopes / sinks must match the
     forward that produced o and lse."""
     _check_sinks(sinks, doc_offsets)
+    sinks = min(sinks, k.shape[1])
     _check_bwd_tensors(q, k, v, o, lse, dout, dq, dk, dv)
     if not torch.is_tensor(workspace) or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
@@ -500,7 +502,7 @@ def attention_backward(q, k, v, o, lse, dout, *, scale=None, causal=False, windo
     dq = torch.empty(q.shape, dtype=torch.float32, device=q.device)
     dk = torch.empty_like(k)
     dv = torch.empty_like(v)
-    ws = torch.empty(bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D, max(sinks, 0)),
+    ws = torch.empty(bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D, min(max(sinks, 0), Sk)),
                      dtype=torch.uint8, device=q.device)
     if doc_offsets is not None and not torch.is_tensor(doc_offsets):
         doc_offsets = torch.as_tensor(doc_offsets, dtype=torch.int32)

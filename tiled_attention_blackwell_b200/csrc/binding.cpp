@@ -130,7 +130,8 @@ struct Norm {
     explicit Norm(PyObject *const *a)
         : q(tensor(a[0], "q")), k(tensor(a[1], "k")), qw(tensor(a[2], "q_weight")),
           kw(tensor(a[3], "k_weight")), cos(tensor(a[4], "cos")), sin(tensor(a[5], "sin")),
-          pos(tensor(a[6], "positions")), eps(number(a[7])), interleaved(PyObject_IsTrue(a[8]) == 1) {
+          pos(tensor(a[6], "positions")), eps(number(a[7])), interleaved(PyObject_IsTrue(a[8])) {
+        if (interleaved < 0) throw PythonError{};
         const int n = (int)q.dim();
         require(q.scalar_type() == kBF16 && n >= 3, "q", "a bf16 tensor [..., Hq, D]");
         require(k.scalar_type() == kBF16 && k.dim() == n && k.size(n - 1) == q.size(n - 1) &&

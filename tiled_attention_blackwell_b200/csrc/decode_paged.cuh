@@ -289,10 +289,11 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
         long long base = sm.base;
         int b = sm.b0;
         struct Item {
-            int page[kBlocks], row[kBlocks], head, blocks;
+            int page[kBlocks], row[kBlocks], head;  // page -1: no copy
         };
         auto look_up = [&](uint32_t i) {
             Item it{};
+            for (int u = 0; u < kBlocks; ++u) it.page[u] = -1;
             if (i >= n_mine) return it;
             const long long pos = start + w + (long long)i * kDecCopyWarps;
             SeqTiles st = seq_tiles<kTile>(p, b);
@@ -308,8 +309,9 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
 #pragma unroll
             for (int u = 0; u < kBlocks; ++u) {
                 const int key = key0 + u * kDecBlock;
-                if (key < st.len) {
-                    it.blocks = u + 1;
+                // Boxes without a visible key are not copied, nor their pages looked up (a
+                // cache may have given them to others).
+                if (key < st.len && (key + kDecBlock > st.lo || key < p.sinks)) {
                     const int page = key / p.page_size;
                     it.row[u] = key - page * p.page_size;
                     int at = __ldg(p.page_table + (size_t)b * p.max_pages + page);
@@ -334,8 +336,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
             const uint32_t n = min(32u, n_mine - i0);
             for (uint32_t i = 0; i < n; ++i) {
                 const int head = __shfl_sync(0xffffffffu, it.head, i);
-                const int blocks = __shfl_sync(0xffffffffu, it.blocks, i);
-                int page = 0, row = 0;
+                int page = -1, row = 0;
 #pragma unroll
                 for (int u = 0; u < kBlocks; ++u) {
                     const int pg = __shfl_sync(0xffffffffu, it.page[u], i);
@@ -348,7 +349,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
                                                           abort_flag, p.status));
                 if (!ok) break;
                 if (my_u < kBlocks) {
-                    if (my_u < blocks) {
+                    if (page >= 0) {
                         mbar_arrive_expect_tx(&sm.full[s], Smem::kBoxBytes);
                         tma_load_5d(my_v ? sm.v[s][my_u] : sm.k[s][my_u], my_v ? &p.tm_v : &p.tm_k,
                                     &sm.full[s], 0, row, 0, head, page);
@@ -664,8 +665,8 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
             }
             // O^T += V^T P^T.  acc[j][nb][i] and [2 + i]: head 8 nb + 2 fc + i, values
             // (bf16) 16 j + fr and 16 j + 8 + fr, or (e4m3, whose words hold value
-            // pairs) 16 j + 2 fr and 16 j + 2 fr + 1.  Boxes behind the sequence's end
-            // were not copied: `see` hides what is left in them.
+            // pairs) 16 j + 2 fr and 16 j + 2 fr + 1.  Boxes without a visible key were
+            // not copied: `see` hides what is left in them.
 #pragma unroll
             for (int u = 0; u < kBlocks; ++u) {
                 const uint32_t vb = smem_u32(sm.v[s][u]) + head * Smem::kHeadBytes;
@@ -830,51 +831,42 @@ template <int D, int kHeads>
 __global__ void __launch_bounds__(kJoinThreads)
 decode_join_kernel(const JoinParams p) {
     constexpr int kCols = D / 4, kParts = kJoinThreads / kCols;  // float4 columns, rows of threads
-    __shared__ float red[kJoinThreads / 32];
     __shared__ float4 sum_o[kParts][kCols];
-    __shared__ float2 sum_l[kParts];
+    __shared__ float4 sum_ml[kParts];
     wait_for_primary();
     const int4 rec = p.record[blockIdx.x];
     const int row = blockIdx.y, head = blockIdx.z;
     if (row >= rec.z) return;
     const int first = blockIdx.x, n = rec.w - first + 1;
-    auto part_row = [&](int i) {
-        return (((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * kHeads + head) * kDecRows + row;
-    };
-    float mx = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += kJoinThreads) mx = fmaxf(mx, p.part_ml[part_row(i)].x);
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane_id() == 0) red[warp_id()] = mx;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, red[w]);
     const int part = threadIdx.x / kCols, c = threadIdx.x % kCols;
+    // Each row of threads joins every kParts-th partial, in order, under a running
+    // maximum; then the rows' results, in order.
+    float mx = -INFINITY;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float2 l = make_float2(0.0f, 0.0f);
+    auto add = [&](const float4 &ml, const float4 &v) {
+        const float to = fmaxf(mx, ml.x);
+        const float f = mx == to ? 1.0f : mx == -INFINITY ? 0.0f : ex2_mufu(mx - to);
+        const float g = ml.x == to ? 1.0f : ml.x == -INFINITY ? 0.0f : ex2_mufu(ml.x - to);
+        mx = to;
+        l.x = fmaf(l.x, f, ml.y * g);
+        l.y = fmaf(l.y, f, ml.z * g);
+        o.x = fmaf(o.x, f, v.x * g);
+        o.y = fmaf(o.y, f, v.y * g);
+        o.z = fmaf(o.z, f, v.z * g);
+        o.w = fmaf(o.w, f, v.w * g);
+    };
 #pragma unroll 4
     for (int i = part; i < n; i += kParts) {
-        const float4 ml = p.part_ml[part_row(i)];
-        const float4 v = *reinterpret_cast<const float4 *>(p.part_o + part_row(i) * D + 4 * c);
-        const float f = ml.x == -INFINITY ? 0.0f : ex2_mufu(ml.x - mx);
-        l.x = fmaf(ml.y, f, l.x);
-        l.y = fmaf(ml.z, f, l.y);
-        o.x = fmaf(v.x, f, o.x);
-        o.y = fmaf(v.y, f, o.y);
-        o.z = fmaf(v.z, f, o.z);
-        o.w = fmaf(v.w, f, o.w);
+        const size_t at = (((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * kHeads + head) * kDecRows + row;
+        add(p.part_ml[at], *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * c));
     }
     sum_o[part][c] = o;
-    if (c == 0) sum_l[part] = l;
+    if (c == 0) sum_ml[part] = make_float4(mx, l.x, l.y, 0.0f);
     __syncthreads();
     if (part == 0) {
-        o = sum_o[0][c];
-        l = sum_l[0];
 #pragma unroll
-        for (int w = 1; w < kParts; ++w) {
-            const float4 v = sum_o[w][c];
-            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
-            l.x += sum_l[w].x, l.y += sum_l[w].y;
-        }
+        for (int w = 1; w < kParts; ++w) add(sum_ml[w], sum_o[w][c]);
         const size_t out = (size_t)rec.x * p.Hq + rec.y + head * p.group + row;
         const float inv = l.y == 0.0f ? 0.0f : p.v_descale / l.y;
         *reinterpret_cast<uint2 *>(p.o + out * D + 4 * c) =

@@ -439,6 +439,7 @@ attn_status_t attn_decode_paged(const void *q, const void *k_cache, const void *
             return fail(ATTN_ERR_MISALIGNED, "q, caches, o and workspace must be 16-byte aligned");
     }
     if (!page_table || !seq_lens || !lse) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+    if (q == o) return fail(ATTN_ERR_INVALID_ARG, "o must not be q: blocks that share a sequence read q late");
     if (!aligned4(page_table) || !aligned4(seq_lens) || !aligned4(lse) || !aligned4(alibi_slopes))
         return fail(ATTN_ERR_MISALIGNED, "page_table, seq_lens, lse, alibi_slopes must be 4-byte aligned");
     if (B < 1 || Hq < 1 || Hkv < 1 || num_pages < 1 || max_pages < 1)
@@ -465,7 +466,7 @@ attn_status_t attn_decode_paged(const void *q, const void *k_cache, const void *
     const int group = Hq / Hkv, hchunks = (group + tab::kDecRows - 1) / tab::kDecRows;
     const double keys = (double)max_pages * page_size;
     const double tiles = (keys / tab::kDecBlock + 1.0) * Hkv * hchunks;  // of one sequence, at most
-    if (keys > 2147483647.0 - 4096.0 || tiles > 2147483647.0 || tiles * B > 2147483647.0 * 256.0)
+    if (keys > 2147483647.0 - 4096.0 || tiles > 2147483647.0 || tiles * B > 2.0 * 2147483647.0)
         return fail(ATTN_ERR_UNSUPPORTED, "sequences too long for one call");
     if ((double)page_size * Hkv * D * 2.0 >= 1099511627776.0)
         return fail(ATTN_ERR_UNSUPPORTED, "pages too large for a TMA descriptor");
