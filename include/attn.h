@@ -151,11 +151,20 @@ ATTN_API attn_status_t attn_fwd_ex(const void *q, const void *k, const void *v, 
  * window_right) and j >= i + shift - window_left or j < sinks.  sinks >= 0;
  * without a window's lower end (window_left = -1) they change nothing.  The
  * other rules are those of attn_fwd_ex; there is no document mask.
+ * workspace: NULL, or device memory of at least
+ * attn_fwd_sinks_workspace_size() bytes, 16-byte aligned (contents on entry
+ * ignored).  With one, calls of few rows cut each row's keys into parts that
+ * run side by side and are joined; a size of 0 says that there would be none.
  */
+ATTN_API size_t attn_fwd_sinks_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                                              int causal, int window_left, int window_right,
+                                              int sinks);
+
 ATTN_API attn_status_t attn_fwd_sinks(const void *q, const void *k, const void *v, void *o,
                                       float *lse, int B, int Hq, int Hkv, int Sq, int Sk, int D,
                                       float scale, int causal, int window_left, int window_right,
-                                      int sinks, const attn_fwd_options_t *opts, void *stream);
+                                      int sinks, void *workspace, size_t workspace_bytes,
+                                      const attn_fwd_options_t *opts, void *stream);
 
 /*
  * Low-precision forward ("Hardware-Aware FP4 FlashAttention-4", "Precisión":

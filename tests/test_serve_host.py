@@ -207,10 +207,10 @@ def test_decode_binding_refuses(L, name, bad):
 
 def call_fwd_sinks(L, **kw):
     a = dict(q=P, k=P, v=P, o=P, lse=P, B=1, Hq=2, Hkv=2, Sq=16, Sk=16, D=128, scale=0.1, causal=1, wl=7, wr=-1,
-             sinks=4, opts=None)
+             sinks=4, ws=None, wsb=0, opts=None)
     a.update(kw)
     return L.attn_fwd_sinks(a["q"], a["k"], a["v"], a["o"], a["lse"], a["B"], a["Hq"], a["Hkv"], a["Sq"], a["Sk"],
-                            a["D"], a["scale"], a["causal"], a["wl"], a["wr"], a["sinks"],
+                            a["D"], a["scale"], a["causal"], a["wl"], a["wr"], a["sinks"], a["ws"], a["wsb"],
                             None if a["opts"] is None else ctypes.byref(a["opts"]), None)
 
 
@@ -230,6 +230,20 @@ def call_bwd_sinks(L, **kw):
 def test_sinks_refusals(L, call, kw, status):
     assert call(L, **kw) == status
     assert L.attn_last_error_detail().decode() != ""
+
+
+def test_sinks_forward_workspace(L):
+    # 777 queries of 8 heads are 4 x 8 items of 256 rows: 4 parts of two blocks or more each fill 148 SMs
+    need = attn.sinks_workspace_size(1, 8, 2, 777, 2345, 64, True, (500, 0), 130)
+    assert need == 3 * 777 * 8 * 65 * 4  # (500 + 256 + 130) / 128 + 1 = 7 blocks: 3 parts
+    assert attn.sinks_workspace_size(1, 8, 2, 777, 2345, 64, True, (5000, 0), 130) == 4 * 777 * 8 * 65 * 4
+    assert attn.sinks_workspace_size(2, 16, 16, 8192, 8192, 128, True, (1023, 0), 4) == 0  # fills the device
+    assert attn.sinks_workspace_size(1, 2, 2, 100, 200, 128, True, (10, 0), 4) == 0  # one block
+    assert attn.sinks_workspace_size(1, 8, 2, 777, 2345, 64, True, (-1, 0), 4) == 0
+    assert attn.sinks_workspace_size(1, 8, 2, 777, 2345, 64, True, (500, 0), 0) == 0
+    kw = dict(Hq=8, Sq=777, Sk=2345, D=64, wl=500, sinks=130, wsb=need)
+    assert call_fwd_sinks(L, **{**kw, "ws": P, "wsb": need - 1}) == INV
+    assert call_fwd_sinks(L, **{**kw, "ws": P + 4}) == MIS
 
 
 def test_sinks_workspace(L):

@@ -288,3 +288,45 @@ def test_a_training_step_of_the_whole_path():
     for got, want in ((o, out), (grad, xd.grad), (dqw, qwd.grad), (dkw, kwd.grad)):
         got, want = got.double().cpu(), want.detach()
         assert float((got - want).norm() / want.norm()) <= 4 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("shape", [(1, 2, 1, 1, 700, 128), (1, 8, 2, 777, 2345, 64), (1, 2, 2, 300, 2000, 128), (2, 3, 1, 130, 900, 64),
+                                   (1, 4, 4, 260, 100, 128)])
+@pytest.mark.parametrize("window,sinks,causal", [((900, 0), 4, True), ((260, 0), 300, True), ((100, 50), 130, False),
+                                                 ((400, -1), 7, False)])
+def test_parts_of_a_call_of_few_rows(shape, window, sinks, causal):
+    """With a workspace the keys are cut into parts; without, they are not:
+    both hold the forward's bound (a part's output is normalised in fp32 and
+    weighted by exp of its LSE less the row's, within 2^-18 in all)."""
+    B, Hq, Hkv, Sq, Sk, D = shape
+    t = make_tensors(B, Hq, Hkv, Sq, Sk, D, Sq + sinks)
+    g = {n: x.to(DEV) for n, x in t.items()}
+    see = visible(Sq, Sk, causal, window, sinks)
+    size = attn.sinks_workspace_size(B, Hq, Hkv, Sq, Sk, D, causal, window, min(sinks, Sk))
+    o, lse = torch.empty_like(g["q"]), torch.empty(B, Hq, Sq, device=DEV)
+    for ws in (None, torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV)) if size else (None,):
+        for out in (o, lse):
+            out.fill_(float("nan"))
+        attn.attn_fwd(g["q"], g["k"], g["v"], o, lse, scale=D ** -0.5, causal=causal, window=window, sinks=sinks,
+                      workspace=ws)
+        check_forward(t, o, lse, D ** -0.5, see)
+    again = attn.attention(g["q"], g["k"], g["v"], causal=causal, window=window, sinks=sinks)
+    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
+def test_parts_with_score_modifiers_and_captured():
+    slopes = 2.0 ** -torch.arange(2, 6).float()
+    t = make_tensors(1, 4, 2, 200, 1500, 128, 31, qk_std=1.5)
+    g = {n: x.to(DEV) for n, x in t.items()}
+    kw = dict(causal=True, window=(1000, 0), sinks=20, softcap=8.0, alibi_slopes=slopes.to(DEV))
+    assert attn.sinks_workspace_size(1, 4, 2, 200, 1500, 128, True, (1000, 0), 20) > 0
+    o, lse = attn.attention(g["q"], g["k"], g["v"], **kw)
+    check_forward(t, o, lse, 128 ** -0.5, visible(200, 1500, True, (1000, 0), 20), 8.0, slopes)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = attn.attention(g["q"], g["k"], g["v"], **kw)
+    for _ in range(2):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        assert torch.equal(got[0], o) and torch.equal(got[1], lse)

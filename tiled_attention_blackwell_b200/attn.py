@@ -41,7 +41,7 @@ ATTN_KV_E4M3 = 1
 
 EXPORTED = ("attn_fwd", "attn_fwd_ex", "attn_fwd_fp8", "attn_fwd_default_options",
             "attn_fp4_default_options", "attn_fwd_fp4_workspace_size", "attn_fwd_fp4", "attn_bwd",
-            "attn_bwd_ex", "attn_fwd_sinks", "attn_bwd_sinks", "attn_bwd_sinks_workspace_size",
+            "attn_bwd_ex", "attn_fwd_sinks", "attn_fwd_sinks_workspace_size", "attn_bwd_sinks", "attn_bwd_sinks_workspace_size",
             "attn_bwd_workspace_size", "attn_bwd_noalloc", "attn_qk_norm_rope",
             "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_size",
             "attn_qk_norm_rope_cache", "attn_decode_paged", "attn_decode_paged_workspace_size",
@@ -132,8 +132,12 @@ def lib():
             L.attn_bwd_ex.argtypes = L.attn_bwd.argtypes[:-1] + [ctypes.POINTER(BwdOptions),
                                                                  ctypes.c_void_p]
             L.attn_fwd_sinks.restype = ctypes.c_int
-            L.attn_fwd_sinks.argtypes = _FWD_ARGS[:-2] + [ctypes.c_int, ctypes.POINTER(FwdOptions),
+            L.attn_fwd_sinks.argtypes = _FWD_ARGS[:-2] + [ctypes.c_int, ctypes.c_void_p,
+                                                          ctypes.c_size_t,
+                                                          ctypes.POINTER(FwdOptions),
                                                           ctypes.c_void_p]
+            L.attn_fwd_sinks_workspace_size.restype = ctypes.c_size_t
+            L.attn_fwd_sinks_workspace_size.argtypes = [ctypes.c_int] * 10
             L.attn_bwd_sinks_workspace_size.restype = ctypes.c_size_t
             L.attn_bwd_sinks_workspace_size.argtypes = [ctypes.c_int] * 7
             L.attn_bwd_sinks.restype = ctypes.c_int
@@ -213,14 +217,15 @@ def _check_sinks(sinks, doc_offsets):
 
 
 def attn_fwd(q, k, v, o, lse, *, scale, causal=False, window=None, doc_offsets=None,
-             options=None, stream=None, softcap=None, alibi_slopes=None, sinks=0):
+             options=None, stream=None, softcap=None, alibi_slopes=None, sinks=0, workspace=None):
     """Enqueue the forward on `stream` (default: torch's current stream).
 
     q, o: bf16 CUDA [B,Sq,Hq,D]; k, v: bf16 CUDA [B,Sk,Hkv,D]; lse: fp32 CUDA
     [B,Hq,Sq]; doc_offsets: int32 CUDA [num_docs+1] or None.  All contiguous.
     softcap (> 0) and alibi_slopes (fp32 [Hq]) select the score modifiers;
     they override the same fields of `options`.  With `sinks` the first keys
-    stay visible beside the window (no document mask then).
+    stay visible beside the window (no document mask then); a workspace
+    (uint8, sinks_workspace_size()) lets calls of few rows run in parts.
     """
     _check_sinks(sinks, doc_offsets)
     sinks = min(sinks, k.shape[1])
@@ -256,7 +261,11 @@ def attn_fwd(q, k, v, o, lse, *, scale, causal=False, window=None, doc_offsets=N
                                ("o", o, (B, Sq, Hq, D)), ("lse", lse, (B, Hq, Sq))):
             if tuple(t.shape) != shape:
                 raise TypeError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-        st = L.attn_fwd_sinks(*args[:-2], int(sinks),
+        if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
+            raise TypeError("workspace must be a contiguous CUDA tensor")
+        ws = (None, 0) if workspace is None else \
+            (_ptr(workspace), workspace.numel() * workspace.element_size())
+        st = L.attn_fwd_sinks(*args[:-2], int(sinks), *ws,
                               None if options is None else ctypes.byref(options),
                               _stream_handle(stream))
     elif options is None:
@@ -264,6 +273,12 @@ def attn_fwd(q, k, v, o, lse, *, scale, causal=False, window=None, doc_offsets=N
     else:
         st = L.attn_fwd_ex(*args, ctypes.byref(options), _stream_handle(stream))
     _check(st, "attn_fwd")
+
+
+def sinks_workspace_size(B, Hq, Hkv, Sq, Sk, D, causal, window, sinks) -> int:
+    """Bytes of device workspace with which attn_fwd runs in parts (0: it would not)."""
+    return int(lib().attn_fwd_sinks_workspace_size(B, Hq, Hkv, Sq, Sk, D, int(bool(causal)),
+                                                   int(window[0]), int(window[1]), sinks))
 
 
 def attention(q, k, v, *, scale=None, causal=False, window=None, doc_offsets=None,
@@ -278,9 +293,17 @@ def attention(q, k, v, *, scale=None, causal=False, window=None, doc_offsets=Non
         doc_offsets = torch.as_tensor(doc_offsets, dtype=torch.int32)
     if doc_offsets is not None and not doc_offsets.is_cuda:
         doc_offsets = doc_offsets.to(q.device)
+    ws = None
+    if sinks > 0 and window is not None:
+        size = sinks_workspace_size(B, Hq, k.shape[2], Sq, k.shape[1], D, causal, window,
+                                    min(sinks, k.shape[1]))
+        if size:
+            ws = torch.empty(size, dtype=torch.uint8, device=q.device)
     attn_fwd(q, k, v, o, lse, scale=scale, causal=causal, window=window,
              doc_offsets=doc_offsets, options=options, stream=stream, softcap=softcap,
-             alibi_slopes=alibi_slopes, sinks=sinks)
+             alibi_slopes=alibi_slopes, sinks=sinks, workspace=ws)
+    if ws is not None:
+        _keep_for(stream, o, lse, ws)
     return o, lse
 
 

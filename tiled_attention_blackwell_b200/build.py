@@ -25,10 +25,10 @@ COUNT_LIB = os.path.join(PKG, "libattn_count.so")
 BINDING = os.path.join(PKG, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
-# attn_api.cu: the forward and backward; sinks.cu: their variants with first
+# attn_api.cu: the forward and backward; sinks_*.cu: their variants with first
 # keys beside a window; serve_api.cu: head norms with rotation, the paged cache
 # and its decode.
-UNITS = ("attn_api.cu", "sinks.cu", "serve_api.cu")
+UNITS = ("attn_api.cu", "sinks_fwd.cu", "sinks_parts.cu", "sinks_bwd.cu", "serve_api.cu")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

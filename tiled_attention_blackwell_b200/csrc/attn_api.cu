@@ -340,6 +340,22 @@ void attn_fwd_default_options(attn_fwd_options_t *opts) {
     opts->exp2_mode = 1;
 }
 
+// Parts that the key blocks of an item (256 query rows of a head) are cut into
+// (attn_fwd_sinks): as many as give every SM of the device a CTA, each with
+// two blocks at least.  A block takes about 2 us: a chunk of 777 queries of 8
+// heads, 32 items of 6 to 9 blocks, takes 23 us whole and 18 in three parts
+// with their join; items that fill the device are not cut.
+constexpr int kFwdPartCtas = 148;
+static int fwd_parts(int B, int Hq, int Sq, int Sk, int causal, int window_left, int window_right,
+                     int sinks) {
+    const long long items = (Sq + 2LL * tab::kBlockM - 1) / (2LL * tab::kBlockM) * Hq * B;
+    // Most keys that an item can see, in blocks.
+    long long keys = window_left + 2LL * tab::kBlockM + sinks;
+    if (!causal) keys = window_right < 0 ? Sk : keys + window_right;
+    const long long blocks = std::min((long long)Sk, keys) / tab::kBlockN + 1;
+    return (int)std::max(1LL, std::min(kFwdPartCtas / items, blocks / 2));
+}
+
 // The forward of both entry points.  fp8: Q, K, V are e4m3 codes with the
 // given dequantisation factors (ignored for bf16).
 static attn_status_t fwd_impl(const void *q, const void *k, const void *v, void *o, float *lse, int B,
@@ -347,7 +363,7 @@ static attn_status_t fwd_impl(const void *q, const void *k, const void *v, void 
                        int window_left, int window_right, const int *doc_offsets,
                        int num_docs, const attn_fwd_options_t *opts, bool fp8,
                        float q_descale, float k_descale, float v_descale, void *stream,
-                       int sinks = 0) {
+                       int sinks = 0, void *workspace = nullptr) {
     attn_fwd_options_t op;
     attn_fwd_default_options(&op);
     if (opts) op = *opts;
@@ -450,7 +466,11 @@ static attn_status_t fwd_impl(const void *q, const void *k, const void *v, void 
     // First keys matter only beside a window's lower end.
     if (sinks > 0 && window_left >= 0) {
         p.sinks = std::min(sinks, Sk);
-        return tab_host::dispatch_fwd_sinks(p, grid, D, op.exp2_mode, mod, cs);
+        p.parts = workspace ? fwd_parts(B, Hq, Sq, Sk, causal, window_left, window_right, sinks) : 1;
+        p.part_o = static_cast<float *>(workspace);
+        p.part_lse = p.part_o + (size_t)p.parts * B * Sq * Hq * D;
+        return p.parts > 1 ? tab_host::dispatch_fwd_parts(p, grid, D, op.exp2_mode, mod, cs)
+                           : tab_host::dispatch_fwd_sinks(p, grid, D, op.exp2_mode, mod, cs);
     }
     if (fp8) return dispatch_fp8(p, grid, op.exp2_mode, cs);
     if (D == 128) return dispatch_exp<128, kStagesD128>(p, grid, op.exp2_mode, mod, cs);
@@ -469,10 +489,26 @@ attn_status_t attn_fwd_ex(const void *q, const void *k, const void *v, void *o, 
 attn_status_t attn_fwd_sinks(const void *q, const void *k, const void *v, void *o, float *lse,
                              int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
                              int causal, int window_left, int window_right, int sinks,
+                             void *workspace, size_t workspace_bytes,
                              const attn_fwd_options_t *opts, void *stream) {
     if (sinks < 0) return fail(ATTN_ERR_INVALID_ARG, "sinks must be >= 0");
+    if (workspace) {
+        if (!aligned16(workspace)) return fail(ATTN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+        const size_t need = attn_fwd_sinks_workspace_size(B, Hq, Hkv, Sq, Sk, D, causal, window_left,
+                                                          window_right, sinks);
+        if (workspace_bytes < need)
+            return fail(ATTN_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    }
     return fwd_impl(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, scale, causal, window_left,
-                    window_right, nullptr, 0, opts, false, 1.0f, 1.0f, 1.0f, stream, sinks);
+                    window_right, nullptr, 0, opts, false, 1.0f, 1.0f, 1.0f, stream, sinks, workspace);
+}
+
+size_t attn_fwd_sinks_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal,
+                                     int window_left, int window_right, int sinks) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || Sq < 1 || Sk < 1 || D < 1 || window_left < 0 || window_right < -1 || sinks < 1)
+        return 0;
+    const size_t parts = fwd_parts(B, Hq, Sq, Sk, causal, window_left, window_right, sinks);
+    return parts == 1 ? 0 : parts * B * Sq * Hq * (D + 1) * sizeof(float);
 }
 
 attn_status_t attn_fwd_fp8(const void *q, const void *k, const void *v, float q_descale,

@@ -114,7 +114,11 @@ struct FwdParams {
     // V per 128-key block; two 512-byte atoms each) and the tile counts.
     const uint8_t *sf_q, *sf_k, *sf_v;
     int nq_tiles, nk_tiles;
-    int sinks;  // SINKS kernels: first keys that stay visible beside the window
+    // SINKS kernels: first keys that stay visible beside the window; parts that
+    // each item's key blocks are cut into (1: none), and the parts' results:
+    // fp32 O [part][B][Sq][Hq][D], each normalised, and LSE [part][B][Hq][Sq].
+    int sinks, parts;
+    float *part_o, *part_lse;
 };
 
 // Opt-in event trace (compile with -DATTN_TRACE): lane 0 of warps 0 and 4
@@ -175,6 +179,7 @@ struct FwdSmem {
     uint32_t tmem_base;
     int abort_flag;
     int range[2][2];  // per query tile: first and last key block (inclusive)
+    int item[3];      // SINKS = 2: batch, query head and part, for the epilogue
 };
 
 // Column pairs that use the polynomial in EXP_MODE 1: one pair in eight,
@@ -367,8 +372,11 @@ __device__ __forceinline__ void modify_scores(float *v, float c, float k1, float
 // the interval's upper end.  The blocks of a tile are then those of the first
 // keys and those of its window, at most two runs: the kernel walks the union
 // of both tiles' blocks under "virtual" indices in which the window's blocks
-// keep their own and the sb first blocks stand directly before them.
-template <int D, int NS, int EXP_MODE, int MOD = 0, int PREC = 0, bool SINKS = false>
+// keep their own and the sb first blocks stand directly before them.  SINKS =
+// 2, for few items: the walk is cut into parts, a CTA each, which
+// attn_fwd_join_kernel joins by their LSEs.  (A kernel of its own: the counts
+// of a part cost the full-size forward 4 %.)
+template <int D, int NS, int EXP_MODE, int MOD = 0, int PREC = 0, int SINKS = 0>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 attn_fwd_kernel(const __grid_constant__ FwdParams p) {
     static_assert(!(PREC && MOD), "the low-precision paths have no score modifiers");
@@ -392,7 +400,12 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
     const int G = p.head_group;
     const int nq = p.num_qblocks;
     const int full_groups = bh_count / G;
-    const int lin = (int)blockIdx.x;
+    int lin = (int)blockIdx.x, part = 0;
+    if constexpr (SINKS == 2) {
+        part = lin / (bh_count * nq);
+        lin -= part * bh_count * nq;
+        launch_dependents();
+    }
     int grp, r, ge;
     if (lin < full_groups * G * nq) {
         grp = lin / (G * nq);
@@ -425,6 +438,11 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
         }
         mbar_init(&sm.drain, 1);
         sm.abort_flag = 0;
+        if constexpr (SINKS == 2) {
+            sm.item[0] = b;
+            sm.item[1] = hq;
+            sm.item[2] = part;
+        }
         fence_mbar_init();
     }
     if (warp == 9) {
@@ -473,13 +491,34 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
     const int lo1 = sm.range[1][0], hi1 = sm.range[1][1];
     const bool has0 = lo0 <= hi0, has1 = lo1 <= hi1;
     const int wlo = has0 ? (has1 ? min(lo0, lo1) : lo0) : lo1;
-    const int uhi = has0 ? (has1 ? max(hi0, hi1) : hi0) : hi1;
+    const int uhi0 = has0 ? (has1 ? max(hi0, hi1) : hi0) : hi1;
     // Blocks with first keys; those before both tiles' windows come first.
     const int nsb = SINKS ? (p.sinks + kBlockN - 1) / kBlockN : 0;
-    const int ulo = SINKS ? wlo - min(nsb, wlo) : wlo;
-    const int n_blocks = (has0 || has1) ? (uhi - ulo + 1) : 0;
+    const int ulo0 = SINKS ? wlo - min(nsb, wlo) : wlo;
     // Key block of virtual index j.
-    auto block_of = [&](int j) -> int { return !SINKS || j >= wlo ? j : j - ulo; };
+    auto block_of = [&](int j) -> int { return !SINKS || j >= wlo ? j : j - ulo0; };
+    // This CTA's virtual indices [ulo, ulo + n_blocks), and per tile the number
+    // of its blocks before them (skip) and up to their end (upto).
+    int ulo = ulo0, n_blocks = (has0 || has1) ? (uhi0 - ulo0 + 1) : 0;
+    int skip0 = 0, skip1 = 0, upto0 = 0, upto1 = 0;
+    if constexpr (SINKS == 2) {
+        const int total = n_blocks;
+        ulo = ulo0 + (int)((long long)total * part / p.parts);
+        n_blocks = ulo0 + (int)((long long)total * (part + 1) / p.parts) - ulo;
+        // A tile's blocks with a virtual index below j: of its s first blocks,
+        // then of [lo, hi].
+        auto before = [&](bool has, int lo, int hi, int j) -> int {
+            if (!has) return 0;
+            const int s = min(nsb, lo);
+            if (j <= wlo) return min(j - ulo0, s);
+            return min(s, j) + max(0, min(j, hi + 1) - lo);
+        };
+        skip0 = before(has0, lo0, hi0, ulo);
+        skip1 = before(has1, lo1, hi1, ulo);
+        upto0 = before(has0, lo0, hi0, ulo + n_blocks);
+        upto1 = before(has1, lo1, hi1, ulo + n_blocks);
+    }
+    const int uhi = ulo + n_blocks - 1;
 
     // Registers: the softmax warpgroups hold a 128-column score row per
     // thread; the MMA / TMA warpgroup needs few.  384 x 168 at launch =
@@ -613,7 +652,10 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                             if constexpr (SINKS) {
                                 const int kb = block_of(j), s_i = min(nsb, lo_i);
                                 nth = kb < s_i ? kb : kb - lo_i + s_i;
+                                if (SINKS == 2) nth -= i == 0 ? skip0 : skip1;
                             }
+                            const bool last =
+                                SINKS == 2 ? nth == (i == 0 ? upto0 - skip0 : upto1 - skip1) - 1 : j == hi_i;
                             const uint32_t par = (uint32_t)nth & 1u;
                             const uint32_t o_tmem = tmem + 2 * kBlockN + i * D;
                             const uint32_t p_tmem = tmem + i * kBlockN;
@@ -644,7 +686,7 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                                 for (int ks = kPvSteps; ks < 2 * kPvSteps; ++ks)
                                     mma_ts_k<FP8>(o_tmem, p_tmem + ks * 8,
                                                   vb + ((ks * kPvK * 128) >> 4), kIdescPV, 1u);
-                                if (j == hi_i) tc_commit(&sm.o_final[i]);
+                                if (last) tc_commit(&sm.o_final[i]);
                             }
                             __syncwarp();
                         }
@@ -701,9 +743,11 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
         float l_pv = 0.0f;    // row sum of the p that PV consumes (the output's normaliser)
         bool ok = true;
 
-        for (int jj = lo_b - s_b; jj <= hi_b; ++jj) {
-            const int t = jj - (lo_b - s_b);
-            const int j = !SINKS || jj >= lo_b ? jj : t;
+        // The tile's blocks (SINKS = 2: skip .. upto - 1 of them), in its order.
+        const int skip = i == 0 ? skip0 : skip1;
+        const int blocks = SINKS == 2 ? (i == 0 ? upto0 : upto1) - skip : hi_b - lo_b + 1 + s_b;
+        for (int t = 0; t < blocks; ++t) {
+            const int j = !SINKS || t + skip >= s_b ? lo_b - s_b + skip + t : skip + t;
             if ((warp & 3) == 0) ATTN_TRACE_EVENT(i, t, 0);
             ok = wait_bounded(&sm.s_full[i], (uint32_t)t & 1u, abort_flag, p.status, true, p.timeout_ns);
             ok = __all_sync(0xffffffffu, ok);
@@ -919,7 +963,7 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
         }
 
         // ----------------------------------------------------------- epilogue
-        const bool has_blocks = lo_b <= hi_b;
+        const bool has_blocks = blocks > 0;
         if (ok && has_blocks) {
             ok = wait_bounded(&sm.o_final[i], 0, abort_flag, p.status, true, p.timeout_ns);
             ok = __all_sync(0xffffffffu, ok);
@@ -932,8 +976,12 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
             // it; Direct-P's sum is already over the values PV consumes).
             const float l_out = PREC ? l_run : l_pv;
             const float inv_l = l_out > 0.0f ? (PREC ? p.v_descale : 1.0f) / l_out : 0.0f;
+            // (SINKS = 2: from shared memory, so that no register holds them till here.)
+            const int eb = SINKS == 2 ? *(volatile int *)&sm.item[0] : b;
+            const int eh = SINKS == 2 ? *(volatile int *)&sm.item[1] : hq;
+            const int ep = SINKS == 2 ? *(volatile int *)&sm.item[2] : 0;
             __nv_bfloat16 *o_row =
-                p.o + (((size_t)b * p.Sq + row) * p.Hq + hq) * (size_t)D;
+                p.o + (((size_t)eb * p.Sq + row) * p.Hq + eh) * (size_t)D;
 #pragma unroll
             for (int ch = 0; ch < D / 32; ++ch) {
                 uint32_t r[32];
@@ -951,7 +999,17 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                 for (int e = 0; e < 16; ++e)
                     w[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * inv_l,
                                        __uint_as_float(r[2 * e + 1]) * inv_l);
-                if (row_ok) {
+                if (SINKS == 2) {
+                    if (row_ok) {
+                        float4 *dst = reinterpret_cast<float4 *>(
+                            p.part_o + ((((size_t)ep * p.B + eb) * p.Sq + row) * p.Hq + eh) * (size_t)D + ch * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_float4(__uint_as_float(r[4 * e]) * inv_l, __uint_as_float(r[4 * e + 1]) * inv_l,
+                                                 __uint_as_float(r[4 * e + 2]) * inv_l,
+                                                 __uint_as_float(r[4 * e + 3]) * inv_l);
+                    }
+                } else if (row_ok) {
                     uint4 *dst = reinterpret_cast<uint4 *>(o_row + ch * 32);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) dst[e] = out[e];
@@ -961,7 +1019,8 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                 const float m_lse = PREC ? m_run - p.p_offset : m_run;
                 const float lse = l_run > 0.0f ? (m_lse + log2f(l_run)) * 0.69314718055994531f
                                                : -INFINITY;
-                p.lse[((size_t)b * p.Hq + hq) * p.Sq + row] = lse;
+                float *dst = SINKS == 2 ? p.part_lse + (size_t)ep * p.B * p.Hq * p.Sq : p.lse;
+                dst[((size_t)eb * p.Hq + eh) * p.Sq + row] = lse;
             }
         }
 #ifdef ATTN_COUNT_RESCALES
@@ -988,6 +1047,42 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+}
+
+// Joins the parts of attn_fwd_kernel<..., SINKS = 2>: O = sum_s w_s O_s, w_s =
+// exp(LSE_s - LSE).  D / 4 lanes per row of O; the parts in order.
+constexpr int kFwdJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kFwdJoinThreads)
+attn_fwd_join_kernel(const __grid_constant__ FwdParams p) {
+    constexpr int kLanes = D / 4;
+    wait_for_primary();
+    const long long rows = (long long)p.B * p.Sq * p.Hq;
+    const long long r = (long long)blockIdx.x * (kFwdJoinThreads / kLanes) + threadIdx.x / kLanes;
+    const int d = (threadIdx.x % kLanes) * 4;
+    if (r >= rows) return;
+    const int hq = (int)(r % p.Hq), row = (int)(r / p.Hq % p.Sq), b = (int)(r / p.Hq / p.Sq);
+    const size_t at = ((size_t)b * p.Hq + hq) * p.Sq + row;
+    const size_t lses = (size_t)p.B * p.Hq * p.Sq;
+    float m = -INFINITY;
+    for (int s = 0; s < p.parts; ++s) m = fmaxf(m, p.part_lse[s * lses + at]);
+    float sum = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = 0; s < p.parts; ++s) {
+        const float l = p.part_lse[s * lses + at];
+        const float4 v = *reinterpret_cast<const float4 *>(p.part_o + ((size_t)s * rows + r) * D + d);
+        if (l == -INFINITY) continue;  // no key of this part
+        const float w = ex2_mufu((l - m) * kLog2eF);
+        sum += w;
+        o.x = fmaf(v.x, w, o.x);
+        o.y = fmaf(v.y, w, o.y);
+        o.z = fmaf(v.z, w, o.z);
+        o.w = fmaf(v.w, w, o.w);
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    *reinterpret_cast<uint2 *>(p.o + (size_t)r * D + d) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (d == 0) p.lse[at] = sum == 0.0f ? -INFINITY : m + log2f(sum) * 0.69314718055994531f;
 }
 
 }  // namespace tab

@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <string.h>
+
 #include <mutex>
 
 #include "../../include/attn.h"
@@ -34,6 +36,29 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 // The driver's cuTensorMapEncodeTiled, or null.
 EncodeTiledFn encode_fn();
+
+// Launches `kernel` so that its blocks may start while what stands before it in
+// the stream ends; the kernel waits for that end (wait_for_primary()) before
+// it touches memory.
+template <class... Args>
+attn_status_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 threads, cudaStream_t stream, size_t smem,
+                                const Args &...args) {
+    cudaLaunchAttribute attr;
+    memset(&attr, 0, sizeof attr);
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config;
+    memset(&config, 0, sizeof config);
+    config.gridDim = grid;
+    config.blockDim = threads;
+    config.dynamicSmemBytes = smem;
+    config.stream = stream;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&config, kernel, args...);
+    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
+    return ok();
+}
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }

@@ -11,8 +11,12 @@
 
 namespace tab_host {
 
-// sinks.cu: SINKS variants of the forward (one CTA per item) and the backward.
+// The SINKS variants of the forward (one CTA per item, or p.parts of them)
+// and the backward, in translation units of their own: they compile side by
+// side.  sinks_fwd.cu, sinks_parts.cu, sinks_bwd.cu
 attn_status_t dispatch_fwd_sinks(const tab::FwdParams &p, int grid, int D, int exp_mode, int mod,
+                                 cudaStream_t stream);
+attn_status_t dispatch_fwd_parts(const tab::FwdParams &p, int grid, int D, int exp_mode, int mod,
                                  cudaStream_t stream);
 attn_status_t dispatch_bwd_sinks(const tab::BwdParams &p, int D, int mod, cudaStream_t stream);
 
@@ -27,7 +31,7 @@ using tab_host::ok;
 // PERSIST selects the persistent kernel (fwd_persistent.cuh: one CTA per SM
 // running many items), otherwise one CTA per item.
 template <int D, int NS, int EXP, int MOD = 0, int PREC = 0, bool PERSIST = false,
-          bool SINKS = false>
+          int SINKS = 0>
 attn_status_t launch_fwd(const tab::FwdParams &p, int grid, cudaStream_t stream) {
     using Smem = std::conditional_t<PERSIST, tab::FwdSmemPersistent<D, NS, PREC == 1 ? 1 : 2>,
                                     tab::FwdSmem<D, NS, PREC == 1 ? 1 : 2>>;
@@ -68,7 +72,7 @@ attn_status_t launch_fwd(const tab::FwdParams &p, int grid, cudaStream_t stream)
 constexpr int kStagesD128 = 4;
 constexpr int kStagesD64 = 8;
 
-template <int D, int NS, bool SINKS = false>
+template <int D, int NS, int SINKS = 0>
 attn_status_t dispatch_exp(const tab::FwdParams &p, int grid, int exp_mode, int mod,
                            cudaStream_t s) {
     // With a score modifier the exponentials all run on MUFU.

@@ -20,34 +20,12 @@ using tab_host::DeviceState;
 using tab_host::encode_fn;
 using tab_host::fail;
 using tab_host::kMaxDevices;
+using tab_host::launch_dependent;
 using tab_host::ok;
 
 namespace {
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-
-// Launches `kernel` so that its blocks may start while what stands before it in
-// the stream ends; the kernel waits for that end (wait_for_primary()) before
-// it touches memory.
-template <class... Args>
-attn_status_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 threads, cudaStream_t stream,
-                               size_t smem, const Args &...args) {
-    cudaLaunchAttribute attr;
-    memset(&attr, 0, sizeof attr);
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t config;
-    memset(&config, 0, sizeof config);
-    config.gridDim = grid;
-    config.blockDim = threads;
-    config.dynamicSmemBytes = smem;
-    config.stream = stream;
-    config.attrs = &attr;
-    config.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&config, kernel, args...);
-    if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
-    return ok();
-}
 
 // ------------------------------------------------------------- norm + rope
 
