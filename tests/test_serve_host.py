@@ -259,6 +259,31 @@ def test_sinks_workspace(L):
     assert call_bwd_sinks(L, wsb=need - 1) == INV
 
 
+@pytest.mark.parametrize("name,bad", [
+    ("q", cpu(1, 16, 2, 64, dtype=F32)), ("q", cpu(16, 2, 64)), ("q", cpu(1, 2, 16, 64).transpose(1, 2)),
+    ("k", cpu(2, 16, 2, 64)), ("k", cpu(1, 16, 2, 128)), ("k", None), ("v", cpu(1, 17, 2, 64)),
+    ("v", cpu(1, 16, 2, 64, dtype=F32)), ("o", cpu(1, 16, 1, 64)), ("lse", cpu(1, 2, 16)), ("lse", cpu(1, 16, 2, dtype=F32)),
+    ("dout", cpu(1, 16, 2, 64, dtype=F32))])
+def test_sinks_bindings_refuse(L, name, bad):
+    x = cpu(1, 16, 2, 64)
+    t = dict(q=x, k=x, v=x, o=x, lse=cpu(1, 2, 16, dtype=F32), dout=x)
+    kw = dict(causal=True, window=(4, 0), sinks=2)
+    for call in (lambda: attn.attention(t["q"], t["k"], t["v"], **kw), lambda: attn.attention_backward(*t.values(), **kw)):
+        with pytest.raises(TypeError, match="q must be a CUDA tensor"):
+            call()
+    t[name] = bad
+    if name in "qkv":
+        with pytest.raises(TypeError, match=name):
+            attn.attention(t["q"], t["k"], t["v"], **kw)
+    with pytest.raises(TypeError, match=name):
+        attn.attention_backward(*t.values(), **kw)
+    with pytest.raises(attn.AttnError) as e:
+        attn.attention(x, x, x, doc_offsets=[0, 16], **kw)
+    assert e.value.status == attn.ATTN_ERR_UNSUPPORTED
+    with pytest.raises(TypeError):
+        attn.attention(x, x, x, causal=True, window=(4, 0), sinks="2")
+
+
 def test_sinks_beside_documents_are_refused(L):
     q, lse = stand_in(1, 16, 2, 64), stand_in(1, 2, 16, dtype=torch.float32)
     docs = stand_in(2, dtype=torch.int32)

@@ -284,6 +284,10 @@ def sinks_workspace_size(B, Hq, Hkv, Sq, Sk, D, causal, window, sinks) -> int:
 def attention(q, k, v, *, scale=None, causal=False, window=None, doc_offsets=None,
               options=None, stream=None, softcap=None, alibi_slopes=None, sinks=0):
     """Allocate O and LSE with torch and run the forward.  Returns (O, LSE)."""
+    if sinks:
+        _check_sinks(sinks, doc_offsets)
+        return _attention_sinks(q, k, v, scale, causal, window, sinks, options, stream, softcap,
+                                alibi_slopes)
     B, Sq, Hq, D = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(D)
@@ -293,17 +297,9 @@ def attention(q, k, v, *, scale=None, causal=False, window=None, doc_offsets=Non
         doc_offsets = torch.as_tensor(doc_offsets, dtype=torch.int32)
     if doc_offsets is not None and not doc_offsets.is_cuda:
         doc_offsets = doc_offsets.to(q.device)
-    ws = None
-    if sinks > 0 and window is not None:
-        size = sinks_workspace_size(B, Hq, k.shape[2], Sq, k.shape[1], D, causal, window,
-                                    min(sinks, k.shape[1]))
-        if size:
-            ws = torch.empty(size, dtype=torch.uint8, device=q.device)
     attn_fwd(q, k, v, o, lse, scale=scale, causal=causal, window=window,
              doc_offsets=doc_offsets, options=options, stream=stream, softcap=softcap,
-             alibi_slopes=alibi_slopes, sinks=sinks, workspace=ws)
-    if ws is not None:
-        _keep_for(stream, o, lse, ws)
+             alibi_slopes=alibi_slopes)
     return o, lse
 
 
@@ -518,6 +514,10 @@ def attention_backward(q, k, v, o, lse, dout, *, scale=None, causal=False, windo
                        doc_offsets=None, stream=None, softcap=None, alibi_slopes=None, sinks=0):
     """Allocate dQ (fp32), dK, dV (bf16) and the workspace with torch and run
     the backward.  Returns (dQ, dK, dV)."""
+    if sinks:
+        _check_sinks(sinks, doc_offsets)
+        return _attention_backward_sinks(q, k, v, o, lse, dout, scale, causal, window, sinks,
+                                         stream, softcap, alibi_slopes)
     B, Sq, Hq, D = q.shape
     _, Sk, Hkv, _ = k.shape
     if scale is None:
@@ -525,15 +525,14 @@ def attention_backward(q, k, v, o, lse, dout, *, scale=None, causal=False, windo
     dq = torch.empty(q.shape, dtype=torch.float32, device=q.device)
     dk = torch.empty_like(k)
     dv = torch.empty_like(v)
-    ws = torch.empty(bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D, min(max(sinks, 0), Sk)),
-                     dtype=torch.uint8, device=q.device)
+    ws = torch.empty(bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D), dtype=torch.uint8,
+                     device=q.device)
     if doc_offsets is not None and not torch.is_tensor(doc_offsets):
         doc_offsets = torch.as_tensor(doc_offsets, dtype=torch.int32)
     if doc_offsets is not None and not doc_offsets.is_cuda:
         doc_offsets = doc_offsets.to(q.device)
     attn_bwd(q, k, v, o, lse, dout, dq, dk, dv, ws, scale=scale, causal=causal, window=window,
-             doc_offsets=doc_offsets, stream=stream, softcap=softcap, alibi_slopes=alibi_slopes,
-             sinks=sinks)
+             doc_offsets=doc_offsets, stream=stream, softcap=softcap, alibi_slopes=alibi_slopes)
     _keep_for(stream, dq, dk, dv, ws)
     return dq, dk, dv
 
@@ -562,13 +561,16 @@ def attn_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, *, scale, causal=False, 
 #
 # These calls are short (a decoding step makes one of each per layer): their
 # checks of the tensors and the allocation of outputs are native
-# (csrc/binding.cpp), since in Python they cost more than the launches.
+# (csrc/binding.cpp), since in Python they cost more than the launches.  So are
+# those of attention with sinks, whose windows keep the kernels short.
 
 _binding = None
 _bound = None  # the library whose functions the binding calls
 _BOUND_FUNCTIONS = ("attn_qk_norm_rope", "attn_qk_norm_rope_cache", "attn_qk_norm_rope_bwd",
                     "attn_qk_norm_rope_bwd_workspace_size", "attn_decode_paged",
-                    "attn_decode_paged_workspace_size")
+                    "attn_decode_paged_workspace_size", "attn_fwd_sinks",
+                    "attn_fwd_sinks_workspace_size", "attn_bwd_sinks",
+                    "attn_bwd_sinks_workspace_size")
 
 
 def _native():
@@ -667,6 +669,56 @@ def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos, sin, positions, slots, 
                                     v, slots, k_cache, v_cache, k_descale, v_descale, q_out,
                                     _handle(stream))
     _keep_for(stream, out)
+    return out
+
+
+def _attention_sinks(q, k, v, scale, causal, window, sinks, options, stream, softcap, alibi_slopes):
+    """attention() with first keys that stay visible."""
+    left, right = (-1, -1) if window is None else window
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    opts = None
+    if options is not None or softcap is not None or alibi_slopes is not None:
+        opts = default_options() if options is None else FwdOptions.from_buffer_copy(options)
+        if softcap is not None:
+            opts.softcap = float(softcap)
+        slopes = _slopes(alibi_slopes, q.shape[2], q.device, stream)
+        if slopes is not None:
+            opts.alibi_slopes = slopes.data_ptr()
+    args = (q, k, v, scale, causal, left, right, sinks, None if opts is None else ctypes.addressof(opts))
+    if stream is None:
+        return _native().fwd_sinks(*args, None, None)
+    B, Sq, Hq, D = q.shape
+    size = sinks_workspace_size(B, Hq, k.shape[2], Sq, k.shape[1], D, causal, (left, right),
+                                min(sinks, k.shape[1]))
+    ws = torch.empty(max(size, 1), dtype=torch.uint8, device=q.device)
+    out = _native().fwd_sinks(*args, ws, _handle(stream))
+    _keep_for(stream, ws, *out)
+    return out
+
+
+def _attention_backward_sinks(q, k, v, o, lse, dout, scale, causal, window, sinks, stream, softcap,
+                              alibi_slopes):
+    """attention_backward() with first keys that stay visible."""
+    left, right = (-1, -1) if window is None else window
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    opts = None
+    if softcap is not None or alibi_slopes is not None:
+        opts = BwdOptions()
+        opts.softcap = float(softcap or 0.0)
+        slopes = _slopes(alibi_slopes, q.shape[2], q.device, stream)
+        opts.alibi_slopes = None if slopes is None else slopes.data_ptr()
+    args = (q, k, v, scale, causal, left, right, sinks, o, lse, dout,
+            None if opts is None else ctypes.addressof(opts))
+    if stream is None:
+        return _native().bwd_sinks(*args, None, None)
+    B, Sq, Hq, D = q.shape
+    ws = torch.empty(bwd_workspace_size(B, Hq, k.shape[2], Sq, k.shape[1], D,
+                                        min(max(sinks, 0), k.shape[1])),
+                     dtype=torch.uint8, device=q.device)
+    out = _native().bwd_sinks(*args, ws, _handle(stream))
+    _keep_for(stream, ws, *out)
     return out
 
 

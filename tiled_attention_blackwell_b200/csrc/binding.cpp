@@ -1,7 +1,8 @@
-// Native side of the Python calls that a decoding step makes once per layer
-// (head norms with rotation, the cache write, the decode): checks of the
-// tensors, allocation of outputs, and the call into the library.  In Python
-// these cost two to four times as long as the launches themselves.
+// Native side of the Python calls that a step makes once per layer (head norms
+// with rotation, the cache write, the decode, attention with first tokens that
+// stay visible): checks of the tensors, allocation of outputs, and the call
+// into the library.  In Python these cost two to four times as long as the
+// launches themselves.
 //
 // Everything here is argument marshalling; the work is libattn.so's, whose
 // functions attn.py hands over by address.  A wrong argument raises TypeError,
@@ -26,6 +27,10 @@ decltype(&attn_qk_norm_rope_bwd) g_norm_rope_bwd;
 decltype(&attn_qk_norm_rope_bwd_workspace_size) g_norm_rope_bwd_workspace;
 decltype(&attn_decode_paged) g_decode;
 decltype(&attn_decode_paged_workspace_size) g_decode_workspace;
+decltype(&attn_fwd_sinks) g_fwd_sinks;
+decltype(&attn_fwd_sinks_workspace_size) g_fwd_sinks_workspace;
+decltype(&attn_bwd_sinks) g_bwd_sinks;
+decltype(&attn_bwd_sinks_workspace_size) g_bwd_sinks_workspace;
 PyObject *g_check = nullptr;  // (status, name): raises unless the status is ATTN_OK
 
 constexpr auto kBF16 = at::kBFloat16;
@@ -324,13 +329,113 @@ PyObject *decode(PyObject *const *a) {
     return Py_BuildValue("(NN)", wrap(o), wrap(lse));
 }
 
+// q, k, v of an attention call [B, S, H, D] and its mask: q, k, v, scale,
+// causal, window_left, window_right, sinks.
+struct Masked {
+    const at::Tensor &q, &k, &v;
+    float scale;
+    int causal, left, right, sinks;
+    int B, Hq, Hkv, Sq, Sk, D;
+
+    explicit Masked(PyObject *const *a)
+        : q(tensor(a[0], "q")), k(tensor(a[1], "k")), v(tensor(a[2], "v")), scale(number(a[3])),
+          causal(PyObject_IsTrue(a[4])), left(integer(a[5])), right(integer(a[6])) {
+        if (causal < 0) throw PythonError{};
+        require(q.scalar_type() == kBF16 && q.dim() == 4 && q.is_contiguous(), "q",
+                "a contiguous bf16 tensor [B, Sq, Hq, D]");
+        require(k.scalar_type() == kBF16 && k.dim() == 4 && k.is_contiguous() && k.size(0) == q.size(0) &&
+                    k.size(3) == q.size(3),
+                "k", "a contiguous bf16 tensor [B, Sk, Hkv, D] of q's batch and head dimension");
+        require(v.scalar_type() == kBF16 && v.sizes() == k.sizes() && v.is_contiguous(), "v",
+                "a contiguous bf16 tensor of k's shape");
+        for (const at::Tensor *t : {&q, &k})
+            for (int i = 0; i < 4; ++i) require(t->size(i) <= INT_MAX, "q or k", "smaller");
+        B = (int)q.size(0), Sq = (int)q.size(1), Hq = (int)q.size(2), D = (int)q.size(3);
+        Sk = (int)k.size(1), Hkv = (int)k.size(2);
+        // More first keys than keys are all of them.
+        int overflow = 0;
+        const long long n = PyLong_AsLongLongAndOverflow(a[7], &overflow);
+        if (n == -1 && PyErr_Occurred()) throw PythonError{};
+        sinks = overflow > 0 || n > Sk ? Sk : overflow < 0 || n < 0 ? -1 : (int)n;
+    }
+    void on(Device &dev) const {
+        dev.add(q, "q");
+        dev.add(k, "k");
+        dev.add(v, "v");
+    }
+};
+
+// An option struct by address (None: the defaults).
+template <class T>
+const T *options(PyObject *o) {
+    if (o == Py_None) return nullptr;
+    const void *p = PyLong_AsVoidPtr(o);
+    if (!p && PyErr_Occurred()) throw PythonError{};
+    return static_cast<const T *>(p);
+}
+
+// (q, k, v, scale, causal, window_left, window_right, sinks, options, workspace, stream)
+PyObject *fwd_sinks(PyObject *const *a) {
+    const Masked m(a);
+    Device dev;
+    m.on(dev);
+    c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev.index());
+    const at::Tensor o = at::empty_like(m.q);
+    const at::Tensor lse = at::empty({m.B, m.Hq, m.Sq}, m.q.options().dtype(kF32));
+    const size_t size = g_fwd_sinks_workspace(m.B, m.Hq, m.Hkv, m.Sq, m.Sk, m.D, m.causal, m.left, m.right, m.sinks);
+    at::Tensor ws;
+    if (size) {
+        ws = workspace(a[9], size, m.q);
+        dev.add(ws, "workspace");
+    }
+    check(g_fwd_sinks(m.q.data_ptr(), m.k.data_ptr(), m.v.data_ptr(), o.data_ptr(),
+                      static_cast<float *>(lse.data_ptr()), m.B, m.Hq, m.Hkv, m.Sq, m.Sk, m.D, m.scale, m.causal,
+                      m.left, m.right, m.sinks, size ? ws.data_ptr() : nullptr, size ? (size_t)ws.numel() : 0,
+                      options<attn_fwd_options_t>(a[8]), stream_of(a[10], dev.index())),
+          "attn_fwd_sinks");
+    return Py_BuildValue("(NN)", wrap(o), wrap(lse));
+}
+
+// (q, k, v, scale, causal, window_left, window_right, sinks, o, lse, dout, options, workspace, stream)
+PyObject *bwd_sinks(PyObject *const *a) {
+    const Masked m(a);
+    const at::Tensor &o = tensor(a[8], "o"), &lse = tensor(a[9], "lse"), &dout = tensor(a[10], "dout");
+    require(o.scalar_type() == kBF16 && o.sizes() == m.q.sizes() && o.is_contiguous(), "o",
+            "a contiguous bf16 tensor of q's shape");
+    require(dout.scalar_type() == kBF16 && dout.sizes() == m.q.sizes() && dout.is_contiguous(), "dout",
+            "a contiguous bf16 tensor of q's shape");
+    require(lse.scalar_type() == kF32 && lse.dim() == 3 && lse.size(0) == m.B && lse.size(1) == m.Hq &&
+                lse.size(2) == m.Sq && lse.is_contiguous(),
+            "lse", "a contiguous fp32 tensor [B, Hq, Sq]");
+    Device dev;
+    m.on(dev);
+    dev.add(o, "o");
+    dev.add(lse, "lse");
+    dev.add(dout, "dout");
+    c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev.index());
+    const at::Tensor dq = at::empty_like(m.q, m.q.options().dtype(kF32));
+    const at::Tensor dk = at::empty_like(m.k), dv = at::empty_like(m.v);
+    const at::Tensor ws =
+        workspace(a[12], g_bwd_sinks_workspace(m.B, m.Hq, m.Hkv, m.Sq, m.Sk, m.D, std::max(m.sinks, 0)), m.q);
+    dev.add(ws, "workspace");
+    check(g_bwd_sinks(m.q.data_ptr(), m.k.data_ptr(), m.v.data_ptr(), o.data_ptr(),
+                      static_cast<const float *>(lse.data_ptr()), dout.data_ptr(),
+                      static_cast<float *>(dq.data_ptr()), dk.data_ptr(), dv.data_ptr(), m.B, m.Hq, m.Hkv, m.Sq,
+                      m.Sk, m.D, m.scale, m.causal, m.left, m.right, m.sinks, ws.data_ptr(), (size_t)ws.numel(),
+                      options<attn_bwd_options_t>(a[11]), stream_of(a[13], dev.index())),
+          "attn_bwd_sinks");
+    return Py_BuildValue("(NNN)", wrap(dq), wrap(dk), wrap(dv));
+}
+
 // bind(check, addresses...): the library's functions, in the order of the
 // table in attn.py.
 PyObject *bind(PyObject *const *a) {
     void **to[] = {reinterpret_cast<void **>(&g_norm_rope),      reinterpret_cast<void **>(&g_norm_rope_cache),
                    reinterpret_cast<void **>(&g_norm_rope_bwd),  reinterpret_cast<void **>(&g_norm_rope_bwd_workspace),
-                   reinterpret_cast<void **>(&g_decode),         reinterpret_cast<void **>(&g_decode_workspace)};
-    for (int i = 0; i < 6; ++i) {
+                   reinterpret_cast<void **>(&g_decode),         reinterpret_cast<void **>(&g_decode_workspace),
+                   reinterpret_cast<void **>(&g_fwd_sinks),      reinterpret_cast<void **>(&g_fwd_sinks_workspace),
+                   reinterpret_cast<void **>(&g_bwd_sinks),      reinterpret_cast<void **>(&g_bwd_sinks_workspace)};
+    for (int i = 0; i < 10; ++i) {
         void *p = PyLong_AsVoidPtr(a[1 + i]);
         if (!p) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null function");
@@ -367,11 +472,13 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr
 PyMethodDef g_methods[] = {
-    {"bind", FAST((&entry<bind, 7, false>))},
+    {"bind", FAST((&entry<bind, 11, false>))},
     {"norm_rope", FAST((&entry<norm_rope, 12>))},
     {"norm_rope_cache", FAST((&entry<norm_rope_cache, 17>))},
     {"norm_rope_backward", FAST((&entry<norm_rope_backward, 15>))},
     {"decode", FAST((&entry<decode, 16>))},
+    {"fwd_sinks", FAST((&entry<fwd_sinks, 11>))},
+    {"bwd_sinks", FAST((&entry<bwd_sinks, 14>))},
     {nullptr, nullptr, 0, nullptr},
 };
 
