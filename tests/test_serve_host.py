@@ -253,6 +253,9 @@ def test_sinks_workspace(L):
     assert attn.bwd_workspace_size(2, 16, 16, 4096, 4096, 128, 0) == 2 * 16 * 4096 * 4
     assert L.attn_bwd_sinks_workspace_size(2, 16, 0, 4096, 4096, 128, 4) == 2 * 16 * 4096 * 4
     assert L.attn_bwd_sinks_workspace_size(0, 16, 16, 4096, 4096, 128, 4) == 0
+    # one key head and 8 key blocks: the other 7 are cut too, into at most 148 / 8 parts
+    size = attn.bwd_workspace_size(1, 32, 1, 1000, 1000, 64, 4)
+    assert size == 32 * 1000 * 4 + (32 * 8 // 8 + 18 * 7) * 2 * 128 * 64 * 4
     # more first keys than keys; at most 64 parts
     assert attn.bwd_workspace_size(1, 8, 1, 1 << 16, 130, 64, 10 ** 6) == 8 * (1 << 16) * 4 + 64 * 2 * 2 * 128 * 64 * 4
     need = attn.bwd_workspace_size(1, 2, 2, 16, 16, 128, 4)

@@ -164,6 +164,13 @@ def test_grouped_heads_and_batches(heads):
     case(3, *heads, 260, 260, 64, seed=heads[0], window=(20, 0), sinks=150)
 
 
+@pytest.mark.parametrize("heads", [(8, 1), (32, 1), (6, 2)])
+@pytest.mark.parametrize("sinks", [3, 200])
+def test_few_key_heads_whose_query_heads_are_cut_into_parts(heads, sinks):
+    case(1, *heads, 600, 600, 64, seed=sinks, window=(150, 0), sinks=sinks)
+    case(1, *heads, 130, 700, 128, seed=sinks, window=(70, 40), sinks=sinks, causal=False)
+
+
 @pytest.mark.parametrize("softcap,with_slopes", [(15.0, False), (None, True), (4.0, True)])
 def test_score_modifiers(softcap, with_slopes):
     slopes = 2.0 ** -torch.arange(2, 6).float() if with_slopes else None

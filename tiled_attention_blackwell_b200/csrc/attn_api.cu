@@ -739,6 +739,14 @@ static int sink_parts(int Hq, int Hkv, int Sq) {
     const long long items = (Sq + 127LL) / 128 * (Hq / Hkv);
     return (int)std::min<long long>(kSinkMaxParts, (items + kSinkPartItems - 1) / kSinkPartItems);
 }
+// Parts of a key block without first keys that `items` (query block, head of
+// the group) pairs see: as many as give every SM of the device a CTA, of four
+// items or more.  (One key head under 32 query heads, 1000 tokens, window 501:
+// the backward takes 301 us with those blocks whole, 86 in parts.)
+static int other_parts(int B, int Hkv, int Sk, long long items) {
+    const long long ctas = (Sk + 127LL) / 128 * Hkv * B;
+    return (int)std::max(1LL, std::min(148 / ctas, items / 4));
+}
 
 // The backward of both entry points; sinks > 0 with window_left >= 0 selects
 // the kernels whose rows see first keys beside their window.
@@ -765,7 +773,7 @@ static attn_status_t bwd_impl(const void *q, const void *k, const void *v, const
     const long long num_qb = (Sq + 127LL) / 128, num_kb = (Sk + 127LL) / 128;
     const bool with_sinks = sinks > 0 && window_left >= 0;
     const long long sink_blocks = with_sinks ? (std::min(sinks, Sk) + 127LL) / 128 : 0;
-    if (with_sinks && (num_kb + sink_blocks * (kSinkMaxParts - 1)) * Hkv * B > 0x7fffffffLL)
+    if (with_sinks && (num_kb + 148 + sink_blocks * (kSinkMaxParts - 1)) * Hkv * B > 0x7fffffffLL)
         return fail(ATTN_ERR_UNSUPPORTED, "grid too large");
 
     DeviceState *st = nullptr;
@@ -814,7 +822,11 @@ static attn_status_t bwd_impl(const void *q, const void *k, const void *v, const
         p.sinks = std::min(sinks, Sk);
         p.sink_blocks = (int)sink_blocks;
         p.sink_parts = sink_parts(Hq, Hkv, Sq);
-        p.sink_sums = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
+        // Query blocks that a key block can be seen by: those of its window.
+        long long seen = (window_left + (long long)std::max(window_right, 0) + 127) / 128 + 2;
+        if (!causal && window_right < 0) seen = num_qb;
+        p.other_parts = other_parts(B, Hkv, Sk, std::min(num_qb, seen) * (Hq / Hkv));
+        p.part_sums = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
                                                 attn_bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D));
         return tab_host::dispatch_bwd_sinks(p, D, mod, cs);
     }
@@ -824,8 +836,11 @@ static attn_status_t bwd_impl(const void *q, const void *k, const void *v, const
 size_t attn_bwd_sinks_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int D, int sinks) {
     const size_t rows = attn_bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D);
     if (rows == 0 || Hkv < 1 || Sk < 1 || D < 1 || sinks < 1) return rows;
-    const size_t blocks = (std::min(sinks, Sk) + (size_t)127) / 128;
-    return rows + (size_t)sink_parts(Hq, Hkv, Sq) * blocks * B * Hkv * 2 * 128 * D * sizeof(float);
+    // Sums of all parts; at most the parts that any window would give.
+    const size_t blocks = (std::min(sinks, Sk) + (size_t)127) / 128, others = (Sk + (size_t)127) / 128 - blocks;
+    const size_t parts = other_parts(B, Hkv, Sk, (Sq + 127LL) / 128 * (Hq / Hkv));
+    return rows + (sink_parts(Hq, Hkv, Sq) * blocks + (parts > 1 ? parts * others : 0)) * B * Hkv * 2 * 128 * D *
+                      sizeof(float);
 }
 
 attn_status_t attn_bwd_ex(const void *q, const void *k, const void *v, const void *o,

@@ -93,10 +93,11 @@ struct BwdParams {
     float softcap_out;  // cap * log2(e)
     const float *alibi_slopes;
     // SINKS kernels: first keys that stay visible beside the window, the key
-    // blocks that hold them, the parts that their query blocks are cut into,
-    // and the parts' sums (fp32 [part][block][B * Hkv][dK, dV][128][D]).
-    int sinks, sink_blocks, sink_parts;
-    float *sink_sums;
+    // blocks that hold them, the parts that their query blocks are cut into and
+    // those of the other key blocks (1: none), and the parts' sums: fp32 [part]
+    // [block][B * Hkv][dK, dV][128][D], first the sink blocks', then the others'.
+    int sinks, sink_blocks, sink_parts, other_parts;
+    float *part_sums;
 };
 
 // Modified scores of a pair in log2 units (MOD bit 0 soft-cap, bit 1 ALiBi
@@ -159,11 +160,12 @@ struct DkdvSmem {
     int qb_lo, qb_hi;
 };
 
-// SINKS: key blocks without a first key see what they see without SINKS; one
+// SINKS: key blocks without a first key are seen as they are without SINKS; one
 // with first keys is seen by (nearly) every query block behind it, many times
-// a window's worth.  Its items are cut into sink_parts parts of a block
-// each, which come first in the grid and leave fp32 sums;
-// attn_bwd_sink_sum_kernel adds those in order.
+// a window's worth.  Its items are cut into sink_parts parts, a CTA each,
+// which come first in the grid; where few key blocks leave SMs idle, those of
+// the others are cut too (other_parts).  Parts leave fp32 sums, which
+// attn_bwd_part_sum_kernel adds in order.
 template <int D, int NSQ, int MOD = 0, bool SINKS = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
@@ -179,17 +181,23 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
     const int bh_count = p.Hkv * p.B;
     int kb = (int)(blockIdx.x / bh_count);
     const int bh = (int)(blockIdx.x % bh_count);
-    // SINKS: part `part` of block kb's items, or (part < 0) all of them.
-    int part = -1;
+    // SINKS: part `part` of `parts` of block kb's items, or (part < 0) all of
+    // them; `slot`: the part's place among the sums.
+    int part = -1, parts = 1, slot = kb;
     if constexpr (SINKS) {
-        const int sink_rows = p.sink_blocks * p.sink_parts;
+        const int sink_rows = p.sink_blocks * p.sink_parts, others = p.num_kb - p.sink_blocks;
         if (kb < sink_rows) {
+            parts = p.sink_parts;
             part = kb / p.sink_blocks;
             kb -= part * p.sink_blocks;
         } else {
-            kb += p.sink_blocks - sink_rows;
+            parts = p.other_parts;
+            part = (kb - sink_rows) / others;
+            kb += p.sink_blocks - sink_rows - part * others;
+            if (parts == 1) part = -1;
         }
     }
+    const bool sinky = SINKS && kb < p.sink_blocks;
     const int hkv = bh % p.Hkv;
     const int b = bh / p.Hkv;
     const int k0 = kb * 128;
@@ -223,7 +231,7 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
             const int r1 = min(r0 + 127, p.Sq - 1);
             KeyRange a = row_key_range(p, r0);
             KeyRange z = row_key_range(p, r1);
-            const int a_lo = a.lo <= a.hi && !(SINKS && part >= 0) ? a.lo : -1;
+            const int a_lo = a.lo <= a.hi && !sinky ? a.lo : -1;
             const int z_hi = z.lo <= z.hi ? z.hi : -1;
             if (a_lo <= k1 && z_hi >= k0) {
                 lo = min(lo, qb);
@@ -255,7 +263,7 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
     int it0 = 0, n_items = all_items;      // this block's: [it0, it0 + n_items)
     if constexpr (SINKS) {
         if (part >= 0) {
-            const int per = (all_items + p.sink_parts - 1) / p.sink_parts;
+            const int per = (all_items + parts - 1) / parts;
             it0 = min(part * per, all_items);
             n_items = min(per, all_items - it0);
         }
@@ -299,7 +307,7 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
                 nlo[m] = kr.lo;
                 nhi[m] = SINKS && kr.lo > kr.hi ? -1 : kr.hi;  // no key, so no first key either
                 nfull = nfull && r < p.Sq && kr.hi >= k1 &&
-                        (kr.lo <= k0 || (SINKS && part >= 0 && k1 < p.sinks && kr.lo <= kr.hi));
+                        (kr.lo <= k0 || (sinky && k1 < p.sinks && kr.lo <= kr.hi));
             }
             nfull = __all_sync(0xffffffffu, nfull);
         };
@@ -453,7 +461,7 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
     } else {
         // ---------------------------------------------------- elementwise
         const int key = k0 + (warp & 3) * 32 + lane;
-        const bool first_key = SINKS && part >= 0 && key < p.sinks;  // lower ends do not count
+        const bool first_key = SINKS && key < p.sinks;  // lower ends do not count
         const int h = warp >> 2;  // this warpgroup's half of the columns
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_col = tmem + lane_base + kColS + h * 64;
@@ -593,8 +601,7 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
                     if constexpr (SINKS) {
                         if (part >= 0) {  // fp32 sums of this part, unscaled; every row
                             float4 *dst = reinterpret_cast<float4 *>(
-                                p.sink_sums +
-                                ((((size_t)part * p.sink_blocks + kb) * bh_count + bh) * 2 + which) * 128 * D +
+                                p.part_sums + (((size_t)slot * bh_count + bh) * 2 + which) * 128 * D +
                                 (size_t)(key - k0) * D + h * (D / 2) + ch * 32);
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
@@ -627,14 +634,14 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
     }
 }
 
-// dK and dV of the key blocks with first keys: the parts' sums, in order.
-// One thread per four values.
+// dK and dV of the key blocks that were cut: the parts' sums, in order.  One
+// thread per four values; blocks [0, n_blocks).
 template <int D>
 __global__ void __launch_bounds__(256)
-attn_bwd_sink_sum_kernel(const __grid_constant__ BwdParams p) {
+attn_bwd_part_sum_kernel(const __grid_constant__ BwdParams p, int n_blocks) {
     const int bh_count = p.Hkv * p.B;
-    const size_t n = (size_t)p.sink_blocks * bh_count * 2 * 128 * (D / 4);
-    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
+    const size_t block = (size_t)bh_count * 2 * 128 * (D / 4);  // float4s of a key block
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n_blocks * block; i += (size_t)gridDim.x * 256) {
         const int d = (int)(i % (D / 4)) * 4;
         size_t r = i / (D / 4);
         const int row = (int)(r % 128);
@@ -644,10 +651,16 @@ attn_bwd_sink_sum_kernel(const __grid_constant__ BwdParams p) {
         const int bh = (int)(r % bh_count), kb = (int)(r / bh_count);
         const int key = kb * 128 + row;
         if (key >= p.Sk) continue;
+        const bool sinky = kb < p.sink_blocks;
+        const int parts = sinky ? p.sink_parts : p.other_parts;
+        const size_t step = (size_t)(sinky ? p.sink_blocks : p.num_kb - p.sink_blocks) * block;
+        // A block's first part: its own place, behind all parts of the sink blocks
+        // for the others.
+        const size_t first = sinky ? i : i + (size_t)p.sink_blocks * (p.sink_parts - 1) * block;
         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-        for (int part = 0; part < p.sink_parts; ++part) {
-            const float4 v = *reinterpret_cast<const float4 *>(p.sink_sums + ((size_t)part * n + i) * 4);
+        for (int part = 0; part < parts; ++part) {
+            const float4 v = *reinterpret_cast<const float4 *>(p.part_sums + (first + part * step) * 4);
             sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
         }
         const float mul = which == 0 ? p.scale : 1.0f;

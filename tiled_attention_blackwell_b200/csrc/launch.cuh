@@ -134,12 +134,13 @@ attn_status_t launch_bwd(const tab::BwdParams &p, cudaStream_t stream) {
     // kernel reads.
     k_dq<<<p.num_qb * p.Hq * p.B, tab::kBwdThreads, smem_dq, stream>>>(p);
     if constexpr (SINKS) {
-        // Key blocks with first keys: sink_parts blocks each, and their sum.
-        const int rows = p.num_kb + p.sink_blocks * (p.sink_parts - 1);
+        // A CTA per part of a key block, and the sum of the parts.
+        const int rows = p.sink_blocks * p.sink_parts + (p.num_kb - p.sink_blocks) * p.other_parts;
         k_dkdv<<<rows * p.Hkv * p.B, tab::kBwdThreads, smem_dkdv, stream>>>(p);
-        const long long n = (long long)p.sink_blocks * p.Hkv * p.B * 2 * 128 * (D / 4);
+        const int blocks = p.other_parts > 1 ? p.num_kb : p.sink_blocks;
+        const long long n = (long long)blocks * p.Hkv * p.B * 2 * 128 * (D / 4);
         const int grid = (int)std::min<long long>((n + 255) / 256, 148 * 8);
-        tab::attn_bwd_sink_sum_kernel<D><<<grid, 256, 0, stream>>>(p);
+        tab::attn_bwd_part_sum_kernel<D><<<grid, 256, 0, stream>>>(p, blocks);
     } else {
         k_dkdv<<<p.num_kb * p.Hkv * p.B, tab::kBwdThreads, smem_dkdv, stream>>>(p);
     }
