@@ -300,3 +300,50 @@ def test_a_serving_run():
             t = dict(q=qn[last].cpu(), kc=kc.cpu(), vc=vc.cpu(), table=table,
                      lens=torch.tensor(lens, dtype=torch.int32), kd=d, vd=d)
             check(t, run(t, window=(30, 0), sinks=4), scale=D ** -0.5, window=30, sinks=4)
+
+
+def test_two_streams_at_once():
+    a, b = (problem([700, 64, 2000], 8, 2, 128, 16, d, seed=90) for d in (torch.bfloat16, FP8))
+    want = [run(a), run(b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    ga, gb = ({n: x.to(DEV) if torch.is_tensor(x) else x for n, x in t.items()} for t in (a, b))
+    torch.cuda.synchronize()
+    for handle in (lambda s: s, lambda s: s.cuda_stream):
+        got = [run(g, stream=handle(s)) for _ in range(8) for g, s in zip((ga, gb), streams)]
+        torch.cuda.synchronize()
+        for i, res in enumerate(got):
+            assert all(torch.equal(x, y) for x, y in zip(res, want[i % 2]))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+def test_a_cache_of_more_than_32_bits(dtype):
+    """Values, bytes and pages past 2^32: tokens written at the far end and in
+    the middle of a large cache, and read back through the decode."""
+    Hq, Hkv, D, page = 8, 8, 128, 16
+    pages = 2 ** 32 // (page * Hkv * D) + 300
+    d = 1.0 if dtype == torch.bfloat16 else 1 / 32
+    kc, vc = (torch.zeros(pages, page, Hkv, D, dtype=dtype, device=DEV) for _ in range(2))
+    n = 100
+    place = torch.tensor([pages - 1, 2 ** 31 // (page * Hkv * D), pages - 299, 1, pages // 2, pages - 7, 0],
+                         dtype=torch.int32)
+    g = torch.Generator().manual_seed(91)
+    q, k, v = (torch.randn(n, h, D, generator=g).to(torch.bfloat16).to(DEV) for h in (Hq, Hkv, Hkv))
+    w = torch.ones(D, dtype=torch.bfloat16, device=DEV)
+    cos, sin = attn.rope_table(n, D, device=DEV)
+    j = torch.arange(n, dtype=torch.int32)
+    slots = place[j.long() // page] * page + j % page
+    qn = attn.qk_norm_rope_cache(q, k, v, w, w, cos, sin, j.to(DEV), slots.to(DEV), kc, vc, k_descale=d, v_descale=d)
+    # The same in a small cache: the same values, so the same results.
+    small_k, small_v = (torch.zeros(7, page, Hkv, D, dtype=dtype, device=DEV) for _ in range(2))
+    qs = attn.qk_norm_rope_cache(q, k, v, w, w, cos, sin, j.to(DEV), j.to(DEV), small_k, small_v, k_descale=d,
+                                 v_descale=d)
+    assert torch.equal(qn, qs)
+    for big, small in ((kc, small_k), (vc, small_v)):
+        assert torch.equal(big[place.long().to(DEV)].view(torch.uint8), small.view(torch.uint8))
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    got, want = (attn.decode_paged(qn[-1:], a, b, t.to(DEV)[None], lens, k_descale=d, v_descale=d)
+                 for a, b, t in ((kc, vc, place), (small_k, small_v, torch.arange(7, dtype=torch.int32))))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    t = dict(q=qn[-1:].cpu(), kc=small_k.cpu(), vc=small_v.cpu(), table=torch.arange(7, dtype=torch.int32)[None],
+             lens=torch.tensor([n], dtype=torch.int32), kd=d, vd=d)
+    check(t, got, scale=D ** -0.5)

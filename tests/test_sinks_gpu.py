@@ -337,3 +337,60 @@ def test_parts_with_score_modifiers_and_captured():
             x.zero_()
         graph.replay()
         assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+
+
+def test_nan_and_infinity_stay_in_their_rows():
+    """A NaN in a query row, and in a key of the window, reaches the rows that
+    see it and no other, in one piece and in parts alike."""
+    shape, window, sinks = (1, 2, 1, 200, 1500, 128), (900, 0), 4
+    t = make_tensors(*shape, 33)
+    t["q"][0, 140, 1, 7] = float("nan")
+    t["q"][0, 190, 0, 3] = float("inf")
+    t["k"][0, 450, 0, 9] = float("nan")
+    see = visible(200, 1500, True, window, sinks)
+    g = {n: x.to(DEV) for n, x in t.items()}
+    bad = see[:, 450].repeat(2, 1)
+    bad[1, 140] = bad[0, 190] = True
+    assert 0 < int(bad.sum()) < bad.numel() // 2
+    size = attn.sinks_workspace_size(*shape, True, window, sinks)
+    assert size > 0
+    for ws in (None, torch.empty(size, dtype=torch.uint8, device=DEV)):
+        o, lse = torch.empty_like(g["q"]), torch.empty(1, 2, 200, device=DEV)
+        attn.attn_fwd(g["q"], g["k"], g["v"], o, lse, scale=128 ** -0.5, causal=True, window=window, sinks=sinks,
+                      workspace=ws)
+        assert torch.equal(torch.isnan(o[0]).all(-1).T.cpu(), bad)
+        assert torch.isfinite(o[0].transpose(0, 1)[~bad.to(DEV)]).all()
+        assert torch.isfinite(lse[0][~bad.to(DEV)]).all()
+
+
+def test_first_keys_that_fill_the_device_are_not_cut():
+    """Many first keys of many heads: the workspace holds no parts, or few."""
+    rows = attn.bwd_workspace_size(2, 16, 16, 2048, 2048, 64)
+    assert attn.bwd_workspace_size(2, 16, 16, 2048, 2048, 64, sinks=2048) == \
+        attn.bwd_workspace_size(2, 16, 16, 2048, 2048, 64, sinks=2 ** 40)
+    assert attn.bwd_workspace_size(40, 16, 16, 2048, 2048, 64, sinks=4) == \
+        attn.bwd_workspace_size(40, 16, 16, 2048, 2048, 64)
+    assert attn.bwd_workspace_size(2, 16, 16, 2048, 2048, 64, sinks=4) > rows
+    # 9 blocks of 66 heads: whole, where each would have two parts; of 40 heads: two parts for three.
+    case(1, 66, 66, 1100, 1100, 64, seed=34, window=(100, 0), sinks=1090)
+    case(1, 80, 40, 1100, 1100, 64, seed=35, window=(100, 0), sinks=1090)
+
+
+def test_two_streams_at_once():
+    """Two calls in flight together, each with its own allocations."""
+    a, b = (make_tensors(1, 4, 2, 300, 1500, 128, s, with_dout=True) for s in (36, 37))
+    kw = dict(causal=True, window=(700, 0), sinks=4)
+    ga, gb = ({n: x.to(DEV) for n, x in t.items()} for t in (a, b))
+
+    def both(g, stream=None):
+        o, lse = attn.attention(g["q"], g["k"], g["v"], stream=stream, **kw)
+        return (o, lse, *attn.attention_backward(g["q"], g["k"], g["v"], o, lse, g["dout"], stream=stream, **kw))
+
+    want = [both(ga), both(gb)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for handle in (lambda s: s, lambda s: s.cuda_stream):
+        got = [both(g, handle(s)) for _ in range(4) for g, s in zip((ga, gb), streams)]
+        torch.cuda.synchronize()
+        for i, res in enumerate(got):
+            assert all(torch.equal(x, y) for x, y in zip(res, want[i % 2]))

@@ -278,7 +278,7 @@ def attn_fwd(q, k, v, o, lse, *, scale, causal=False, window=None, doc_offsets=N
 def sinks_workspace_size(B, Hq, Hkv, Sq, Sk, D, causal, window, sinks) -> int:
     """Bytes of device workspace with which attn_fwd runs in parts (0: it would not)."""
     return int(lib().attn_fwd_sinks_workspace_size(B, Hq, Hkv, Sq, Sk, D, int(bool(causal)),
-                                                   int(window[0]), int(window[1]), sinks))
+                                                   int(window[0]), int(window[1]), min(sinks, Sk)))
 
 
 def attention(q, k, v, *, scale=None, causal=False, window=None, doc_offsets=None,
@@ -472,7 +472,7 @@ def _docs_arg(doc_offsets):
 def bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D, sinks=0) -> int:
     """Bytes of device workspace attn_bwd needs."""
     if sinks:
-        return int(lib().attn_bwd_sinks_workspace_size(B, Hq, Hkv, Sq, Sk, D, sinks))
+        return int(lib().attn_bwd_sinks_workspace_size(B, Hq, Hkv, Sq, Sk, D, min(sinks, Sk)))
     return int(lib().attn_bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D))
 
 
@@ -598,10 +598,13 @@ def _handle(stream):
 
 
 def _keep_for(stream, *tensors):
-    """Tells the allocator that work on `stream` uses tensors which were
-    allocated on the current stream."""
-    if stream is not None and hasattr(stream, "cuda_stream") \
-            and stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
+    """Tells the allocator that work on `stream` (a stream or its handle) uses
+    tensors which were allocated on the current stream."""
+    if stream is None:
+        return
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=tensors[0].device)
+    if stream.cuda_stream != torch.cuda.current_stream(tensors[0].device).cuda_stream:
         for t in tensors:
             t.record_stream(stream)
 

@@ -467,8 +467,10 @@ static attn_status_t fwd_impl(const void *q, const void *k, const void *v, void 
     if (sinks > 0 && window_left >= 0) {
         p.sinks = std::min(sinks, Sk);
         p.parts = workspace ? fwd_parts(B, Hq, Sq, Sk, causal, window_left, window_right, sinks) : 1;
-        p.part_o = static_cast<float *>(workspace);
-        p.part_lse = p.part_o + (size_t)p.parts * B * Sq * Hq * D;
+        if (p.parts > 1) {
+            p.part_o = static_cast<float *>(workspace);
+            p.part_lse = p.part_o + (size_t)p.parts * B * Sq * Hq * D;
+        }
         return p.parts > 1 ? tab_host::dispatch_fwd_parts(p, grid, D, op.exp2_mode, mod, cs)
                            : tab_host::dispatch_fwd_sinks(p, grid, D, op.exp2_mode, mod, cs);
     }
@@ -731,13 +733,17 @@ attn_status_t attn_bwd(const void *q, const void *k, const void *v, const void *
 
 // Parts that the query blocks of a key block with first keys are cut into
 // (attn_bwd_sinks): about kSinkPartItems of them each, what a key block under
-// a window of 1024 keys has.  At most kSinkMaxParts, which bounds the
-// workspace.
+// a window of 1024 keys has.  At most kSinkMaxParts, and no more than give
+// kSinkCtas CTAs (four per SM) in all: where many first keys fill the device
+// by themselves, parts would only cost their sums' memory.
 constexpr int kSinkPartItems = 8;
 constexpr int kSinkMaxParts = 64;
-static int sink_parts(int Hq, int Hkv, int Sq) {
+constexpr int kSinkCtas = 592;
+static int sink_parts(int B, int Hq, int Hkv, int Sq, int Sk, int sinks) {
     const long long items = (Sq + 127LL) / 128 * (Hq / Hkv);
-    return (int)std::min<long long>(kSinkMaxParts, (items + kSinkPartItems - 1) / kSinkPartItems);
+    const long long ctas = (std::min(sinks, Sk) + 127LL) / 128 * Hkv * B;
+    return (int)std::max(1LL, std::min({(long long)kSinkMaxParts, (items + kSinkPartItems - 1) / kSinkPartItems,
+                                        (kSinkCtas + ctas - 1) / ctas}));
 }
 // Parts of a key block without first keys that `items` (query block, head of
 // the group) pairs see: as many as give every SM of the device a CTA, of four
@@ -821,7 +827,7 @@ static attn_status_t bwd_impl(const void *q, const void *k, const void *v, const
     if (with_sinks) {
         p.sinks = std::min(sinks, Sk);
         p.sink_blocks = (int)sink_blocks;
-        p.sink_parts = sink_parts(Hq, Hkv, Sq);
+        p.sink_parts = sink_parts(B, Hq, Hkv, Sq, Sk, sinks);
         // Query blocks that a key block can be seen by: those of its window.
         long long seen = (window_left + (long long)std::max(window_right, 0) + 127) / 128 + 2;
         if (!causal && window_right < 0) seen = num_qb;
@@ -839,8 +845,9 @@ size_t attn_bwd_sinks_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int
     // Sums of all parts; at most the parts that any window would give.
     const size_t blocks = (std::min(sinks, Sk) + (size_t)127) / 128, others = (Sk + (size_t)127) / 128 - blocks;
     const size_t parts = other_parts(B, Hkv, Sk, (Sq + 127LL) / 128 * (Hq / Hkv));
-    return rows + (sink_parts(Hq, Hkv, Sq) * blocks + (parts > 1 ? parts * others : 0)) * B * Hkv * 2 * 128 * D *
-                      sizeof(float);
+    const size_t s_parts = sink_parts(B, Hq, Hkv, Sq, Sk, sinks);
+    if (s_parts == 1 && parts == 1) return rows;  // nothing is cut
+    return rows + (s_parts * blocks + (parts > 1 ? parts * others : 0)) * B * Hkv * 2 * 128 * D * sizeof(float);
 }
 
 attn_status_t attn_bwd_ex(const void *q, const void *k, const void *v, const void *o,

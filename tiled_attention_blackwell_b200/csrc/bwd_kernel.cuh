@@ -196,6 +196,7 @@ attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
             kb += p.sink_blocks - sink_rows - part * others;
             if (parts == 1) part = -1;
         }
+        if (p.sink_parts == 1 && p.other_parts == 1) part = -1;  // nothing is cut
     }
     const bool sinky = SINKS && kb < p.sink_blocks;
     const int hkv = bh % p.Hkv;

@@ -1017,8 +1017,9 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
             }
             if (row_ok) {
                 const float m_lse = PREC ? m_run - p.p_offset : m_run;
-                const float lse = l_run > 0.0f ? (m_lse + log2f(l_run)) * 0.69314718055994531f
-                                               : -INFINITY;
+                float lse = l_run > 0.0f ? (m_lse + log2f(l_run)) * 0.69314718055994531f
+                                         : -INFINITY;
+                if (SINKS == 2 && l_run != l_run) lse = l_run;  // the join must not take NaN for a part without a key
                 float *dst = SINKS == 2 ? p.part_lse + (size_t)ep * p.B * p.Hq * p.Sq : p.lse;
                 dst[((size_t)eb * p.Hq + eh) * p.Sq + row] = lse;
             }
@@ -1082,7 +1083,7 @@ attn_fwd_join_kernel(const __grid_constant__ FwdParams p) {
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     *reinterpret_cast<uint2 *>(p.o + (size_t)r * D + d) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (d == 0) p.lse[at] = sum == 0.0f ? -INFINITY : m + log2f(sum) * 0.69314718055994531f;
+    if (d == 0) p.lse[at] = sum > 0.0f ? m + log2f(sum) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace tab

@@ -137,10 +137,10 @@ attn_status_t launch_bwd(const tab::BwdParams &p, cudaStream_t stream) {
         // A CTA per part of a key block, and the sum of the parts.
         const int rows = p.sink_blocks * p.sink_parts + (p.num_kb - p.sink_blocks) * p.other_parts;
         k_dkdv<<<rows * p.Hkv * p.B, tab::kBwdThreads, smem_dkdv, stream>>>(p);
-        const int blocks = p.other_parts > 1 ? p.num_kb : p.sink_blocks;
+        const int blocks = p.other_parts > 1 ? p.num_kb : p.sink_parts > 1 ? p.sink_blocks : 0;
         const long long n = (long long)blocks * p.Hkv * p.B * 2 * 128 * (D / 4);
         const int grid = (int)std::min<long long>((n + 255) / 256, 148 * 8);
-        tab::attn_bwd_part_sum_kernel<D><<<grid, 256, 0, stream>>>(p, blocks);
+        if (blocks > 0) tab::attn_bwd_part_sum_kernel<D><<<grid, 256, 0, stream>>>(p, blocks);
     } else {
         k_dkdv<<<p.num_kb * p.Hkv * p.B, tab::kBwdThreads, smem_dkdv, stream>>>(p);
     }
