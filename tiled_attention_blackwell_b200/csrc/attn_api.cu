@@ -465,14 +465,21 @@ static attn_status_t fwd_impl(const void *q, const void *k, const void *v, void 
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     // First keys matter only beside a window's lower end.
     if (sinks > 0 && window_left >= 0) {
-        p.sinks = std::min(sinks, Sk);
-        p.parts = workspace ? fwd_parts(B, Hq, Sq, Sk, causal, window_left, window_right, sinks) : 1;
-        if (p.parts > 1) {
-            p.part_o = static_cast<float *>(workspace);
-            p.part_lse = p.part_o + (size_t)p.parts * B * Sq * Hq * D;
+        tab::WindowParams w;
+        memset(&w, 0, sizeof w);
+        static_cast<tab::FwdParams &>(w) = p;
+        if ((s = make_map(&w.tm_o, o, B, Sq, Hq, D, eb)) != ATTN_OK) return s;
+        w.sinks = std::min(sinks, Sk);
+        w.parts = workspace ? fwd_parts(B, Hq, Sq, Sk, causal, window_left, window_right, sinks) : 1;
+        w.head_group = (int)std::max<long long>(w.head_group, ((long long)B * Hq + 65534) / 65535);
+        w.groups = (int)(((long long)B * Hq + w.head_group - 1) / w.head_group);
+        if (w.num_qblocks > 65535) return fail(ATTN_ERR_UNSUPPORTED, "grid too large");
+        if (w.parts > 1) {
+            w.part_o = static_cast<float *>(workspace);
+            w.part_lse = w.part_o + (size_t)w.parts * B * Sq * Hq * D;
         }
-        return p.parts > 1 ? tab_host::dispatch_fwd_parts(p, grid, D, op.exp2_mode, mod, cs)
-                           : tab_host::dispatch_fwd_sinks(p, grid, D, op.exp2_mode, mod, cs);
+        return w.parts > 1 ? tab_host::dispatch_fwd_parts(w, D, op.exp2_mode, mod, cs)
+                           : tab_host::dispatch_fwd_sinks(w, D, op.exp2_mode, mod, cs);
     }
     if (fp8) return dispatch_fp8(p, grid, op.exp2_mode, cs);
     if (D == 128) return dispatch_exp<128, kStagesD128>(p, grid, op.exp2_mode, mod, cs);

@@ -114,11 +114,6 @@ struct FwdParams {
     // V per 128-key block; two 512-byte atoms each) and the tile counts.
     const uint8_t *sf_q, *sf_k, *sf_v;
     int nq_tiles, nk_tiles;
-    // SINKS kernels: first keys that stay visible beside the window; parts that
-    // each item's key blocks are cut into (1: none), and the parts' results:
-    // fp32 O [part][B][Sq][Hq][D], each normalised, and LSE [part][B][Hq][Sq].
-    int sinks, parts;
-    float *part_o, *part_lse;
 };
 
 // Opt-in event trace (compile with -DATTN_TRACE): lane 0 of warps 0 and 4
@@ -179,7 +174,6 @@ struct FwdSmem {
     uint32_t tmem_base;
     int abort_flag;
     int range[2][2];  // per query tile: first and last key block (inclusive)
-    int item[3];      // SINKS = 2: batch, query head and part, for the epilogue
 };
 
 // Column pairs that use the polynomial in EXP_MODE 1: one pair in eight,
@@ -226,24 +220,6 @@ __device__ __forceinline__ void exp_pack_half(const float *s, float c, float neg
         add_bf16x2_f32(r0s, r1s, h);
     }
     sum += (sum0 + sum1) + (sum2 + sum3);
-    sum_pv += r0s + r1s;
-}
-
-// The same for 32 scores of a masked block, all on MUFU: ex2(-inf) = 0 exactly.
-__device__ __forceinline__ void exp_pack_group(const float *s, float c, float neg_m, uint32_t *pk,
-                                               float &sum, float &sum_pv) {
-    float sum0 = 0.0f, sum1 = 0.0f, r0s = 0.0f, r1s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-        float x0, x1;
-        fma2(x0, x1, s[e], s[e + 1], c, c, neg_m, neg_m);
-        const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
-        add2(sum0, sum1, sum0, sum1, p0, p1);
-        const uint32_t h = pack_bf16x2(p0, p1);
-        pk[e >> 1] = h;
-        add_bf16x2_f32(r0s, r1s, h);
-    }
-    sum += sum0 + sum1;
     sum_pv += r0s + r1s;
 }
 
@@ -368,19 +344,10 @@ __device__ __forceinline__ void modify_scores(float *v, float c, float k1, float
     }
 }
 
-// SINKS: beside its interval (window, causal) a row sees keys j < sinks up to
-// the interval's upper end.  The blocks of a tile are then those of the first
-// keys and those of its window, at most two runs: the kernel walks the union
-// of both tiles' blocks under "virtual" indices in which the window's blocks
-// keep their own and the sb first blocks stand directly before them.  SINKS =
-// 2, for few items: the walk is cut into parts, a CTA each, which
-// attn_fwd_join_kernel joins by their LSEs.  (A kernel of its own: the counts
-// of a part cost the full-size forward 4 %.)
-template <int D, int NS, int EXP_MODE, int MOD = 0, int PREC = 0, int SINKS = 0>
+template <int D, int NS, int EXP_MODE, int MOD = 0, int PREC = 0>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 attn_fwd_kernel(const __grid_constant__ FwdParams p) {
     static_assert(!(PREC && MOD), "the low-precision paths have no score modifiers");
-    static_assert(!(PREC && SINKS), "first keys beside a window: bf16 operands only");
     constexpr bool FP8 = PREC == 1;
     constexpr bool DP = PREC >= 2;  // Direct-P
     constexpr int EB = FP8 ? 1 : 2;
@@ -400,12 +367,7 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
     const int G = p.head_group;
     const int nq = p.num_qblocks;
     const int full_groups = bh_count / G;
-    int lin = (int)blockIdx.x, part = 0;
-    if constexpr (SINKS == 2) {
-        part = lin / (bh_count * nq);
-        lin -= part * bh_count * nq;
-        launch_dependents();
-    }
+    const int lin = (int)blockIdx.x;
     int grp, r, ge;
     if (lin < full_groups * G * nq) {
         grp = lin / (G * nq);
@@ -438,11 +400,6 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
         }
         mbar_init(&sm.drain, 1);
         sm.abort_flag = 0;
-        if constexpr (SINKS == 2) {
-            sm.item[0] = b;
-            sm.item[1] = hq;
-            sm.item[2] = part;
-        }
         fence_mbar_init();
     }
     if (warp == 9) {
@@ -490,35 +447,9 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
     const int lo0 = sm.range[0][0], hi0 = sm.range[0][1];
     const int lo1 = sm.range[1][0], hi1 = sm.range[1][1];
     const bool has0 = lo0 <= hi0, has1 = lo1 <= hi1;
-    const int wlo = has0 ? (has1 ? min(lo0, lo1) : lo0) : lo1;
-    const int uhi0 = has0 ? (has1 ? max(hi0, hi1) : hi0) : hi1;
-    // Blocks with first keys; those before both tiles' windows come first.
-    const int nsb = SINKS ? (p.sinks + kBlockN - 1) / kBlockN : 0;
-    const int ulo0 = SINKS ? wlo - min(nsb, wlo) : wlo;
-    // Key block of virtual index j.
-    auto block_of = [&](int j) -> int { return !SINKS || j >= wlo ? j : j - ulo0; };
-    // This CTA's virtual indices [ulo, ulo + n_blocks), and per tile the number
-    // of its blocks before them (skip) and up to their end (upto).
-    int ulo = ulo0, n_blocks = (has0 || has1) ? (uhi0 - ulo0 + 1) : 0;
-    int skip0 = 0, skip1 = 0, upto0 = 0, upto1 = 0;
-    if constexpr (SINKS == 2) {
-        const int total = n_blocks;
-        ulo = ulo0 + (int)((long long)total * part / p.parts);
-        n_blocks = ulo0 + (int)((long long)total * (part + 1) / p.parts) - ulo;
-        // A tile's blocks with a virtual index below j: of its s first blocks,
-        // then of [lo, hi].
-        auto before = [&](bool has, int lo, int hi, int j) -> int {
-            if (!has) return 0;
-            const int s = min(nsb, lo);
-            if (j <= wlo) return min(j - ulo0, s);
-            return min(s, j) + max(0, min(j, hi + 1) - lo);
-        };
-        skip0 = before(has0, lo0, hi0, ulo);
-        skip1 = before(has1, lo1, hi1, ulo);
-        upto0 = before(has0, lo0, hi0, ulo + n_blocks);
-        upto1 = before(has1, lo1, hi1, ulo + n_blocks);
-    }
-    const int uhi = ulo + n_blocks - 1;
+    const int ulo = has0 ? (has1 ? min(lo0, lo1) : lo0) : lo1;
+    const int uhi = has0 ? (has1 ? max(hi0, hi1) : hi0) : hi1;
+    const int n_blocks = (has0 || has1) ? (uhi - ulo + 1) : 0;
 
     // Registers: the softmax warpgroups hold a 128-column score row per
     // thread; the MMA / TMA warpgroup needs few.  384 x 168 at launch =
@@ -533,7 +464,7 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                 uint32_t it = 0;
                 bool ok = true;
                 for (int t = 0; t < n_blocks && ok; ++t) {
-                    const int key0 = block_of(ulo + t) * kBlockN;
+                    const int key0 = (ulo + t) * kBlockN;
                     for (int which = 0; which < 2 && ok; ++which, ++it) {
                         const uint32_t slot = it % NS;
                         ok = wait_bounded(&sm.kv_empty[slot], ((it / NS) & 1u) ^ 1u, abort_flag,
@@ -618,11 +549,6 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                     __syncwarp();
                 };
                 auto active = [&](int i, int j) -> bool {
-                    if constexpr (SINKS) {
-                        const int kb = block_of(j);
-                        return i == 0 ? (has0 && (kb >= lo0 || kb < nsb) && kb <= hi0)
-                                      : (has1 && (kb >= lo1 || kb < nsb) && kb <= hi1);
-                    }
                     return i == 0 ? (has0 && j >= lo0 && j <= hi0)
                                   : (has1 && j >= lo1 && j <= hi1);
                 };
@@ -647,19 +573,10 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                         if (active(i, j)) {
                             const int lo_i = i == 0 ? lo0 : lo1;
                             const int hi_i = i == 0 ? hi0 : hi1;
-                            // Blocks of this tile before this one.
-                            int nth = j - lo_i;
-                            if constexpr (SINKS) {
-                                const int kb = block_of(j), s_i = min(nsb, lo_i);
-                                nth = kb < s_i ? kb : kb - lo_i + s_i;
-                                if (SINKS == 2) nth -= i == 0 ? skip0 : skip1;
-                            }
-                            const bool last =
-                                SINKS == 2 ? nth == (i == 0 ? upto0 - skip0 : upto1 - skip1) - 1 : j == hi_i;
-                            const uint32_t par = (uint32_t)nth & 1u;
+                            const uint32_t par = (uint32_t)(j - lo_i) & 1u;
                             const uint32_t o_tmem = tmem + 2 * kBlockN + i * D;
                             const uint32_t p_tmem = tmem + i * kBlockN;
-                            const uint32_t first = nth > 0 ? 1u : 0u;
+                            const uint32_t first = j > lo_i ? 1u : 0u;
                             // PV in two halves of 64 keys, each as soon as its P is in TMEM.
                             // V chunk: key rows of 128 bytes, 8-row groups 1024 B apart
                             // (SBO), 64-column chunks kChunkBytes apart (LBO).
@@ -686,7 +603,7 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                                 for (int ks = kPvSteps; ks < 2 * kPvSteps; ++ks)
                                     mma_ts_k<FP8>(o_tmem, p_tmem + ks * 8,
                                                   vb + ((ks * kPvK * 128) >> 4), kIdescPV, 1u);
-                                if (last) tc_commit(&sm.o_final[i]);
+                                if (j == hi_i) tc_commit(&sm.o_final[i]);
                             }
                             __syncwarp();
                         }
@@ -721,12 +638,9 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_tmem = tmem + lane_base + i * kBlockN;
         const uint32_t o_tmem = tmem + lane_base + 2 * kBlockN + i * D;
-        // SINKS: rows behind the last see what it sees (their results go nowhere).
-        KeyRange kr = row_key_range(p, SINKS ? min(row, p.Sq - 1) : row);
-        if (SINKS && kr.lo > kr.hi) kr.hi = -1;  // no key, so no first key either
+        const KeyRange kr = row_key_range(p, row);
         const int lo_b = i == 0 ? lo0 : lo1;
         const int hi_b = i == 0 ? hi0 : hi1;
-        const int s_b = SINKS && lo_b <= hi_b ? min(nsb, lo_b) : 0;  // blocks of first keys before the window
         const float c = p.scale_log2;
         const float tau = p.rescale_threshold;
         // With a modifier the scores are transformed into log2 units before
@@ -743,11 +657,8 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
         float l_pv = 0.0f;    // row sum of the p that PV consumes (the output's normaliser)
         bool ok = true;
 
-        // The tile's blocks (SINKS = 2: skip .. upto - 1 of them), in its order.
-        const int skip = i == 0 ? skip0 : skip1;
-        const int blocks = SINKS == 2 ? (i == 0 ? upto0 : upto1) - skip : hi_b - lo_b + 1 + s_b;
-        for (int t = 0; t < blocks; ++t) {
-            const int j = !SINKS || t + skip >= s_b ? lo_b - s_b + skip + t : skip + t;
+        for (int j = lo_b; j <= hi_b; ++j) {
+            const int t = j - lo_b;
             if ((warp & 3) == 0) ATTN_TRACE_EVENT(i, t, 0);
             ok = wait_bounded(&sm.s_full[i], (uint32_t)t & 1u, abort_flag, p.status, true, p.timeout_ns);
             ok = __all_sync(0xffffffffu, ok);
@@ -772,13 +683,11 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
 
             const int key0 = j * kBlockN;
             const float dist0 = diag_f - (float)key0;  // distance to key0 of this block
-            const bool need_mask = (key0 < kr.lo && (!SINKS || key0 + kBlockN > p.sinks)) ||
-                                   key0 + kBlockN - 1 > kr.hi;
+            const bool need_mask = key0 < kr.lo || key0 + kBlockN - 1 > kr.hi;
             const bool masked = __any_sync(0xffffffffu, need_mask);
             float alpha = 1.0f;
             float neg_m;
             float bm[4];  // Direct-P: maxima of the four 32-key blocks
-            uint32_t unseen = 0u;  // SINKS, masked blocks: groups of 32 keys that no row sees
             if constexpr (DP) {
                 // Direct-P: the anchor m is the running max rounded up to an
                 // integer, so every rescale is an exact power of two and the
@@ -801,30 +710,6 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                 }
                 neg_m = m_run == -INFINITY ? 0.0f : p.p_offset - m_run;
                 if ((warp & 3) == 0) ATTN_TRACE_EVENT(i, t, 3);
-            } else {
-            float row_max;
-            if (SINKS && masked) {
-                // By groups of 32 keys: one that no row of the warp sees is left out
-                // here and below, one that all see needs no mask.
-                row_max = -INFINITY;
-                unseen = 0u;
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const uint32_t bits = visible_bits(key0 + 32 * g, kr.lo, kr.hi, p.sinks);
-                    if (!__any_sync(0xffffffffu, bits != 0u)) {
-                        unseen |= 1u << g;
-                        continue;
-                    }
-                    if (MOD)
-                        modify_scores<MOD, 32>(s + 32 * g, c, k1, p.softcap_out, slope2,
-                                               dist0 - (float)(32 * g));
-                    if (!__all_sync(0xffffffffu, bits == ~0u)) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((bits >> e) & 1u)) s[32 * g + e] = -INFINITY;
-                    }
-                    row_max = fmaxf(row_max, block_max32(s + 32 * g));
-                }
             } else {
             if (MOD) modify_scores<MOD, kBlockN / 2>(s, c, k1, p.softcap_out, slope2, dist0);
             if (masked) {
@@ -858,8 +743,7 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
 #pragma unroll
                 for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], s[e + u], s[e + 4 + u]);
             if ((warp & 3) == 0) ATTN_TRACE_EVENT(i, t, 2);
-            row_max = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-            }
+            const float row_max = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
             const float m_cand = MOD ? row_max : row_max * c;
             ATTN_COUNT_BLOCK(t, m_cand > m_run, m_cand > m_run + tau);
             if (m_cand > m_run + tau) {
@@ -907,17 +791,6 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
             // this warp computes keys [64, 128).  Masked blocks (-inf scores)
             // use MUFU only: ex2(-inf) = 0 exactly.
             uint32_t pk[kBlockN / 2];
-            auto exp_groups = [&](int g0) {  // SINKS, masked: groups g0 and g0 + 1
-#pragma unroll
-                for (int g = g0; g < g0 + 2; ++g) {
-                    if ((unseen >> g) & 1u) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[16 * g + e] = 0u;
-                    } else {
-                        exp_pack_group(s + 32 * g, c_exp, neg_m, pk + 16 * g, l_run, l_pv);
-                    }
-                }
-            };
             if (MOD) __syncwarp();  // converged before the warp-collective TMEM store
             if constexpr (DP) {
                 l_run += direct_p_half<PREC>(s, bm, c, neg_m, pk);
@@ -929,10 +802,8 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                                 : exp_pack_half_fp8<EXP_MODE>(s, c_exp, neg_m, pk);
                 tmem_st16(s_tmem + 0, pk + 0);
             } else {
-                if (SINKS && masked) exp_groups(0);
-                else if (masked) exp_pack_half<0>(s, c_exp, neg_m, pk, l_run, l_pv);
+                if (masked) exp_pack_half<0>(s, c_exp, neg_m, pk, l_run, l_pv);
                 else exp_pack_half<EXP_MODE>(s, c_exp, neg_m, pk, l_run, l_pv);
-                if (SINKS) __syncwarp();
                 tmem_st32(s_tmem + 0, pk + 0);
             }
             tmem_wait_st();
@@ -949,11 +820,9 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                 if ((warp & 3) == 0) ATTN_TRACE_EVENT(i, t, 4);
                 tmem_st16(s_tmem + 16, pk + 16);
             } else {
-                if (SINKS && masked) exp_groups(2);
-                else if (masked) exp_pack_half<0>(s + 64, c_exp, neg_m, pk + 32, l_run, l_pv);
+                if (masked) exp_pack_half<0>(s + 64, c_exp, neg_m, pk + 32, l_run, l_pv);
                 else exp_pack_half<EXP_MODE>(s + 64, c_exp, neg_m, pk + 32, l_run, l_pv);
                 if ((warp & 3) == 0) ATTN_TRACE_EVENT(i, t, 4);
-                if (SINKS) __syncwarp();
                 tmem_st32(s_tmem + 32, pk + 32);
             }
             tmem_wait_st();
@@ -963,7 +832,7 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
         }
 
         // ----------------------------------------------------------- epilogue
-        const bool has_blocks = blocks > 0;
+        const bool has_blocks = lo_b <= hi_b;
         if (ok && has_blocks) {
             ok = wait_bounded(&sm.o_final[i], 0, abort_flag, p.status, true, p.timeout_ns);
             ok = __all_sync(0xffffffffu, ok);
@@ -976,12 +845,8 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
             // it; Direct-P's sum is already over the values PV consumes).
             const float l_out = PREC ? l_run : l_pv;
             const float inv_l = l_out > 0.0f ? (PREC ? p.v_descale : 1.0f) / l_out : 0.0f;
-            // (SINKS = 2: from shared memory, so that no register holds them till here.)
-            const int eb = SINKS == 2 ? *(volatile int *)&sm.item[0] : b;
-            const int eh = SINKS == 2 ? *(volatile int *)&sm.item[1] : hq;
-            const int ep = SINKS == 2 ? *(volatile int *)&sm.item[2] : 0;
             __nv_bfloat16 *o_row =
-                p.o + (((size_t)eb * p.Sq + row) * p.Hq + eh) * (size_t)D;
+                p.o + (((size_t)b * p.Sq + row) * p.Hq + hq) * (size_t)D;
 #pragma unroll
             for (int ch = 0; ch < D / 32; ++ch) {
                 uint32_t r[32];
@@ -999,17 +864,7 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
                 for (int e = 0; e < 16; ++e)
                     w[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * inv_l,
                                        __uint_as_float(r[2 * e + 1]) * inv_l);
-                if (SINKS == 2) {
-                    if (row_ok) {
-                        float4 *dst = reinterpret_cast<float4 *>(
-                            p.part_o + ((((size_t)ep * p.B + eb) * p.Sq + row) * p.Hq + eh) * (size_t)D + ch * 32);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(__uint_as_float(r[4 * e]) * inv_l, __uint_as_float(r[4 * e + 1]) * inv_l,
-                                                 __uint_as_float(r[4 * e + 2]) * inv_l,
-                                                 __uint_as_float(r[4 * e + 3]) * inv_l);
-                    }
-                } else if (row_ok) {
+                if (row_ok) {
                     uint4 *dst = reinterpret_cast<uint4 *>(o_row + ch * 32);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) dst[e] = out[e];
@@ -1017,11 +872,9 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
             }
             if (row_ok) {
                 const float m_lse = PREC ? m_run - p.p_offset : m_run;
-                float lse = l_run > 0.0f ? (m_lse + log2f(l_run)) * 0.69314718055994531f
-                                         : -INFINITY;
-                if (SINKS == 2 && l_run != l_run) lse = l_run;  // the join must not take NaN for a part without a key
-                float *dst = SINKS == 2 ? p.part_lse + (size_t)ep * p.B * p.Hq * p.Sq : p.lse;
-                dst[((size_t)eb * p.Hq + eh) * p.Sq + row] = lse;
+                const float lse = l_run > 0.0f ? (m_lse + log2f(l_run)) * 0.69314718055994531f
+                                               : -INFINITY;
+                p.lse[((size_t)b * p.Hq + hq) * p.Sq + row] = lse;
             }
         }
 #ifdef ATTN_COUNT_RESCALES
@@ -1048,42 +901,6 @@ attn_fwd_kernel(const __grid_constant__ FwdParams p) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
-}
-
-// Joins the parts of attn_fwd_kernel<..., SINKS = 2>: O = sum_s w_s O_s, w_s =
-// exp(LSE_s - LSE).  D / 4 lanes per row of O; the parts in order.
-constexpr int kFwdJoinThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kFwdJoinThreads)
-attn_fwd_join_kernel(const __grid_constant__ FwdParams p) {
-    constexpr int kLanes = D / 4;
-    wait_for_primary();
-    const long long rows = (long long)p.B * p.Sq * p.Hq;
-    const long long r = (long long)blockIdx.x * (kFwdJoinThreads / kLanes) + threadIdx.x / kLanes;
-    const int d = (threadIdx.x % kLanes) * 4;
-    if (r >= rows) return;
-    const int hq = (int)(r % p.Hq), row = (int)(r / p.Hq % p.Sq), b = (int)(r / p.Hq / p.Sq);
-    const size_t at = ((size_t)b * p.Hq + hq) * p.Sq + row;
-    const size_t lses = (size_t)p.B * p.Hq * p.Sq;
-    float m = -INFINITY;
-    for (int s = 0; s < p.parts; ++s) m = fmaxf(m, p.part_lse[s * lses + at]);
-    float sum = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s = 0; s < p.parts; ++s) {
-        const float l = p.part_lse[s * lses + at];
-        const float4 v = *reinterpret_cast<const float4 *>(p.part_o + ((size_t)s * rows + r) * D + d);
-        if (l == -INFINITY) continue;  // no key of this part
-        const float w = ex2_mufu((l - m) * kLog2eF);
-        sum += w;
-        o.x = fmaf(v.x, w, o.x);
-        o.y = fmaf(v.y, w, o.y);
-        o.z = fmaf(v.z, w, o.z);
-        o.w = fmaf(v.w, w, o.w);
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    *reinterpret_cast<uint2 *>(p.o + (size_t)r * D + d) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (d == 0) p.lse[at] = sum > 0.0f ? m + log2f(sum) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace tab

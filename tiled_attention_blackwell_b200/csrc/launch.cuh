@@ -7,17 +7,16 @@
 #include "bwd_kernel.cuh"
 #include "fwd_kernel.cuh"
 #include "fwd_persistent.cuh"
+#include "fwd_window.cuh"
 #include "host_common.h"
 
 namespace tab_host {
 
-// The SINKS variants of the forward (one CTA per item, or p.parts of them)
-// and the backward, in translation units of their own: they compile side by
-// side.  sinks_fwd.cu, sinks_parts.cu, sinks_bwd.cu
-attn_status_t dispatch_fwd_sinks(const tab::FwdParams &p, int grid, int D, int exp_mode, int mod,
-                                 cudaStream_t stream);
-attn_status_t dispatch_fwd_parts(const tab::FwdParams &p, int grid, int D, int exp_mode, int mod,
-                                 cudaStream_t stream);
+// Windows with first keys that stay visible: the forward (one CTA per item, or
+// p.parts of them) and the backward, in translation units of their own: they
+// compile side by side.  sinks_fwd.cu, sinks_parts.cu, sinks_bwd.cu
+attn_status_t dispatch_fwd_sinks(const tab::WindowParams &p, int D, int exp_mode, int mod, cudaStream_t stream);
+attn_status_t dispatch_fwd_parts(const tab::WindowParams &p, int D, int exp_mode, int mod, cudaStream_t stream);
 attn_status_t dispatch_bwd_sinks(const tab::BwdParams &p, int D, int mod, cudaStream_t stream);
 
 }  // namespace tab_host
@@ -28,64 +27,91 @@ using tab_host::fail;
 using tab_host::kMaxDevices;
 using tab_host::ok;
 
-// PERSIST selects the persistent kernel (fwd_persistent.cuh: one CTA per SM
-// running many items), otherwise one CTA per item.
-template <int D, int NS, int EXP, int MOD = 0, int PREC = 0, bool PERSIST = false,
-          int SINKS = 0>
-attn_status_t launch_fwd(const tab::FwdParams &p, int grid, cudaStream_t stream) {
-    using Smem = std::conditional_t<PERSIST, tab::FwdSmemPersistent<D, NS, PREC == 1 ? 1 : 2>,
-                                    tab::FwdSmem<D, NS, PREC == 1 ? 1 : 2>>;
-    constexpr size_t smem = sizeof(Smem) + 1024;
-    static_assert(smem <= 232448, "shared memory budget");
-    auto kernel = []() {
-        if constexpr (PERSIST) return tab::attn_fwd_persistent_kernel<D, NS, EXP, MOD, PREC>;
-        else return tab::attn_fwd_kernel<D, NS, EXP, MOD, PREC, SINKS>;
-    }();
-    static std::once_flag once[kMaxDevices];
-    static cudaError_t attr_err[kMaxDevices];
+// A forward kernel of kFwdThreads threads that moves registers between its
+// warpgroups (setmaxnreg), and what is asked of it once per device.
+struct PreparedFwd {
+    std::once_flag once[kMaxDevices];
+    cudaError_t err[kMaxDevices];
+    cudaFuncAttributes attrs[kMaxDevices];
+};
+template <class Params>
+attn_status_t launch_fwd_kernel(PreparedFwd &st, void (*kernel)(Params), const Params &p, dim3 grid, size_t smem,
+                                cudaStream_t stream) {
     int dev = 0;
     cudaGetDevice(&dev);
-    std::call_once(once[dev], [&]() {
-        attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
+    std::call_once(st.once[dev], [&]() {
+        st.err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (st.err[dev] == cudaSuccess) st.err[dev] = cudaFuncGetAttributes(&st.attrs[dev], kernel);
     });
-    if (attr_err[dev] != cudaSuccess)
-        return fail(ATTN_ERR_LAUNCH, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err[dev]));
-    // The kernel moves registers between warpgroups with setmaxnreg; if the
-    // compiled per-thread count does not cover the split, the increase would
-    // wait forever, so never launch such a build.
-    static cudaFuncAttributes attrs[kMaxDevices];
-    static cudaError_t attrs_err[kMaxDevices];
-    static std::once_flag attrs_once[kMaxDevices];
-    std::call_once(attrs_once[dev], [&]() { attrs_err[dev] = cudaFuncGetAttributes(&attrs[dev], kernel); });
-    if (attrs_err[dev] != cudaSuccess)
-        return fail(ATTN_ERR_LAUNCH, "cudaFuncGetAttributes: %s", cudaGetErrorString(attrs_err[dev]));
-    if (attrs[dev].numRegs < tab::kLaunchRegs)
+    if (st.err[dev] != cudaSuccess)
+        return fail(ATTN_ERR_LAUNCH, "kernel attributes: %s", cudaGetErrorString(st.err[dev]));
+    // If the compiled per-thread count does not cover the register split, the
+    // increase would wait forever, so never launch such a build.
+    if (st.attrs[dev].numRegs < tab::kLaunchRegs)
         return fail(ATTN_ERR_LAUNCH, "kernel compiled with %d registers per thread, %d needed",
-                    attrs[dev].numRegs, tab::kLaunchRegs);
+                    st.attrs[dev].numRegs, tab::kLaunchRegs);
     kernel<<<grid, tab::kFwdThreads, smem, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "launch: %s", cudaGetErrorString(e));
     return ok();
 }
 
+// PERSIST selects the persistent kernel (fwd_persistent.cuh: one CTA per SM
+// running many items), otherwise one CTA per item.
+template <int D, int NS, int EXP, int MOD = 0, int PREC = 0, bool PERSIST = false>
+attn_status_t launch_fwd(const tab::FwdParams &p, int grid, cudaStream_t stream) {
+    using Smem = std::conditional_t<PERSIST, tab::FwdSmemPersistent<D, NS, PREC == 1 ? 1 : 2>,
+                                    tab::FwdSmem<D, NS, PREC == 1 ? 1 : 2>>;
+    constexpr size_t smem = sizeof(Smem) + 1024;
+    static_assert(smem <= 232448, "shared memory budget");
+    static PreparedFwd st;
+    if constexpr (PERSIST)
+        return launch_fwd_kernel(st, tab::attn_fwd_persistent_kernel<D, NS, EXP, MOD, PREC>, p, grid, smem, stream);
+    else
+        return launch_fwd_kernel(st, tab::attn_fwd_kernel<D, NS, EXP, MOD, PREC>, p, grid, smem, stream);
+}
+
+template <int D, int NS, int EXP, int MOD, bool PARTS>
+attn_status_t launch_window(const tab::WindowParams &p, cudaStream_t stream) {
+    constexpr size_t smem = sizeof(tab::WindowSmem<D, NS>) + 1024;
+    static_assert(smem <= 232448, "shared memory budget");
+    static PreparedFwd st;
+    return launch_fwd_kernel(st, tab::attn_fwd_window_kernel<D, NS, EXP, MOD, PARTS>, p,
+                             dim3(p.head_group, p.num_qblocks, p.groups * p.parts), smem, stream);
+}
+
 constexpr int kStagesD128 = 4;
 constexpr int kStagesD64 = 8;
 
-template <int D, int NS, int SINKS = 0>
+// With a score modifier the exponentials all run on MUFU.
+template <int D, int NS>
 attn_status_t dispatch_exp(const tab::FwdParams &p, int grid, int exp_mode, int mod,
                            cudaStream_t s) {
-    // With a score modifier the exponentials all run on MUFU.
     switch (mod) {
-        case 1: return launch_fwd<D, NS, 0, 1, 0, false, SINKS>(p, grid, s);
-        case 2: return launch_fwd<D, NS, 0, 2, 0, false, SINKS>(p, grid, s);
-        case 3: return launch_fwd<D, NS, 0, 3, 0, false, SINKS>(p, grid, s);
+        case 1: return launch_fwd<D, NS, 0, 1>(p, grid, s);
+        case 2: return launch_fwd<D, NS, 0, 2>(p, grid, s);
+        case 3: return launch_fwd<D, NS, 0, 3>(p, grid, s);
         default: break;
     }
     switch (exp_mode) {
-        case 0: return launch_fwd<D, NS, 0, 0, 0, false, SINKS>(p, grid, s);
-        case 1: return launch_fwd<D, NS, 1, 0, 0, false, SINKS>(p, grid, s);
-        default: return launch_fwd<D, NS, 2, 0, 0, false, SINKS>(p, grid, s);
+        case 0: return launch_fwd<D, NS, 0>(p, grid, s);
+        case 1: return launch_fwd<D, NS, 1>(p, grid, s);
+        default: return launch_fwd<D, NS, 2>(p, grid, s);
+    }
+}
+
+template <int D, int NS, bool PARTS>
+attn_status_t dispatch_window(const tab::WindowParams &p, int exp_mode, int mod, cudaStream_t s) {
+    switch (mod) {
+        case 1: return launch_window<D, NS, 0, 1, PARTS>(p, s);
+        case 2: return launch_window<D, NS, 0, 2, PARTS>(p, s);
+        case 3: return launch_window<D, NS, 0, 3, PARTS>(p, s);
+        default: break;
+    }
+    switch (exp_mode) {
+        case 0: return launch_window<D, NS, 0, 0, PARTS>(p, s);
+        case 1: return launch_window<D, NS, 1, 0, PARTS>(p, s);
+        default: return launch_window<D, NS, 2, 0, PARTS>(p, s);
     }
 }
 

@@ -1,8 +1,8 @@
-// The forward kernels whose rows see first keys beside their window.
+// The forward under a window with first keys that stay visible.
 #include "launch.cuh"
 
-attn_status_t tab_host::dispatch_fwd_sinks(const tab::FwdParams &p, int grid, int D, int exp_mode,
-                                           int mod, cudaStream_t stream) {
-    return D == 128 ? dispatch_exp<128, kStagesD128, 1>(p, grid, exp_mode, mod, stream)
-                    : dispatch_exp<64, kStagesD64, 1>(p, grid, exp_mode, mod, stream);
+attn_status_t tab_host::dispatch_fwd_sinks(const tab::WindowParams &p, int D, int exp_mode, int mod,
+                                           cudaStream_t stream) {
+    return D == 128 ? dispatch_window<128, kStagesD128, false>(p, exp_mode, mod, stream)
+                    : dispatch_window<64, kStagesD64, false>(p, exp_mode, mod, stream);
 }
