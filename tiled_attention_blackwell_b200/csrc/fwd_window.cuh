@@ -191,13 +191,12 @@ attn_fwd_window_kernel(const __grid_constant__ WindowParams p) {
                 mbar_init(&sm.kv_empty[s], 1);
             }
             fence_mbar_init();
-            for (int i = 0; i < 2; ++i) {
+            auto copy_q = [&](int i) {
                 mbar_arrive_expect_tx(&sm.q_full[i], kTileBytes);
                 for (int c = 0; c < Smem::kChunks; ++c)
                     tma_load_4d(sm.q[i][c], &p.tm_q, &sm.q_full[i], c * 64, q0 + i * kBlockM, hq, b);
-            }
-        }
-        if (lane == 0) {
+            };
+            copy_q(0);
             // Key blocks of each query tile: from the first row's to the last's; in a tile
             // whose first rows have no key, the first row with one sees key 0.
             for (int i = 0; i < 2; ++i) {
@@ -214,6 +213,7 @@ attn_fwd_window_kernel(const __grid_constant__ WindowParams p) {
                 copy_kv(0, false, walk.block(walk.active(0, t0) ? 0 : 1, t0));
                 if (walk.apart(t0)) copy_kv(1, false, walk.block(1, t0));
             }
+            copy_q(1);
             for (int i = 0; i < 2; ++i) {
                 sm.walk[i][0] = walk.shared;
                 sm.walk[i][1] = (i == 0 ? walk.own0 : walk.own1) - walk.shared;
