@@ -15,6 +15,15 @@
 //    row of a warp sees is left out, one that all see is not masked.
 //  - PARTS, for few items: the walk's steps are cut into parts, a CTA each,
 //    which attn_fwd_join_kernel joins by their LSEs.
+//
+// Measured on 2 x 8192 tokens, 16 heads of 128, four first tokens, in turn with
+// the plain kernel under this mask: window 1024 209 -> 193 us, window 512 148 ->
+// 132, window 128 100 -> 84.  Of a CTA's 43000 cycles at window 1024 the first
+// scores take 4000 and the ends 5000; a step takes 3600 for both tiles, as in
+// the plain forward (softmax warps).  One tile per CTA and two CTAs per SM ran
+// as long (a ring of two slots: 3600 cycles a step too); multiplying only the
+// 32 first keys of a block that has no more cost the issuing warp more than it
+// saved (198 us).
 #pragma once
 
 #include "fwd_kernel.cuh"
