@@ -394,3 +394,45 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for i, res in enumerate(got):
             assert all(torch.equal(x, y) for x, y in zip(res, want[i % 2]))
+
+
+@pytest.mark.parametrize("Sq", [1000, 200])
+@pytest.mark.parametrize("parts", [False, True])
+def test_a_wait_that_runs_out_is_reported(Sq, parts):
+    """As for the plain forward: the first CTA withholds a key copy (nothing
+    faults), in one piece (without a workspace) and in parts; the next call is
+    right again."""
+    shape, mask = (1, 4, 2, Sq, 1500, 128), dict(causal=True, window=(900, 0), sinks=4)
+    t = make_tensors(*shape, 38)
+    g = {n: x.to(DEV) for n, x in t.items()}
+    opts = attn.default_options(wait_timeout_us=20000, debug_withhold_kv=1)
+    size = attn.sinks_workspace_size(*shape, True, (900, 0), 4)
+    assert size > 0
+    ws = torch.zeros(size, dtype=torch.uint8, device=DEV) if parts else None
+    o, lse = torch.empty_like(g["q"]), torch.empty(1, 4, Sq, device=DEV)
+    attn.attn_fwd(g["q"], g["k"], g["v"], o, lse, scale=128 ** -0.5, options=opts, workspace=ws, **mask)
+    assert attn.device_status() == attn.ATTN_ERR_DEVICE_TIMEOUT
+    assert attn.device_status() == attn.ATTN_OK
+    attn.attn_fwd(g["q"], g["k"], g["v"], o, lse, scale=128 ** -0.5, workspace=ws, **mask)
+    check_forward(t, o, lse, 128 ** -0.5, visible(Sq, 1500, True, (900, 0), 4))
+
+
+def test_tiles_at_the_ends_of_rows_and_groups():
+    """Last tiles of one row, heads that do not fill the last schedule group, and
+    rows before the first key beside rows behind it."""
+    for heads in ((9, 9), (20, 2)):
+        case(1, *heads, 257, 257, 64, seed=39, window=(60, 0), sinks=3)
+        case(3, *heads, 129, 100, 64, seed=40, window=(60, 0), sinks=3)
+    case(1, 2, 2, 513, 300, 128, seed=41, window=(130, 0), sinks=200)
+    case(1, 2, 2, 640, 200, 128, seed=42, causal=False, window=(130, 100), sinks=20)
+
+
+def test_the_output_may_be_a_view_aligned_to_16_bytes():
+    t = make_tensors(1, 2, 2, 300, 300, 64, 43)
+    g = {n: x.to(DEV) for n, x in t.items()}
+    kw = dict(scale=0.125, causal=True, window=(80, 0), sinks=4)
+    want, _ = attn.attention(g["q"], g["k"], g["v"], **kw)
+    buf = torch.full((300 * 2 * 64 + 24,), 7.0, dtype=torch.bfloat16, device=DEV)
+    o, lse = buf[8:8 + 300 * 2 * 64].view(1, 300, 2, 64), torch.empty(1, 2, 300, device=DEV)
+    attn.attn_fwd(g["q"], g["k"], g["v"], o, lse, **kw)
+    assert torch.equal(o, want) and (buf[:8] == 7).all() and (buf[-16:] == 7).all()

@@ -91,11 +91,6 @@ struct TileWalk {
     __device__ __forceinline__ int block(int i, int t) const {
         return t >= shared ? (i == 0 ? own0 : own1) + t - shared : t < first ? t : next + t - first;
     }
-    // Tiles of K and V that the steps before t copy: two a step, four where the
-    // tiles are apart.  A step's are K, V, or both tiles' K and then both V.
-    __device__ __forceinline__ int copies(int t) const {
-        return 2 * t + 2 * max(0, min(t, min(n0, n1)) - shared);
-    }
 };
 
 // exp_pack_half for 32 scores of a masked block, all on MUFU: ex2(-inf) = 0 exactly.
@@ -115,7 +110,6 @@ __device__ __forceinline__ void exp_pack_group(const float *s, float c, float ne
     sum += sum0 + sum1;
     sum_pv += r0s + r1s;
 }
-
 
 template <int D, int NS>
 struct WindowSmem {
