@@ -235,7 +235,7 @@ def test_sinks_refusals(L, call, kw, status):
 def test_sinks_forward_workspace(L):
     # 777 queries of 8 heads are 4 x 8 items of 256 rows: 4 parts of two blocks or more each fill 148 SMs
     need = attn.sinks_workspace_size(1, 8, 2, 777, 2345, 64, True, (500, 0), 130)
-    assert need == 3 * 777 * 8 * 65 * 4  # (500 + 256 + 130) / 128 + 1 = 7 blocks: 3 parts
+    assert need == 4 * 777 * 8 * 65 * 4  # (500 + 255) / 128 + 1 steps of the window, 2 of first keys: 8, in 4 parts
     assert attn.sinks_workspace_size(1, 8, 2, 777, 2345, 64, True, (5000, 0), 130) == 4 * 777 * 8 * 65 * 4
     assert attn.sinks_workspace_size(2, 16, 16, 8192, 8192, 128, True, (1023, 0), 4) == 0  # fills the device
     assert attn.sinks_workspace_size(1, 2, 2, 100, 200, 128, True, (10, 0), 4) == 0  # one block

@@ -340,20 +340,22 @@ void attn_fwd_default_options(attn_fwd_options_t *opts) {
     opts->exp2_mode = 1;
 }
 
-// Parts that the key blocks of an item (256 query rows of a head) are cut into
+// Parts that the steps of an item (256 query rows of a head) are cut into
 // (attn_fwd_sinks): as many as give every SM of the device a CTA, each with
-// two blocks at least.  A block takes about 2 us: a chunk of 777 queries of 8
-// heads, 32 items of 6 to 9 blocks, takes 23 us whole and 18 in three parts
-// with their join; items that fill the device are not cut.
+// two steps at least, where there are six or more.  A step takes about 2 us,
+// and so does the join: 777 queries of 8 heads under a window of 501 keys
+// (8 steps) take 19.9 us whole, 16.5 in three parts, 14.6 in four; 600 of 16
+// heads under 301 (5 steps) 12.9 whole, 14.4 in two parts.  Items that fill the
+// device are not cut.
 constexpr int kFwdPartCtas = 148;
 static int fwd_parts(int B, int Hq, int Sq, int Sk, int causal, int window_left, int window_right,
                      int sinks) {
     const long long items = (Sq + 2LL * tab::kBlockM - 1) / (2LL * tab::kBlockM) * Hq * B;
-    // Most keys that an item can see, in blocks.
-    long long keys = window_left + 2LL * tab::kBlockM + sinks;
-    if (!causal) keys = window_right < 0 ? Sk : keys + window_right;
-    const long long blocks = std::min((long long)Sk, keys) / tab::kBlockN + 1;
-    return (int)std::max(1LL, std::min(kFwdPartCtas / items, blocks / 2));
+    // Steps of an item, about: the blocks of a tile's window and of its first keys.
+    long long window = window_left + 255LL;
+    if (!causal) window = window_right < 0 ? Sk : window + window_right;
+    const long long steps = std::min((Sk + 127LL) / tab::kBlockN, window / tab::kBlockN + 1 + (sinks + 127LL) / tab::kBlockN);
+    return steps < 6 ? 1 : (int)std::max(1LL, std::min(kFwdPartCtas / items, steps / 2));
 }
 
 // The forward of both entry points.  fp8: Q, K, V are e4m3 codes with the
