@@ -150,7 +150,8 @@ ATTN_API attn_status_t attn_fwd_ex(const void *q, const void *k, const void *v, 
  * key j is visible for row i iff the upper ends allow it (causal,
  * window_right) and j >= i + shift - window_left or j < sinks.  sinks >= 0;
  * without a window's lower end (window_left = -1) they change nothing.  The
- * other rules are those of attn_fwd_ex; there is no document mask.
+ * other rules are those of attn_fwd_ex; there is no document mask, and Sq is
+ * at most 65535 * 256.
  * workspace: NULL, or device memory of at least
  * attn_fwd_sinks_workspace_size() bytes, 16-byte aligned (contents on entry
  * ignored).  With one, calls of few rows cut each row's keys into parts that
