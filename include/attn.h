@@ -391,7 +391,8 @@ ATTN_API attn_status_t attn_bwd_noalloc(const void *q, const void *k, const void
  * cos, sin: fp32 [max_positions][rot/2]; positions: int32 [tokens].  Weights
  * and tables 16-byte aligned.  D is 64 or 128; rot a multiple of 16 in
  * [16, D]; eps >= 0; tokens >= 1.  Everything is computed in fp32 and rounded
- * once.  A position outside [0, max_positions) is clamped and makes
+ * once; the sum of a head's squares has to be one that fp32 holds (values up to
+ * 1e18 in size; with eps = 0 not all below 1e-18).  A position outside [0, max_positions) is clamped and makes
  * attn_get_device_status() report ATTN_ERR_RANGE.
  */
 ATTN_API attn_status_t attn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,

@@ -225,6 +225,29 @@ def test_backward_against_differences():
             assert abs(float(dw[d]) - want) <= 1e-4
 
 
+@pytest.mark.parametrize("size,eps", [(1e-17, 0.0), (1e-13, 0.0), (1e-13, 1e-6), (1e14, 1e-6), (1e15, 1e-6), (1e17, 1e-6)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_far_from_one(size, eps, D):
+    """Inputs whose squares fp32 still holds (sums of 128 of them included), but
+    not the cube of their norm: the bounds are those of ordinary inputs."""
+    shape = (5, 3, 2, D, D)
+    q, k, _, qw, kw, cos, sin, pos, c, s = inputs(*shape, seed=31, w_dtype=torch.float32)
+    q, k = ((x.double() * size).to(torch.bfloat16) for x in (q, k))
+    g = torch.Generator().manual_seed(32)
+    dq, dk = (torch.randn(x.shape, generator=g).to(DEV) for x in (q, k))
+    out = attn.qk_norm_rope(q, k, qw, kw, cos, sin, pos, eps=eps)
+    dqi, dki, dqw, dkw = attn.qk_norm_rope_backward(dq, dk, q, k, qw, kw, cos, sin, pos, eps=eps)
+    for y, dy, x, w, dx, dw in ((out[0], dq, q, qw, dqi, dqw), (out[1], dk, k, kw, dki, dkw)):
+        want, bound, R = reference(x, w, c, s, D, eps, False)
+        within(y, want, bound)
+        want, bound, want_w, size_w = backward_reference(dy, x, w, R, D, eps)
+        within(dx, want, bound)
+        x = x.double().cpu()
+        r = (x.pow(2).mean(-1, keepdim=True) + eps).rsqrt()
+        mixed = size_w + (dy.double().cpu().abs().amax(-1, keepdim=True) * 2 * x.abs() * r).flatten(0, 1).sum(0)
+        within(dw, want_w, 2.0 ** -24 * (24 * mixed + 128 * size_w))
+
+
 def test_backward_into_a_packed_gradient_deterministic():
     T, Hq, Hkv, D = 700, 6, 2, 128
     q, k, _, qw, kw, cos, sin, pos, _, _ = inputs(T, Hq, Hkv, D, 128, seed=30)

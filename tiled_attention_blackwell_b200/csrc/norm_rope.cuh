@@ -8,7 +8,7 @@
 //   token's position, y_a = u_a c - u_b s, y_b = u_b c + u_a s, where the
 //   pair is (i, i + rot/2), or (2i, 2i + 1) when interleaved.
 // Backward, with g = R^T dy and h = w g:
-//   dx_d = r h_d - r^3 x_d (sum_e h_e x_e) / D
+//   dx_d = r (h_d - x_d r (r sum_e h_e x_e) / D)
 //   dw_d = sum over tokens and heads of g_d x_d r
 //
 // Bound by memory: two bytes in and two out per value (eight in all for a
@@ -381,7 +381,9 @@ __device__ __forceinline__ Pairs norm_rope_bwd_side(const NormRopeParams &p, con
                 mul2(gx.q[e], gx.q[e + 1], g.q[e], g.q[e + 1], x.q[e], x.q[e + 1]);
             }
             const float r = rsqrtf(head_sum<D>(lane_dot(x, x)) * (1.0f / D) + p.eps);
-            const float t = -(r * r * r) * (head_sum<D>(lane_dot(w, gx)) * (1.0f / D));
+            // dx = r (h - (x r) (r mean(h x))): x r and r mean(h x) are of the sizes of 1
+            // and h, where r^3 leaves fp32 long before the result does (|x| of 1e15).
+            const float t = -r * (head_sum<D>(lane_dot(w, gx)) * (1.0f / D));
             if (u >= heads) continue;
             Pairs dx;
 #pragma unroll
@@ -390,10 +392,12 @@ __device__ __forceinline__ Pairs norm_rope_bwd_side(const NormRopeParams &p, con
                 fma2(dw.q[e], dw.q[e + 1], gx.q[e], gx.q[e + 1], r, r, dw.q[e], dw.q[e + 1]);
                 mul2(g.p[e], g.p[e + 1], g.p[e], g.p[e + 1], w.p[e], w.p[e + 1]);
                 mul2(g.q[e], g.q[e + 1], g.q[e], g.q[e + 1], w.q[e], w.q[e + 1]);
-                mul2(dx.p[e], dx.p[e + 1], x.p[e], x.p[e + 1], t, t);
-                mul2(dx.q[e], dx.q[e + 1], x.q[e], x.q[e + 1], t, t);
-                fma2(dx.p[e], dx.p[e + 1], g.p[e], g.p[e + 1], r, r, dx.p[e], dx.p[e + 1]);
-                fma2(dx.q[e], dx.q[e + 1], g.q[e], g.q[e + 1], r, r, dx.q[e], dx.q[e + 1]);
+                mul2(dx.p[e], dx.p[e + 1], x.p[e], x.p[e + 1], r, r);
+                mul2(dx.q[e], dx.q[e + 1], x.q[e], x.q[e + 1], r, r);
+                fma2(dx.p[e], dx.p[e + 1], dx.p[e], dx.p[e + 1], t, t, g.p[e], g.p[e + 1]);
+                fma2(dx.q[e], dx.q[e + 1], dx.q[e], dx.q[e + 1], t, t, g.q[e], g.q[e + 1]);
+                mul2(dx.p[e], dx.p[e + 1], dx.p[e], dx.p[e + 1], r, r);
+                mul2(dx.q[e], dx.q[e + 1], dx.q[e], dx.q[e + 1], r, r);
             }
             store_bf16<INTERLEAVED>(dst + u * D, at, dx);
         }
