@@ -7,6 +7,7 @@ There is no fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -196,15 +197,38 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _handle(stream):
+    """A stream argument as an integer handle."""
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _torch_stream(stream, device):
+    """A stream argument (a stream, or its handle) as a torch stream."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _handle(stream)
+    if handle in (0, 1):  # cudaStreamLegacy; an ExternalStream of 0 would be a stream from torch's pool
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
+def _current(stream, device):
+    """A context in which torch allocates for a stream argument: memory that
+    belongs to another stream may still be in use there, and may be given
+    away there, while `stream` uses it."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    return torch.cuda.stream(_torch_stream(stream, device))
+
+
 def _slopes(alibi_slopes, Hq, device, stream):
     """ALiBi slopes as a contiguous CUDA fp32 [Hq] tensor that stays valid
     until the kernel that reads it has run on `stream`."""
     if alibi_slopes is None:
         return None
     if not torch.is_tensor(alibi_slopes) or not alibi_slopes.is_cuda:
-        alibi_slopes = torch.as_tensor(alibi_slopes, dtype=torch.float32).to(device)
-        if stream is not None:
-            alibi_slopes.record_stream(stream)
+        with _current(stream, device):
+            alibi_slopes = torch.as_tensor(alibi_slopes, dtype=torch.float32).to(device)
     if alibi_slopes.dtype != torch.float32 or not alibi_slopes.is_contiguous() \
             or alibi_slopes.numel() != Hq:
         raise TypeError("alibi_slopes must be a contiguous fp32 tensor of Hq entries")
@@ -592,18 +616,12 @@ def _native():
     return _binding
 
 
-def _handle(stream):
-    """A stream argument as an integer handle."""
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
 def _keep_for(stream, *tensors):
     """Tells the allocator that work on `stream` (a stream or its handle) uses
     tensors which were allocated on the current stream."""
     if stream is None:
         return
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=tensors[0].device)
+    stream = _torch_stream(stream, tensors[0].device)
     if stream.cuda_stream != torch.cuda.current_stream(tensors[0].device).cuda_stream:
         for t in tensors:
             t.record_stream(stream)
