@@ -4,6 +4,11 @@ of a decoding step through ``_binding.so``).
 Argument marshalling only: every step of the attention forward runs in the
 CUDA kernels of ``libattn.so``.  PyTorch supplies device memory and streams.
 There is no fallback: if the library is missing, every call raises.
+
+Calls run on the current stream or on the one given (``stream=``, a torch stream
+or its integer handle).  As elsewhere in PyTorch, a caller who gives one sees to
+it that the inputs are ready there (``stream.wait_stream(...)``) and live until
+it has read them, and lets the stream that reads the results wait for it.
 """
 from __future__ import annotations
 
@@ -221,6 +226,25 @@ def _current(stream, device):
     return torch.cuda.stream(_torch_stream(stream, device))
 
 
+def _on_stream(stream, q, call):
+    """The results of call() made with `stream` (a stream, or its handle) as the
+    current one: all that it allocates belongs to `stream`.  The results are
+    marked as used by the caller's stream too, where they are read (once that
+    stream waits for `stream`) and dropped; and by `stream`, for those that the
+    caller gave."""
+    if not torch.is_tensor(q) or q.device.type != "cuda":
+        return call()  # which refuses q
+    caller, own = torch.cuda.current_stream(q.device), _torch_stream(stream, q.device)
+    if own.cuda_stream == caller.cuda_stream and torch.cuda.current_device() == q.device.index:
+        return call()
+    with torch.cuda.stream(own):
+        out = call()
+    for t in out if isinstance(out, tuple) else (out,):
+        t.record_stream(caller)
+        t.record_stream(own)
+    return out
+
+
 def _slopes(alibi_slopes, Hq, device, stream):
     """ALiBi slopes as a contiguous CUDA fp32 [Hq] tensor that stays valid
     until the kernel that reads it has run on `stream`."""
@@ -310,8 +334,10 @@ def attention(q, k, v, *, scale=None, causal=False, window=None, doc_offsets=Non
     """Allocate O and LSE with torch and run the forward.  Returns (O, LSE)."""
     if sinks:
         _check_sinks(sinks, doc_offsets)
-        return _attention_sinks(q, k, v, scale, causal, window, sinks, options, stream, softcap,
-                                alibi_slopes)
+        args = (q, k, v, scale, causal, window, sinks, options, softcap, alibi_slopes)
+        if stream is not None:
+            return _on_stream(stream, q, lambda: _attention_sinks(*args))
+        return _attention_sinks(*args)
     B, Sq, Hq, D = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(D)
@@ -540,8 +566,10 @@ def attention_backward(q, k, v, o, lse, dout, *, scale=None, causal=False, windo
     the backward.  Returns (dQ, dK, dV)."""
     if sinks:
         _check_sinks(sinks, doc_offsets)
-        return _attention_backward_sinks(q, k, v, o, lse, dout, scale, causal, window, sinks,
-                                         stream, softcap, alibi_slopes)
+        args = (q, k, v, o, lse, dout, scale, causal, window, sinks, softcap, alibi_slopes)
+        if stream is not None:
+            return _on_stream(stream, q, lambda: _attention_backward_sinks(*args))
+        return _attention_backward_sinks(*args)
     B, Sq, Hq, D = q.shape
     _, Sk, Hkv, _ = k.shape
     if scale is None:
@@ -586,7 +614,8 @@ def attn_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, *, scale, causal=False, 
 # These calls are short (a decoding step makes one of each per layer): their
 # checks of the tensors and the allocation of outputs are native
 # (csrc/binding.cpp), since in Python they cost more than the launches.  So are
-# those of attention with sinks, whose windows keep the kernels short.
+# those of attention with sinks, whose windows keep the kernels short.  They run
+# on the current stream: _on_stream() makes the one that a caller gives current.
 
 _binding = None
 _bound = None  # the library whose functions the binding calls
@@ -647,13 +676,12 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6, int
     first `rot` values of a head are rotated, in halves or, with
     `interleaved`, in neighbouring pairs; positions int32 [...].  q_out and
     k_out are allocated unless given; they may be q and k themselves."""
-    if stream is None:
-        return _native().norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
-                                   q_out, k_out, None)
-    out = _native().norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out,
-                              k_out, _handle(stream))
-    _keep_for(stream, *out)
-    return out
+    if stream is not None:
+        return _on_stream(stream, q, lambda: qk_norm_rope(
+            q, k, q_weight, k_weight, cos, sin, positions, eps=eps, interleaved=interleaved,
+            q_out=q_out, k_out=k_out))
+    return _native().norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
+                               q_out, k_out)
 
 
 def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6,
@@ -662,15 +690,12 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos, sin, positions,
     bf16, such as attention_backward returns) and its inputs.  Returns
     (dq_in, dk_in, dq_weight, dk_weight): bf16 like q and k (allocated unless
     given: views of a packed gradient are fine), fp32 [D]."""
-    if stream is None:
-        return _native().norm_rope_backward(q, k, q_weight, k_weight, cos, sin, positions, eps,
-                                            interleaved, dq, dk, dq_in, dk_in, None, None)
-    ws = torch.empty(lib().attn_qk_norm_rope_bwd_workspace_size(q.shape[-1]), dtype=torch.uint8,
-                     device=q.device)
-    out = _native().norm_rope_backward(q, k, q_weight, k_weight, cos, sin, positions, eps,
-                                       interleaved, dq, dk, dq_in, dk_in, ws, _handle(stream))
-    _keep_for(stream, ws, *out)
-    return out
+    if stream is not None:
+        return _on_stream(stream, q, lambda: qk_norm_rope_backward(
+            dq, dk, q, k, q_weight, k_weight, cos, sin, positions, eps=eps, interleaved=interleaved,
+            dq_in=dq_in, dk_in=dk_in))
+    return _native().norm_rope_backward(q, k, q_weight, k_weight, cos, sin, positions, eps,
+                                        interleaved, dq, dk, dq_in, dk_in)
 
 
 def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos, sin, positions, slots, k_cache, v_cache, *,
@@ -682,19 +707,16 @@ def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos, sin, positions, slots, 
     float8_e4m3fn (codes of value / descale).  slots int32 [...], distinct; a
     negative slot marks padding, for which nothing is written (its row of
     q_out keeps what it held)."""
-    if stream is None:
-        return _native().norm_rope_cache(q, k, q_weight, k_weight, cos, sin, positions, eps,
-                                         interleaved, v, slots, k_cache, v_cache, k_descale,
-                                         v_descale, q_out, None)
-    out = _native().norm_rope_cache(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
-                                    v, slots, k_cache, v_cache, k_descale, v_descale, q_out,
-                                    _handle(stream))
-    _keep_for(stream, out)
-    return out
+    if stream is not None:
+        return _on_stream(stream, q, lambda: qk_norm_rope_cache(
+            q, k, v, q_weight, k_weight, cos, sin, positions, slots, k_cache, v_cache,
+            k_descale=k_descale, v_descale=v_descale, eps=eps, interleaved=interleaved, q_out=q_out))
+    return _native().norm_rope_cache(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
+                                     v, slots, k_cache, v_cache, k_descale, v_descale, q_out)
 
 
-def _attention_sinks(q, k, v, scale, causal, window, sinks, options, stream, softcap, alibi_slopes):
-    """attention() with first keys that stay visible."""
+def _attention_sinks(q, k, v, scale, causal, window, sinks, options, softcap, alibi_slopes):
+    """attention() with first keys that stay visible, on the current stream."""
     left, right = (-1, -1) if window is None else window
     if scale is None:
         scale = q.shape[-1] ** -0.5
@@ -703,24 +725,16 @@ def _attention_sinks(q, k, v, scale, causal, window, sinks, options, stream, sof
         opts = default_options() if options is None else FwdOptions.from_buffer_copy(options)
         if softcap is not None:
             opts.softcap = float(softcap)
-        slopes = _slopes(alibi_slopes, q.shape[2], q.device, stream)
+        slopes = _slopes(alibi_slopes, q.shape[2], q.device, None)
         if slopes is not None:
             opts.alibi_slopes = slopes.data_ptr()
-    args = (q, k, v, scale, causal, left, right, sinks, None if opts is None else ctypes.addressof(opts))
-    if stream is None:
-        return _native().fwd_sinks(*args, None, None)
-    B, Sq, Hq, D = q.shape
-    size = sinks_workspace_size(B, Hq, k.shape[2], Sq, k.shape[1], D, causal, (left, right),
-                                min(sinks, k.shape[1]))
-    ws = torch.empty(max(size, 1), dtype=torch.uint8, device=q.device)
-    out = _native().fwd_sinks(*args, ws, _handle(stream))
-    _keep_for(stream, ws, *out)
-    return out
+    return _native().fwd_sinks(q, k, v, scale, causal, left, right, sinks,
+                               None if opts is None else ctypes.addressof(opts))
 
 
-def _attention_backward_sinks(q, k, v, o, lse, dout, scale, causal, window, sinks, stream, softcap,
+def _attention_backward_sinks(q, k, v, o, lse, dout, scale, causal, window, sinks, softcap,
                               alibi_slopes):
-    """attention_backward() with first keys that stay visible."""
+    """attention_backward() with first keys that stay visible, on the current stream."""
     left, right = (-1, -1) if window is None else window
     if scale is None:
         scale = q.shape[-1] ** -0.5
@@ -728,19 +742,10 @@ def _attention_backward_sinks(q, k, v, o, lse, dout, scale, causal, window, sink
     if softcap is not None or alibi_slopes is not None:
         opts = BwdOptions()
         opts.softcap = float(softcap or 0.0)
-        slopes = _slopes(alibi_slopes, q.shape[2], q.device, stream)
+        slopes = _slopes(alibi_slopes, q.shape[2], q.device, None)
         opts.alibi_slopes = None if slopes is None else slopes.data_ptr()
-    args = (q, k, v, scale, causal, left, right, sinks, o, lse, dout,
-            None if opts is None else ctypes.addressof(opts))
-    if stream is None:
-        return _native().bwd_sinks(*args, None, None)
-    B, Sq, Hq, D = q.shape
-    ws = torch.empty(bwd_workspace_size(B, Hq, k.shape[2], Sq, k.shape[1], D,
-                                        min(max(sinks, 0), k.shape[1])),
-                     dtype=torch.uint8, device=q.device)
-    out = _native().bwd_sinks(*args, ws, _handle(stream))
-    _keep_for(stream, ws, *out)
-    return out
+    return _native().bwd_sinks(q, k, v, scale, causal, left, right, sinks, o, lse, dout,
+                               None if opts is None else ctypes.addressof(opts))
 
 
 def decode_workspace_size(D) -> int:
@@ -760,25 +765,20 @@ def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, scale=None, windo
     = (left, right) as in attention(): the last left + 1 keys stay visible, and
     with `sinks` the first ones too.  o, lse and workspace (uint8, at least
     decode_workspace_size(D)) are allocated unless given."""
+    if stream is not None:
+        return _on_stream(stream, q, lambda: decode_paged(
+            q, k_cache, v_cache, page_table, seq_lens, scale=scale, window=window, sinks=sinks,
+            softcap=softcap, alibi_slopes=alibi_slopes, k_descale=k_descale, v_descale=v_descale, o=o,
+            lse=lse, workspace=workspace))
     left, right = (-1, -1) if window is None else window
     if right < -1:
         raise ValueError("window bounds must be -1 or >= 0")
     if scale is None:
         scale = q.shape[-1] ** -0.5
     if alibi_slopes is not None:
-        alibi_slopes = _slopes(alibi_slopes, q.shape[-2], q.device, stream)
-    if stream is None:
-        return _native().decode(q, k_cache, v_cache, page_table, seq_lens, scale, left, sinks,
-                                softcap or 0.0, alibi_slopes, k_descale, v_descale, o, lse,
-                                workspace, None)
-    if workspace is None:
-        workspace = torch.empty(decode_workspace_size(q.shape[-1]), dtype=torch.uint8,
-                                device=q.device)
-    out = _native().decode(q, k_cache, v_cache, page_table, seq_lens, scale, left, sinks,
-                           softcap or 0.0, alibi_slopes, k_descale, v_descale, o, lse, workspace,
-                           _handle(stream))
-    _keep_for(stream, workspace, *out)
-    return out
+        alibi_slopes = _slopes(alibi_slopes, q.shape[-2], q.device, None)
+    return _native().decode(q, k_cache, v_cache, page_table, seq_lens, scale, left, sinks,
+                            softcap or 0.0, alibi_slopes, k_descale, v_descale, o, lse, workspace)
 
 
 def device_status(stream=None) -> int:

@@ -81,13 +81,8 @@ int integer(PyObject *o) {
     return (int)v;
 }
 
-// The stream argument as a handle: None is the device's current one.
-void *stream_of(PyObject *o, int device) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(device).stream();
-    void *s = PyLong_AsVoidPtr(o);
-    if (!s && PyErr_Occurred()) throw PythonError{};
-    return s;
-}
+// Calls run on the device's current stream, whose pool the outputs come from.
+void *current_stream(int device) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream(); }
 
 void check(int status, const char *name) {
     if (status == ATTN_OK) return;
@@ -177,7 +172,7 @@ struct Norm {
 
 PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
 
-// (q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out, k_out, stream)
+// (q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out, k_out)
 PyObject *norm_rope(PyObject *const *a) {
     const Norm n(a);
     Device dev;
@@ -190,7 +185,7 @@ PyObject *norm_rope(PyObject *const *a) {
                       token_stride(n.q, "q"), token_stride(n.k, "k"), token_stride(q_out, "q_out"),
                       token_stride(k_out, "k_out"), n.qw.data_ptr(), n.kw.data_ptr(), n.w_fp32(),
                       n.cos_ptr(), n.sin_ptr(), n.pos_ptr(), n.tokens, n.Hq, n.Hkv, n.D, n.rot(),
-                      n.max_positions(), n.eps, n.interleaved, stream_of(a[11], dev.index())),
+                      n.max_positions(), n.eps, n.interleaved, current_stream(dev.index())),
           "attn_qk_norm_rope");
     return Py_BuildValue("(NN)", wrap(q_out), wrap(k_out));
 }
@@ -207,7 +202,7 @@ int cache_type(const at::Tensor &k, const at::Tensor &v) {
 }
 
 // (q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, v, slots, k_cache, v_cache,
-//  k_descale, v_descale, q_out, stream)
+//  k_descale, v_descale, q_out)
 PyObject *norm_rope_cache(PyObject *const *a) {
     const Norm n(a);
     const at::Tensor &v = tensor(a[9], "v"), &slots = tensor(a[10], "slots");
@@ -233,20 +228,16 @@ PyObject *norm_rope_cache(PyObject *const *a) {
                             n.cos_ptr(), n.sin_ptr(), n.pos_ptr(), static_cast<const int *>(slots.data_ptr()),
                             kc.data_ptr(), vc.data_ptr(), kv, kd, vd, kc.size(0) * kc.size(1), n.tokens, n.Hq,
                             n.Hkv, n.D, n.rot(), n.max_positions(), n.eps, n.interleaved,
-                            stream_of(a[16], dev.index())),
+                            current_stream(dev.index())),
           "attn_qk_norm_rope_cache");
     return wrap(q_out);
 }
 
-at::Tensor workspace(PyObject *o, size_t bytes, const at::Tensor &like) {
-    if (o == Py_None) return at::empty({(int64_t)bytes}, like.options().dtype(at::kByte));
-    const at::Tensor &t = tensor(o, "workspace");
-    require(t.scalar_type() == at::kByte && t.is_contiguous(), "workspace", "a contiguous uint8 tensor");
-    return t;
+at::Tensor workspace(size_t bytes, const at::Tensor &like) {
+    return at::empty({(int64_t)bytes}, like.options().dtype(at::kByte));
 }
 
-// (q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, dq, dk, dq_in, dk_in, workspace,
-//  stream)
+// (q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, dq, dk, dq_in, dk_in)
 PyObject *norm_rope_backward(PyObject *const *a) {
     const Norm n(a);
     const at::Tensor &dq = tensor(a[9], "dq"), &dk = tensor(a[10], "dk");
@@ -263,8 +254,7 @@ PyObject *norm_rope_backward(PyObject *const *a) {
     dev.add(dk_in, "dk_in");
     const at::Tensor dqw = at::empty_like(n.qw, n.qw.options().dtype(kF32));
     const at::Tensor dkw = at::empty_like(n.kw, n.kw.options().dtype(kF32));
-    const at::Tensor ws = workspace(a[13], g_norm_rope_bwd_workspace(n.D), n.q);
-    dev.add(ws, "workspace");
+    const at::Tensor ws = workspace(g_norm_rope_bwd_workspace(n.D), n.q);
     check(g_norm_rope_bwd(dq.data_ptr(), dk.data_ptr(), dq.scalar_type() == kF32, dk.scalar_type() == kF32,
                           n.q.data_ptr(), n.k.data_ptr(), dq_in.data_ptr(), dk_in.data_ptr(),
                           static_cast<float *>(dqw.data_ptr()), static_cast<float *>(dkw.data_ptr()),
@@ -272,13 +262,13 @@ PyObject *norm_rope_backward(PyObject *const *a) {
                           token_stride(n.k, "k"), token_stride(dq_in, "dq_in"), token_stride(dk_in, "dk_in"),
                           n.qw.data_ptr(), n.kw.data_ptr(), n.w_fp32(), n.cos_ptr(), n.sin_ptr(), n.pos_ptr(),
                           n.tokens, n.Hq, n.Hkv, n.D, n.rot(), n.max_positions(), n.eps, n.interleaved,
-                          ws.data_ptr(), (size_t)ws.numel(), stream_of(a[14], dev.index())),
+                          ws.data_ptr(), (size_t)ws.numel(), current_stream(dev.index())),
           "attn_qk_norm_rope_bwd");
     return Py_BuildValue("(NNNN)", wrap(dq_in), wrap(dk_in), wrap(dqw), wrap(dkw));
 }
 
 // (q, k_cache, v_cache, page_table, seq_lens, scale, window_left, sinks, softcap, alibi_slopes,
-//  k_descale, v_descale, o, lse, workspace, stream)
+//  k_descale, v_descale, o, lse, workspace)
 PyObject *decode(PyObject *const *a) {
     const at::Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache");
     const at::Tensor &table = tensor(a[3], "page_table"), &lens = tensor(a[4], "seq_lens");
@@ -315,7 +305,9 @@ PyObject *decode(PyObject *const *a) {
     require(lse.scalar_type() == kF32 && lse.dim() == 2 && lse.size(0) == B && lse.size(1) == Hq &&
                 lse.is_contiguous(),
             "lse", "a contiguous fp32 tensor [B, Hq]");
-    const at::Tensor ws = workspace(a[14], g_decode_workspace((int)D), q);
+    const at::Tensor ws =
+        a[14] == Py_None ? workspace(g_decode_workspace((int)D), q) : tensor(a[14], "workspace");
+    require(ws.scalar_type() == at::kByte && ws.is_contiguous(), "workspace", "a contiguous uint8 tensor");
     dev.add(o, "o");
     dev.add(lse, "lse");
     dev.add(ws, "workspace");
@@ -324,7 +316,7 @@ PyObject *decode(PyObject *const *a) {
                    o.data_ptr(), static_cast<float *>(lse.data_ptr()), (int)B, (int)Hq, (int)kc.size(2), (int)D,
                    (int)kc.size(0), (int)kc.size(1), (int)table.size(1), number(a[5]), integer(a[6]),
                    integer(a[7]), number(a[8]), slopes, ws.data_ptr(), (size_t)ws.numel(),
-                   stream_of(a[15], dev.index())),
+                   current_stream(dev.index())),
           "attn_decode_paged");
     return Py_BuildValue("(NN)", wrap(o), wrap(lse));
 }
@@ -374,7 +366,7 @@ const T *options(PyObject *o) {
     return static_cast<const T *>(p);
 }
 
-// (q, k, v, scale, causal, window_left, window_right, sinks, options, workspace, stream)
+// (q, k, v, scale, causal, window_left, window_right, sinks, options)
 PyObject *fwd_sinks(PyObject *const *a) {
     const Masked m(a);
     Device dev;
@@ -384,19 +376,16 @@ PyObject *fwd_sinks(PyObject *const *a) {
     const at::Tensor lse = at::empty({m.B, m.Hq, m.Sq}, m.q.options().dtype(kF32));
     const size_t size = g_fwd_sinks_workspace(m.B, m.Hq, m.Hkv, m.Sq, m.Sk, m.D, m.causal, m.left, m.right, m.sinks);
     at::Tensor ws;
-    if (size) {
-        ws = workspace(a[9], size, m.q);
-        dev.add(ws, "workspace");
-    }
+    if (size) ws = workspace(size, m.q);
     check(g_fwd_sinks(m.q.data_ptr(), m.k.data_ptr(), m.v.data_ptr(), o.data_ptr(),
                       static_cast<float *>(lse.data_ptr()), m.B, m.Hq, m.Hkv, m.Sq, m.Sk, m.D, m.scale, m.causal,
                       m.left, m.right, m.sinks, size ? ws.data_ptr() : nullptr, size ? (size_t)ws.numel() : 0,
-                      options<attn_fwd_options_t>(a[8]), stream_of(a[10], dev.index())),
+                      options<attn_fwd_options_t>(a[8]), current_stream(dev.index())),
           "attn_fwd_sinks");
     return Py_BuildValue("(NN)", wrap(o), wrap(lse));
 }
 
-// (q, k, v, scale, causal, window_left, window_right, sinks, o, lse, dout, options, workspace, stream)
+// (q, k, v, scale, causal, window_left, window_right, sinks, o, lse, dout, options)
 PyObject *bwd_sinks(PyObject *const *a) {
     const Masked m(a);
     const at::Tensor &o = tensor(a[8], "o"), &lse = tensor(a[9], "lse"), &dout = tensor(a[10], "dout");
@@ -416,13 +405,12 @@ PyObject *bwd_sinks(PyObject *const *a) {
     const at::Tensor dq = at::empty_like(m.q, m.q.options().dtype(kF32));
     const at::Tensor dk = at::empty_like(m.k), dv = at::empty_like(m.v);
     const at::Tensor ws =
-        workspace(a[12], g_bwd_sinks_workspace(m.B, m.Hq, m.Hkv, m.Sq, m.Sk, m.D, std::max(m.sinks, 0)), m.q);
-    dev.add(ws, "workspace");
+        workspace(g_bwd_sinks_workspace(m.B, m.Hq, m.Hkv, m.Sq, m.Sk, m.D, std::max(m.sinks, 0)), m.q);
     check(g_bwd_sinks(m.q.data_ptr(), m.k.data_ptr(), m.v.data_ptr(), o.data_ptr(),
                       static_cast<const float *>(lse.data_ptr()), dout.data_ptr(),
                       static_cast<float *>(dq.data_ptr()), dk.data_ptr(), dv.data_ptr(), m.B, m.Hq, m.Hkv, m.Sq,
                       m.Sk, m.D, m.scale, m.causal, m.left, m.right, m.sinks, ws.data_ptr(), (size_t)ws.numel(),
-                      options<attn_bwd_options_t>(a[11]), stream_of(a[13], dev.index())),
+                      options<attn_bwd_options_t>(a[11]), current_stream(dev.index())),
           "attn_bwd_sinks");
     return Py_BuildValue("(NNN)", wrap(dq), wrap(dk), wrap(dv));
 }
@@ -473,12 +461,12 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr
 PyMethodDef g_methods[] = {
     {"bind", FAST((&entry<bind, 11, false>))},
-    {"norm_rope", FAST((&entry<norm_rope, 12>))},
-    {"norm_rope_cache", FAST((&entry<norm_rope_cache, 17>))},
-    {"norm_rope_backward", FAST((&entry<norm_rope_backward, 15>))},
-    {"decode", FAST((&entry<decode, 16>))},
-    {"fwd_sinks", FAST((&entry<fwd_sinks, 11>))},
-    {"bwd_sinks", FAST((&entry<bwd_sinks, 14>))},
+    {"norm_rope", FAST((&entry<norm_rope, 11>))},
+    {"norm_rope_cache", FAST((&entry<norm_rope_cache, 16>))},
+    {"norm_rope_backward", FAST((&entry<norm_rope_backward, 13>))},
+    {"decode", FAST((&entry<decode, 15>))},
+    {"fwd_sinks", FAST((&entry<fwd_sinks, 9>))},
+    {"bwd_sinks", FAST((&entry<bwd_sinks, 12>))},
     {nullptr, nullptr, 0, nullptr},
 };
 
