@@ -69,6 +69,31 @@ def test_slopes_from_the_host_on_a_side_stream(handle):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("handle", HANDLES, ids=["stream", "handle"])
+def test_slopes_from_the_host_do_not_wait_for_the_stream(handle):
+    """The call returns while its stream has work of its own to do, and what
+    holds the slopes is not given away till then."""
+    t = on_device(make_tensors(1, 4, 2, 200, 200, 64, 1))
+    x = decode_arguments(torch.Generator().manual_seed(2), Hq=4)
+    kw = dict(alibi_slopes=[0.5, 0.25, 0.125, 0.0625])
+
+    def both(**more):
+        return attn.attention(t["q"], t["k"], t["v"], causal=True, window=(60, 0), sinks=3, **kw, **more) + \
+            attn.decode_paged(*x, **kw, **more)
+
+    want = both()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        sleep()
+    got = both(stream=handle(side))
+    assert not side.query()
+    small = [torch.zeros(4, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    check(got, want)
+    check_value(small, 0)
+
+
 def calls():
     """Every call that allocates: its name and a function of the stream."""
     t = on_device(make_tensors(1, 4, 2, 300, 300, 128, 3, with_dout=True))

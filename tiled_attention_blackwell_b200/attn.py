@@ -12,7 +12,6 @@ it has read them, and lets the stream that reads the results wait for it.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -217,13 +216,14 @@ def _torch_stream(stream, device):
     return torch.cuda.ExternalStream(handle, device=device)
 
 
-def _current(stream, device):
-    """A context in which torch allocates for a stream argument: memory that
-    belongs to another stream may still be in use there, and may be given
-    away there, while `stream` uses it."""
-    if stream is None or device.type != "cuda":
-        return contextlib.nullcontext()
-    return torch.cuda.stream(_torch_stream(stream, device))
+def _bring(t, device, stream):
+    """A host tensor on the device, valid until `stream` has read it.  The copy
+    is the caller's stream's, and complete on return: in `stream` it would make
+    the host wait for all that `stream` has still to do."""
+    t = t.to(device)
+    if stream is not None and device.type == "cuda":
+        t.record_stream(_torch_stream(stream, device))
+    return t
 
 
 def _on_stream(stream, q, call):
@@ -251,8 +251,7 @@ def _slopes(alibi_slopes, Hq, device, stream):
     if alibi_slopes is None:
         return None
     if not torch.is_tensor(alibi_slopes) or not alibi_slopes.is_cuda:
-        with _current(stream, device):
-            alibi_slopes = torch.as_tensor(alibi_slopes, dtype=torch.float32).to(device)
+        alibi_slopes = _bring(torch.as_tensor(alibi_slopes, dtype=torch.float32), device, stream)
     if alibi_slopes.dtype != torch.float32 or not alibi_slopes.is_contiguous() \
             or alibi_slopes.numel() != Hq:
         raise TypeError("alibi_slopes must be a contiguous fp32 tensor of Hq entries")
@@ -334,6 +333,8 @@ def attention(q, k, v, *, scale=None, causal=False, window=None, doc_offsets=Non
     """Allocate O and LSE with torch and run the forward.  Returns (O, LSE)."""
     if sinks:
         _check_sinks(sinks, doc_offsets)
+        if alibi_slopes is not None:
+            alibi_slopes = _slopes(alibi_slopes, q.shape[2], q.device, stream)
         args = (q, k, v, scale, causal, window, sinks, options, softcap, alibi_slopes)
         if stream is not None:
             return _on_stream(stream, q, lambda: _attention_sinks(*args))
@@ -566,6 +567,8 @@ def attention_backward(q, k, v, o, lse, dout, *, scale=None, causal=False, windo
     the backward.  Returns (dQ, dK, dV)."""
     if sinks:
         _check_sinks(sinks, doc_offsets)
+        if alibi_slopes is not None:
+            alibi_slopes = _slopes(alibi_slopes, q.shape[2], q.device, stream)
         args = (q, k, v, o, lse, dout, scale, causal, window, sinks, softcap, alibi_slopes)
         if stream is not None:
             return _on_stream(stream, q, lambda: _attention_backward_sinks(*args))
@@ -715,34 +718,31 @@ def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos, sin, positions, slots, 
                                      v, slots, k_cache, v_cache, k_descale, v_descale, q_out)
 
 
-def _attention_sinks(q, k, v, scale, causal, window, sinks, options, softcap, alibi_slopes):
+def _attention_sinks(q, k, v, scale, causal, window, sinks, options, softcap, slopes):
     """attention() with first keys that stay visible, on the current stream."""
     left, right = (-1, -1) if window is None else window
     if scale is None:
         scale = q.shape[-1] ** -0.5
     opts = None
-    if options is not None or softcap is not None or alibi_slopes is not None:
+    if options is not None or softcap is not None or slopes is not None:
         opts = default_options() if options is None else FwdOptions.from_buffer_copy(options)
         if softcap is not None:
             opts.softcap = float(softcap)
-        slopes = _slopes(alibi_slopes, q.shape[2], q.device, None)
         if slopes is not None:
             opts.alibi_slopes = slopes.data_ptr()
     return _native().fwd_sinks(q, k, v, scale, causal, left, right, sinks,
                                None if opts is None else ctypes.addressof(opts))
 
 
-def _attention_backward_sinks(q, k, v, o, lse, dout, scale, causal, window, sinks, softcap,
-                              alibi_slopes):
+def _attention_backward_sinks(q, k, v, o, lse, dout, scale, causal, window, sinks, softcap, slopes):
     """attention_backward() with first keys that stay visible, on the current stream."""
     left, right = (-1, -1) if window is None else window
     if scale is None:
         scale = q.shape[-1] ** -0.5
     opts = None
-    if softcap is not None or alibi_slopes is not None:
+    if softcap is not None or slopes is not None:
         opts = BwdOptions()
         opts.softcap = float(softcap or 0.0)
-        slopes = _slopes(alibi_slopes, q.shape[2], q.device, None)
         opts.alibi_slopes = None if slopes is None else slopes.data_ptr()
     return _native().bwd_sinks(q, k, v, scale, causal, left, right, sinks, o, lse, dout,
                                None if opts is None else ctypes.addressof(opts))
@@ -765,6 +765,8 @@ def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, scale=None, windo
     = (left, right) as in attention(): the last left + 1 keys stay visible, and
     with `sinks` the first ones too.  o, lse and workspace (uint8, at least
     decode_workspace_size(D)) are allocated unless given."""
+    if alibi_slopes is not None:
+        alibi_slopes = _slopes(alibi_slopes, q.shape[-2], q.device, stream)
     if stream is not None:
         return _on_stream(stream, q, lambda: decode_paged(
             q, k_cache, v_cache, page_table, seq_lens, scale=scale, window=window, sinks=sinks,
@@ -775,8 +777,6 @@ def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, scale=None, windo
         raise ValueError("window bounds must be -1 or >= 0")
     if scale is None:
         scale = q.shape[-1] ** -0.5
-    if alibi_slopes is not None:
-        alibi_slopes = _slopes(alibi_slopes, q.shape[-2], q.device, None)
     return _native().decode(q, k_cache, v_cache, page_table, seq_lens, scale, left, sinks,
                             softcap or 0.0, alibi_slopes, k_descale, v_descale, o, lse, workspace)
 
