@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from tiled_attention_blackwell_b200 import attn, build
-from tiled_attention_blackwell_b200.workloads import make_tensors
+from tiled_attention_blackwell_b200.workloads import make_tensors, make_tensors_fp4, make_tensors_fp8
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -98,8 +98,11 @@ def calls():
     """Every call that allocates: its name and a function of the stream."""
     t = on_device(make_tensors(1, 4, 2, 300, 300, 128, 3, with_dout=True))
     q, k, v, dout = (t[n] for n in ("q", "k", "v", "dout"))
+    plain, docs = dict(causal=True), dict(causal=True, doc_offsets=[0, 70, 201, 300])
     window = dict(causal=True, window=(140, 0), sinks=4)
-    saved = {"window": attn.attention(q, k, v, **window)}
+    saved = {n: attn.attention(q, k, v, **kw) for n, kw in (("docs", docs), ("window", window))}
+    f8, f4 = on_device(make_tensors_fp8(1, 4, 2, 300, 300, 128, 4)), on_device(make_tensors_fp4(1, 4, 2, 300, 300, 128, 5))
+    names = [f"{x}_{y}" for x in "qkv" for y in ("codes", "scales", "global")]
     long = on_device(make_tensors(1, 4, 2, 200, 1500, 128, 6))
     g = torch.Generator().manual_seed(7)
     qkv = torch.randn(60, 12 * 128, generator=g).to(torch.bfloat16).to(DEV)
@@ -111,6 +114,12 @@ def calls():
     caches = [torch.zeros(4, 16, 2, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
     token = decode_arguments(g)
     return {
+        "attention": lambda s: attn.attention(q, k, v, stream=s, **plain),
+        "attention docs": lambda s: attn.attention(q, k, v, stream=s, **docs),
+        "attention_backward docs": lambda s: attn.attention_backward(q, k, v, *saved["docs"], dout, stream=s, **docs),
+        "attention_fp8": lambda s: attn.attention_fp8(*(f8[n] for n in "qkv"), stream=s, **docs,
+                                                      **{n: f8[n] for n in ("q_descale", "k_descale", "v_descale")}),
+        "attention_fp4": lambda s: attn.attention_fp4(*(f4[n] for n in names), stream=s, **docs),
         "window": lambda s: attn.attention(q, k, v, stream=s, **window),
         "window in parts": lambda s: attn.attention(long["q"], long["k"], long["v"], stream=s, causal=True,
                                                     window=(900, 0), sinks=4),
@@ -123,8 +132,10 @@ def calls():
     }
 
 
-NAMES = ["window", "window in parts", "window backward", "qk_norm_rope", "qk_norm_rope_backward",
-         "qk_norm_rope_cache", "decode_paged"]
+NAMES = ["attention", "attention docs", "attention_backward docs", "attention_fp8", "attention_fp4", "window",
+         "window in parts", "window backward", "qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_cache",
+         "decode_paged"]
+FROM_HOST = ("attention docs", "attention_backward docs", "attention_fp8", "attention_fp4")  # document offsets as a list
 
 
 @pytest.fixture(scope="module")
@@ -183,6 +194,7 @@ def test_memory_of_a_call_stays_its_own_until_it_has_run(every, name):
     with torch.cuda.stream(side):
         sleep()
     call(side)  # dropped
+    assert not side.query()  # nor has it waited for the stream
     mine = [torch.full_like(x, 7) for x in want for _ in range(3)]
     kept = call(side)
     small = [torch.zeros(4, dtype=torch.int32, device=DEV) for _ in range(3)]
@@ -213,7 +225,7 @@ def test_results_in_use_on_the_current_stream_are_not_taken_by_the_next_call(eve
     check_value(mine, 7)
 
 
-@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("name", [n for n in NAMES if n not in FROM_HOST])
 def test_captured_on_a_stream_beside_the_capturing_one(every, name):
     call = every[name]
     want = call(None)

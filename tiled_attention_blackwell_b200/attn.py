@@ -258,6 +258,15 @@ def _slopes(alibi_slopes, Hq, device, stream):
     return alibi_slopes
 
 
+def _device_docs(doc_offsets, device, stream):
+    """Document offsets on the device, as _slopes has its slopes there."""
+    if doc_offsets is None:
+        return None
+    if not torch.is_tensor(doc_offsets):
+        doc_offsets = torch.as_tensor(doc_offsets, dtype=torch.int32)
+    return doc_offsets if doc_offsets.is_cuda else _bring(doc_offsets, device, stream)
+
+
 def _check_sinks(sinks, doc_offsets):
     if sinks and doc_offsets is not None:
         raise AttnError(ATTN_ERR_UNSUPPORTED, "sinks: not built beside a document mask")
@@ -331,26 +340,23 @@ def sinks_workspace_size(B, Hq, Hkv, Sq, Sk, D, causal, window, sinks) -> int:
 def attention(q, k, v, *, scale=None, causal=False, window=None, doc_offsets=None,
               options=None, stream=None, softcap=None, alibi_slopes=None, sinks=0):
     """Allocate O and LSE with torch and run the forward.  Returns (O, LSE)."""
+    _check_sinks(sinks, doc_offsets)
+    if alibi_slopes is not None:
+        alibi_slopes = _slopes(alibi_slopes, q.shape[2], q.device, stream)
+    doc_offsets = _device_docs(doc_offsets, q.device, stream)
+    if stream is not None:
+        return _on_stream(stream, q, lambda: attention(
+            q, k, v, scale=scale, causal=causal, window=window, doc_offsets=doc_offsets,
+            options=options, softcap=softcap, alibi_slopes=alibi_slopes, sinks=sinks))
     if sinks:
-        _check_sinks(sinks, doc_offsets)
-        if alibi_slopes is not None:
-            alibi_slopes = _slopes(alibi_slopes, q.shape[2], q.device, stream)
-        args = (q, k, v, scale, causal, window, sinks, options, softcap, alibi_slopes)
-        if stream is not None:
-            return _on_stream(stream, q, lambda: _attention_sinks(*args))
-        return _attention_sinks(*args)
+        return _attention_sinks(q, k, v, scale, causal, window, sinks, options, softcap, alibi_slopes)
     B, Sq, Hq, D = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     o = torch.empty_like(q)
     lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
-    if doc_offsets is not None and not torch.is_tensor(doc_offsets):
-        doc_offsets = torch.as_tensor(doc_offsets, dtype=torch.int32)
-    if doc_offsets is not None and not doc_offsets.is_cuda:
-        doc_offsets = doc_offsets.to(q.device)
     attn_fwd(q, k, v, o, lse, scale=scale, causal=causal, window=window,
-             doc_offsets=doc_offsets, options=options, stream=stream, softcap=softcap,
-             alibi_slopes=alibi_slopes)
+             doc_offsets=doc_offsets, options=options, softcap=softcap, alibi_slopes=alibi_slopes)
     return o, lse
 
 
@@ -386,18 +392,19 @@ def attn_fwd_fp8(q, k, v, o, lse, *, q_descale, k_descale, v_descale, scale, cau
 def attention_fp8(q, k, v, *, q_descale, k_descale, v_descale, scale=None, causal=False,
                   window=None, doc_offsets=None, options=None, stream=None):
     """Allocate O (bf16) and LSE with torch and run the fp8 forward."""
+    doc_offsets = _device_docs(doc_offsets, q.device, stream)
+    if stream is not None:
+        return _on_stream(stream, q, lambda: attention_fp8(
+            q, k, v, q_descale=q_descale, k_descale=k_descale, v_descale=v_descale, scale=scale,
+            causal=causal, window=window, doc_offsets=doc_offsets, options=options))
     B, Sq, Hq, D = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     o = torch.empty((B, Sq, Hq, D), dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
-    if doc_offsets is not None and not torch.is_tensor(doc_offsets):
-        doc_offsets = torch.as_tensor(doc_offsets, dtype=torch.int32)
-    if doc_offsets is not None and not doc_offsets.is_cuda:
-        doc_offsets = doc_offsets.to(q.device)
     attn_fwd_fp8(q, k, v, o, lse, q_descale=q_descale, k_descale=k_descale,
                  v_descale=v_descale, scale=scale, causal=causal, window=window,
-                 doc_offsets=doc_offsets, options=options, stream=stream)
+                 doc_offsets=doc_offsets, options=options)
     return o, lse
 
 
@@ -467,6 +474,12 @@ def attention_fp4(q_codes, q_scales, q_global, k_codes, k_scales, k_global, v_co
                   classifier="affine", mma=None, options=None, stream=None, workspace=None):
     """Allocate O, LSE (and the workspace unless given) with torch and run the
     FP4 Direct-P forward.  Returns (O, LSE)."""
+    doc_offsets = _device_docs(doc_offsets, q_codes.device, stream)
+    if stream is not None:
+        return _on_stream(stream, q_codes, lambda: attention_fp4(
+            q_codes, q_scales, q_global, k_codes, k_scales, k_global, v_codes, v_scales, v_global,
+            scale=scale, causal=causal, window=window, doc_offsets=doc_offsets,
+            classifier=classifier, mma=mma, options=options, workspace=workspace))
     B, Sq, Hq, Dh = q_codes.shape
     _, Sk, Hkv, _ = k_codes.shape
     D = 2 * Dh
@@ -478,14 +491,9 @@ def attention_fp4(q_codes, q_scales, q_global, k_codes, k_scales, k_global, v_co
     if workspace is None:
         workspace = torch.empty(fp4_workspace_size(B, Hq, Hkv, Sq, Sk, D), dtype=torch.uint8,
                                 device=dev)
-    if doc_offsets is not None and not torch.is_tensor(doc_offsets):
-        doc_offsets = torch.as_tensor(doc_offsets, dtype=torch.int32)
-    if doc_offsets is not None and not doc_offsets.is_cuda:
-        doc_offsets = doc_offsets.to(dev)
     attn_fwd_fp4(q_codes, q_scales, q_global, k_codes, k_scales, k_global, v_codes, v_scales,
                  v_global, o, lse, workspace, scale=scale, causal=causal, window=window,
-                 doc_offsets=doc_offsets, classifier=classifier, mma=mma, options=options,
-                 stream=stream)
+                 doc_offsets=doc_offsets, classifier=classifier, mma=mma, options=options)
     return o, lse
 
 
@@ -565,14 +573,17 @@ def attention_backward(q, k, v, o, lse, dout, *, scale=None, causal=False, windo
                        doc_offsets=None, stream=None, softcap=None, alibi_slopes=None, sinks=0):
     """Allocate dQ (fp32), dK, dV (bf16) and the workspace with torch and run
     the backward.  Returns (dQ, dK, dV)."""
+    _check_sinks(sinks, doc_offsets)
+    if alibi_slopes is not None:
+        alibi_slopes = _slopes(alibi_slopes, q.shape[2], q.device, stream)
+    doc_offsets = _device_docs(doc_offsets, q.device, stream)
+    if stream is not None:
+        return _on_stream(stream, q, lambda: attention_backward(
+            q, k, v, o, lse, dout, scale=scale, causal=causal, window=window,
+            doc_offsets=doc_offsets, softcap=softcap, alibi_slopes=alibi_slopes, sinks=sinks))
     if sinks:
-        _check_sinks(sinks, doc_offsets)
-        if alibi_slopes is not None:
-            alibi_slopes = _slopes(alibi_slopes, q.shape[2], q.device, stream)
-        args = (q, k, v, o, lse, dout, scale, causal, window, sinks, softcap, alibi_slopes)
-        if stream is not None:
-            return _on_stream(stream, q, lambda: _attention_backward_sinks(*args))
-        return _attention_backward_sinks(*args)
+        return _attention_backward_sinks(q, k, v, o, lse, dout, scale, causal, window, sinks,
+                                         softcap, alibi_slopes)
     B, Sq, Hq, D = q.shape
     _, Sk, Hkv, _ = k.shape
     if scale is None:
@@ -582,13 +593,8 @@ def attention_backward(q, k, v, o, lse, dout, *, scale=None, causal=False, windo
     dv = torch.empty_like(v)
     ws = torch.empty(bwd_workspace_size(B, Hq, Hkv, Sq, Sk, D), dtype=torch.uint8,
                      device=q.device)
-    if doc_offsets is not None and not torch.is_tensor(doc_offsets):
-        doc_offsets = torch.as_tensor(doc_offsets, dtype=torch.int32)
-    if doc_offsets is not None and not doc_offsets.is_cuda:
-        doc_offsets = doc_offsets.to(q.device)
     attn_bwd(q, k, v, o, lse, dout, dq, dk, dv, ws, scale=scale, causal=causal, window=window,
-             doc_offsets=doc_offsets, stream=stream, softcap=softcap, alibi_slopes=alibi_slopes)
-    _keep_for(stream, dq, dk, dv, ws)
+             doc_offsets=doc_offsets, softcap=softcap, alibi_slopes=alibi_slopes)
     return dq, dk, dv
 
 
@@ -646,17 +652,6 @@ def _native():
                                     for name in _BOUND_FUNCTIONS])
             _bound = L
     return _binding
-
-
-def _keep_for(stream, *tensors):
-    """Tells the allocator that work on `stream` (a stream or its handle) uses
-    tensors which were allocated on the current stream."""
-    if stream is None:
-        return
-    stream = _torch_stream(stream, tensors[0].device)
-    if stream.cuda_stream != torch.cuda.current_stream(tensors[0].device).cuda_stream:
-        for t in tensors:
-            t.record_stream(stream)
 
 
 def rope_table(max_positions, rot, *, theta=10000.0, device="cuda"):
