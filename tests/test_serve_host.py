@@ -304,6 +304,15 @@ def test_sinks_beside_documents_are_refused(L):
     assert e.value.status == attn.ATTN_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("sinks", [0, 2])
+def test_a_key_that_is_no_tensor_is_refused_by_name(L, sinks):
+    q, lse, dq = stand_in(1, 16, 2, 64), stand_in(1, 2, 16, dtype=F32), stand_in(1, 16, 2, 64, dtype=F32)
+    for k in (None, [1.0], 3):
+        with pytest.raises(TypeError, match="k must be"):
+            attn.attn_bwd(q, k, q, q, lse, q, dq, q, q, stand_in(1 << 20, dtype=torch.uint8), scale=0.1, window=(4, 0),
+                          sinks=sinks, stream=0)
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU path only")
 def test_valid_sinks_calls_without_gpu_report_cuda_error(L):
     for sinks in (0, 4, 1000):

@@ -542,8 +542,8 @@ def attn_bwd(q, k, v, o, lse, dout, dq, dk, dv, workspace, *, scale, causal=Fals
     bwd_workspace_size() bytes.  softcap / alibi_slopes / sinks must match the
     forward that produced o and lse."""
     _check_sinks(sinks, doc_offsets)
-    sinks = min(sinks, k.shape[1])
     _check_bwd_tensors(q, k, v, o, lse, dout, dq, dk, dv)
+    sinks = min(sinks, k.shape[1])
     if not torch.is_tensor(workspace) or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
     B, Sq, Hq, D = q.shape
