@@ -190,6 +190,35 @@ def test_rising_scores_and_one_dominating_key(dtype):
     check(t, run(t), scale=128 ** -0.5)
 
 
+@pytest.mark.parametrize("gap", [17.5, 21.0])
+@pytest.mark.parametrize("heads", [(8, 8, 128), (12, 3, 128), (8, 8, 64), (20, 1, 64)])
+def test_small_weights_beside_a_dominating_key_of_an_8_bit_cache(gap, heads):
+    """A first token `gap` nats above n others: all of the output is theirs (its
+    V is 0, theirs 1), at weights of 2^-25 and 2^-30 of the largest.  Enough
+    sequences, on the same pages, that blocks hold whole pairs.
+
+    f16 weights, 2^7 times the exact ones, are off by half of 2^-24 at most where
+    they are subnormal: 2^-32 of the largest weight each."""
+    Hq, Hkv, D = heads
+    n, page, B = 70000, 80, 600 // Hkv
+    pages = n // page
+    kc, vc = (torch.zeros(pages, page, Hkv, D, dtype=torch.float32) for _ in range(2))
+    kc[0, 0], vc[:] = 1.0, 1.0
+    vc[0, 0] = 0.0
+    kc, vc = (x.to(FP8).to(DEV) for x in (kc, vc))
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).repeat(B, 1)
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    q = torch.ones(B, Hq, D, dtype=torch.bfloat16, device=DEV)
+    o, lse = (x.double().cpu() for x in attn.decode_paged(q, kc, vc, table, lens, scale=gap / D))
+    total = 1 + (n - 1) * math.exp(-gap)
+    want = (n - 1) * math.exp(-gap) / total
+    e = D * 2.0 ** -23 * gap
+    bound = (2 * (2.0 ** -11 + e + 2.0 ** -18) + 2.0 ** -8) * want + 2.0 ** -32 * (n - 1)
+    assert (o - want).abs().max() <= bound, (float(o.min()), float(o.max()), want)
+    want = gap + math.log(total)
+    assert (lse - want).abs().max() <= e + 2.0 ** -18 + 2.0 ** -22 * want
+
+
 def test_tiny_and_huge_queries_against_an_8_bit_cache():
     for std in (1e-20, 1e-3, 300.0):
         t = problem([200, 31], 4, 2, 128, 16, FP8, seed=60, q_std=std)

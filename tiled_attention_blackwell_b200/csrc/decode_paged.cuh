@@ -61,9 +61,15 @@ static_assert(kDecComputeRegs + kDecCopyRegs <= 2 * kDecLaunchRegs, "register sp
 // A row's maximum moves only when a tile raises it by more than this (log2
 // units), as in the forward; P stays below 2^8.
 constexpr float kDecTau = 8.0f;
+// f16 weights (e4m3 caches) are 2^kDecBias times P, so at most 2^15, within f16:
+// its smallest step, 2^-24, is then 2^-31 of a weight of 1.  Without it many small
+// weights beside a first token 17 nats above them became zero in the products,
+// though not in the sum below.  Partial results scale alike; maxima are
+// handed on less the bias, so that only the weights know of it.
+constexpr float kDecBias = 7.0f;
 
 struct DecodeParams {
-    CUtensorMap tm_k, tm_v;  // [pages][page_size][Hkv][D], box 16 keys of one head
+    CUtensorMap tm_k, tm_v;  // [pages][page_size][Hkv][D], box 16 keys of kHeads heads
     const __nv_bfloat16 *q;  // [B][Hq][D]
     __nv_bfloat16 *o;        // [B][Hq][D]
     float *lse;              // [B][Hq]
@@ -152,8 +158,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 
 // Weights of two heads in the operand type.  bf16: with the sums of the rounded
 // values, which normalise the output, as in the forward (a row that one key
-// dominates gives that key's V).  f16 weights are off by 2^-12 at most, which
-// the output's own rounding hides: the plain sum normalises them.
+// dominates gives that key's V).  f16 weights are off by 2^-11 of themselves or by
+// 2^-32 of the largest (kDecBias): less than the output's own rounding, 2^-8 of the
+// largest V, for the 2^23 keys that n 2^-32 allows, so the plain sum normalises them.
 template <bool F8>
 __device__ __forceinline__ uint32_t pack_weights(float p0, float p1, float &sum0, float &sum1) {
     if constexpr (F8) {
@@ -636,7 +643,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
                         m[nb][i] = mx;
                         moved = true;
                     }
-                    neg_m[i] = m[nb][i] == -INFINITY ? 0.0f : -m[nb][i];
+                    neg_m[i] = m[nb][i] == -INFINITY ? 0.0f : (F8 ? kDecBias : 0.0f) - m[nb][i];
                 }
                 float sum[2] = {0.0f, 0.0f}, rounded[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -707,12 +714,14 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i) {
+                if (F8) m[nb][i] -= kDecBias;
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) {
                     l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], o);
                     lr[nb][i] += __shfl_xor_sync(0xffffffffu, lr[nb][i], o);
                 }
+            }
         const bool whole = t0 == 0 && t1 == st.n;
         if (whole && t1 == 1) {
             // A pair of one tile is its team's alone: the team writes the output, and
