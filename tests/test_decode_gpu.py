@@ -190,6 +190,25 @@ def test_rising_scores_and_one_dominating_key(dtype):
     check(t, run(t), scale=128 ** -0.5)
 
 
+@pytest.mark.parametrize("heads,n", [((8, 2), 1000), ((8, 8), 77), ((32, 2), 3000), ((6, 3), 20), ((40, 1), 300)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_of_a_bf16_cache_keep_their_bits(heads, n, D):
+    """Beside the output's own rounding (2^-8 of it) only fp32's: weights in two
+    bf16 words are off by 2^-17."""
+    t = problem([n, 2 * n], *heads, D, 16, torch.bfloat16, seed=n + D, q_std=0.3)
+    o, _ = (x.double().cpu() for x in run(t))
+    want, bound, _, _ = reference(t, scale=D ** -0.5)
+    # the bound holds 2 * 2^-8 sum p |v| for the weights: 2 * 2^-17 in its place
+    G = heads[0] // heads[1]
+    for b, m in enumerate((n, 2 * n)):
+        j = torch.arange(m)
+        k, v = (c[t["table"].long()[b][j // 16], j % 16].double() for c in (t["kc"], t["vc"]))
+        for h in range(heads[0]):
+            p = torch.softmax(k[:, h // G] @ t["q"][b, h].double() * D ** -0.5, 0)
+            bound[b, h] -= 2 * (2.0 ** -8 - 2.0 ** -17) * (p @ v[:, h // G].abs())
+    assert ((o - want).abs() <= bound).all(), float(((o - want).abs() / bound).max())
+
+
 @pytest.mark.parametrize("gap", [17.5, 21.0])
 @pytest.mark.parametrize("heads", [(8, 8, 128), (12, 3, 128), (8, 8, 64), (20, 1, 64)])
 def test_small_weights_beside_a_dominating_key_of_an_8_bit_cache(gap, heads):

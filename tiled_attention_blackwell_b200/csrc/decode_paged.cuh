@@ -79,7 +79,7 @@ struct DecodeParams {
     // Workspace: per block two partial results (a pair that begins before
     // the block, one that ends behind it) and one record.
     float *part_o;           // [blocks][2][kHeads][16][D], relative to the partial's maximum
-    float4 *part_ml;         // [blocks][2][kHeads][16]: maximum (log2), sum, sum of the rounded weights
+    float2 *part_ml;         // [blocks][2][kHeads][16]: maximum (log2), sum
     int4 *record;            // [blocks]: the pair that is first cut at this block's end
     int B, Hq, Hkv, group, hchunks;  // hchunks: parts of a key head's query heads
     int max_pages, page_size, num_pages;
@@ -156,18 +156,21 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     return d;
 }
 
-// Weights of two heads in the operand type.  bf16: with the sums of the rounded
-// values, which normalise the output, as in the forward (a row that one key
-// dominates gives that key's V).  f16 weights are off by 2^-11 of themselves or by
-// 2^-32 of the largest (kDecBias): less than the output's own rounding, 2^-8 of the
-// largest V, for the 2^23 keys that n 2^-32 allows, so the plain sum normalises them.
+// Weights of two heads in the operand type.  bf16: in two words, what the first
+// rounding leaves in `rest`, so that a weight is off by 2^-17, and their sum in
+// fp32 normalises them.  (One word, normalised by the sum of what it held, put
+// the output off by sqrt(2) of its own rounding; the time is the keys' bytes
+// either way: 64 ragged sequences of 32 / 8 heads of 128 172.2 us, 173.9 with one word,
+// 48 of 16 / 16 heads of 64 128.2 against 127.2.)  f16 weights are off by 2^-11 of themselves or by 2^-32 of the
+// largest (kDecBias): less than the output's own rounding, 2^-8 of the largest V,
+// for the 2^23 keys that n 2^-32 allows.
 template <bool F8>
-__device__ __forceinline__ uint32_t pack_weights(float p0, float p1, float &sum0, float &sum1) {
+__device__ __forceinline__ uint32_t pack_weights(float p0, float p1, uint32_t &rest) {
     if constexpr (F8) {
         return pack_f16x2(p0, p1);
     } else {
         const uint32_t h = pack_bf16x2(p0, p1);
-        add_bf16x2_f32(sum0, sum1, h);
+        rest = pack_bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u));
         return h;
     }
 }
@@ -186,7 +189,7 @@ struct DecodeSmem {
     uint8_t v[kStages][kBlocks][kBoxBytes];
     static constexpr int kRows = 8 * NB;
     float o[kDecWarps][kRows][D + 4];  // + 4: rows start in different banks
-    float4 ml[kDecWarps][kRows];
+    float2 ml[kDecWarps][kRows];
     uint64_t full[kStages], empty[kStages];
     long long start, end, share, base;    // this block's run; tiles before sequence b0
     int b0;
@@ -518,11 +521,11 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[j][nb][e] = 0.0f;
-        float m[NB][2], l[NB][2], lr[NB][2];
+        float m[NB][2], l[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) m[nb][i] = -INFINITY, l[nb][i] = lr[nb][i] = 0.0f;
+            for (int i = 0; i < 2; ++i) m[nb][i] = -INFINITY, l[nb][i] = 0.0f;
 
         // This team's tiles of the pair.
         const uint32_t g0 = seg.g0;
@@ -622,7 +625,8 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
                         }
                     }
             }
-            uint32_t pt[kBlocks][NB][2];  // P^T as the B operand
+            // P^T as the B operand; bf16: and what its rounding leaves.
+            uint32_t pt[kBlocks][NB][2], rest[kBlocks][NB][2];
             float alpha[NB][2];
             bool moved = false;
 #pragma unroll
@@ -645,7 +649,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
                     }
                     neg_m[i] = m[nb][i] == -INFINITY ? 0.0f : (F8 ? kDecBias : 0.0f) - m[nb][i];
                 }
-                float sum[2] = {0.0f, 0.0f}, rounded[2] = {0.0f, 0.0f};
+                float sum[2] = {0.0f, 0.0f};
 #pragma unroll
                 for (int u = 0; u < kBlocks; ++u)
 #pragma unroll
@@ -654,13 +658,12 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
                         const float e1 = ex2_mufu(fmaf(x[u][nb][2 * h + 1], c[1], neg_m[1]));
                         sum[0] += e0;
                         sum[1] += e1;
-                        pt[u][nb][h] = transpose8x8(pack_weights<F8>(e0, e1, rounded[0], rounded[1]));
+                        uint32_t left = 0u;
+                        pt[u][nb][h] = transpose8x8(pack_weights<F8>(e0, e1, left));
+                        if (!F8) rest[u][nb][h] = transpose8x8(left);
                     }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    l[nb][i] = fmaf(l[nb][i], alpha[nb][i], sum[i]);
-                    lr[nb][i] = fmaf(lr[nb][i], alpha[nb][i], rounded[i]);
-                }
+                for (int i = 0; i < 2; ++i) l[nb][i] = fmaf(l[nb][i], alpha[nb][i], sum[i]);
             }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -702,6 +705,9 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
                             mma16816<false>(acc[j / 2][nb], a, pt[u][nb][0], pt[u][nb][1]);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+                            mma16816<false>(acc[j / 2][nb], a, rest[u][nb][0], rest[u][nb][1]);
                     }
                 }
             }
@@ -717,10 +723,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
             for (int i = 0; i < 2; ++i) {
                 if (F8) m[nb][i] -= kDecBias;
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], o);
-                    lr[nb][i] += __shfl_xor_sync(0xffffffffu, lr[nb][i], o);
-                }
+                for (int o = 4; o < 32; o <<= 1) l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], o);
             }
         const bool whole = t0 == 0 && t1 == st.n;
         if (whole && t1 == 1) {
@@ -734,8 +737,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
                         const int r = 8 * nb + 2 * fc + i;
                         if (r >= rows) continue;
                         const size_t row = (size_t)seg.b * p.Hq + hq + r;
-                        const float sum = F8 ? l[nb][i] : lr[nb][i];
-                        const float inv = sum == 0.0f ? 0.0f : p.v_descale / sum;
+                        const float inv = l[nb][i] == 0.0f ? 0.0f : p.v_descale / l[nb][i];
                         __nv_bfloat16 *o = p.o + row * D;
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j) {
@@ -766,7 +768,7 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
                 const int r = 8 * nb + 2 * fc + i;
                 if (r >= rows) continue;
                 if (fr == 0)
-                    sm.ml[warp][r] = make_float4(m[nb][i], l[nb][i], F8 ? l[nb][i] : lr[nb][i], 0.0f);
+                    sm.ml[warp][r] = make_float2(m[nb][i], l[nb][i]);
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
                     if constexpr (F8) {
@@ -786,15 +788,14 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
             float mx = sm.ml[k][r].x;
 #pragma unroll
             for (int w = 1; w < kTeams; ++w) mx = fmaxf(mx, sm.ml[k + w * kHeads][r].x);
-            float ls = 0.0f, lrs = 0.0f;
+            float ls = 0.0f;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int w = 0; w < kTeams; ++w) {
-                const float4 ml = sm.ml[k + w * kHeads][r];
+                const float2 ml = sm.ml[k + w * kHeads][r];
                 const float f = ml.x == -INFINITY ? 0.0f : ex2_mufu(ml.x - mx);
                 const float4 ow = *reinterpret_cast<const float4 *>(&sm.o[k + w * kHeads][r][d]);
                 ls = fmaf(ml.y, f, ls);
-                lrs = fmaf(ml.z, f, lrs);
                 o.x = fmaf(ow.x, f, o.x);
                 o.y = fmaf(ow.y, f, o.y);
                 o.z = fmaf(ow.z, f, o.z);
@@ -802,14 +803,14 @@ decode_paged_kernel(const __grid_constant__ DecodeParams p) {
             }
             if (whole) {
                 const size_t row = (size_t)seg.b * p.Hq + seg.hq0 + k * p.group + r;
-                const float inv = lrs == 0.0f ? 0.0f : p.v_descale / lrs;
+                const float inv = ls == 0.0f ? 0.0f : p.v_descale / ls;
                 *reinterpret_cast<uint2 *>(p.o + row * D + d) =
                     make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
                 if (d == 0) p.lse[row] = ls == 0.0f ? -INFINITY : (mx + log2f(ls)) * 0.69314718055994531f;
             } else {
                 const size_t row = (part * kHeads + k) * kDecRows + r;
                 *reinterpret_cast<float4 *>(p.part_o + row * D + d) = o;
-                if (d == 0) p.part_ml[row] = make_float4(mx, ls, lrs, 0.0f);
+                if (d == 0) p.part_ml[row] = make_float2(mx, ls);
             }
         }
         named_bar_sync(1, kDecWarps * 32);  // the buffers are free again
@@ -828,7 +829,7 @@ constexpr int kJoinThreads = 256;
 
 struct JoinParams {
     const float *part_o;
-    const float4 *part_ml;
+    const float2 *part_ml;
     const int4 *record;
     __nv_bfloat16 *o;
     float *lse;
@@ -841,7 +842,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 decode_join_kernel(const JoinParams p) {
     constexpr int kCols = D / 4, kParts = kJoinThreads / kCols;  // float4 columns, rows of threads
     __shared__ float4 sum_o[kParts][kCols];
-    __shared__ float4 sum_ml[kParts];
+    __shared__ float2 sum_ml[kParts];
     wait_for_primary();
     const int4 rec = p.record[blockIdx.x];
     const int row = blockIdx.y, head = blockIdx.z;
@@ -852,14 +853,13 @@ decode_join_kernel(const JoinParams p) {
     // maximum; then the rows' results, in order.
     float mx = -INFINITY;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float2 l = make_float2(0.0f, 0.0f);
-    auto add = [&](const float4 &ml, const float4 &v) {
+    float l = 0.0f;
+    auto add = [&](const float2 &ml, const float4 &v) {
         const float to = fmaxf(mx, ml.x);
         const float f = mx == to ? 1.0f : mx == -INFINITY ? 0.0f : ex2_mufu(mx - to);
         const float g = ml.x == to ? 1.0f : ml.x == -INFINITY ? 0.0f : ex2_mufu(ml.x - to);
         mx = to;
-        l.x = fmaf(l.x, f, ml.y * g);
-        l.y = fmaf(l.y, f, ml.z * g);
+        l = fmaf(l, f, ml.y * g);
         o.x = fmaf(o.x, f, v.x * g);
         o.y = fmaf(o.y, f, v.y * g);
         o.z = fmaf(o.z, f, v.z * g);
@@ -871,16 +871,16 @@ decode_join_kernel(const JoinParams p) {
         add(p.part_ml[at], *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * c));
     }
     sum_o[part][c] = o;
-    if (c == 0) sum_ml[part] = make_float4(mx, l.x, l.y, 0.0f);
+    if (c == 0) sum_ml[part] = make_float2(mx, l);
     __syncthreads();
     if (part == 0) {
 #pragma unroll
         for (int w = 1; w < kParts; ++w) add(sum_ml[w], sum_o[w][c]);
         const size_t out = (size_t)rec.x * p.Hq + rec.y + head * p.group + row;
-        const float inv = l.y == 0.0f ? 0.0f : p.v_descale / l.y;
+        const float inv = l == 0.0f ? 0.0f : p.v_descale / l;
         *reinterpret_cast<uint2 *>(p.o + out * D + 4 * c) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (c == 0) p.lse[out] = l.x == 0.0f ? -INFINITY : (mx + log2f(l.x)) * 0.69314718055994531f;
+        if (c == 0) p.lse[out] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
     }
 }
 

@@ -113,7 +113,7 @@ DecodeLayout decode_layout(int D) {
     const size_t rows = (size_t)kDecodeMaxBlocks * 2 * std::max(1, 256 / D) * tab::kDecRows;
     DecodeLayout L;
     L.part_ml = align256(rows * D * sizeof(float));
-    L.record = L.part_ml + align256(rows * sizeof(float4));
+    L.record = L.part_ml + align256(rows * sizeof(float2));
     L.total = L.record + align256((size_t)kDecodeMaxBlocks * sizeof(int4));
     return L;
 }
@@ -465,7 +465,7 @@ attn_status_t attn_decode_paged(const void *q, const void *k_cache, const void *
     p.seq_lens = seq_lens;
     p.status = st->status;
     p.part_o = reinterpret_cast<float *>(ws);
-    p.part_ml = reinterpret_cast<float4 *>(ws + L.part_ml);
+    p.part_ml = reinterpret_cast<float2 *>(ws + L.part_ml);
     p.record = reinterpret_cast<int4 *>(ws + L.record);
     p.B = B;
     p.Hq = Hq;
