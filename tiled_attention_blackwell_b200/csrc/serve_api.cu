@@ -69,6 +69,42 @@ attn_status_t check_norm(const void *qw, const void *kw, int w_fp32, const float
 
 int chunks_of(int heads, int per) { return (heads + per - 1) / per; }
 
+// Parameters that every form has, in one place: a field that a form forgot would
+// be a zero.  `rows`: heads of a token that the form's kernel takes together.
+tab::NormRopeParams norm_params(const void *q, const void *k, void *q_out, void *k_out,
+                                long long q_stride, long long k_stride, long long q_out_stride,
+                                long long k_out_stride, const void *qw, const void *kw, int w_fp32,
+                                const float *cos, const float *sin, const int *positions,
+                                long long tokens, int Hq, int Hkv, int rot, int max_positions,
+                                float eps, int rows, int *status) {
+    tab::NormRopeParams p;
+    memset(&p, 0, sizeof p);
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    p.k_out = static_cast<__nv_bfloat16 *>(k_out);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_out_stride = k_out_stride;
+    p.qw = qw;
+    p.kw = kw;
+    p.w_fp32 = w_fp32;
+    p.cos = cos;
+    p.sin = sin;
+    p.positions = positions;
+    p.status = status;
+    p.tokens = tokens;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.rot = rot;
+    p.max_positions = max_positions;
+    p.chunks_q = chunks_of(Hq, rows);
+    p.chunks_k = chunks_of(Hkv, rows);
+    p.eps = eps;
+    return p;
+}
+
 template <int KV, bool INTERLEAVED>
 attn_status_t launch_norm(const tab::NormRopeParams &p, int D, cudaStream_t stream) {
     const long long items = p.tokens * (p.chunks_q + (KV ? 2 : 1) * p.chunks_k);
@@ -229,31 +265,9 @@ attn_status_t attn_qk_norm_rope(const void *q, const void *k, void *q_out, void 
         return s;
     DeviceState *st = nullptr;
     if ((s = device_state(&st)) != ATTN_OK) return s;
-    tab::NormRopeParams p;
-    memset(&p, 0, sizeof p);
-    p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.k = static_cast<const __nv_bfloat16 *>(k);
-    p.q_out = static_cast<__nv_bfloat16 *>(q_out);
-    p.k_out = static_cast<__nv_bfloat16 *>(k_out);
-    p.q_stride = q_stride;
-    p.k_stride = k_stride;
-    p.q_out_stride = q_out_stride;
-    p.k_out_stride = k_out_stride;
-    p.qw = q_weight;
-    p.kw = k_weight;
-    p.w_fp32 = w_fp32;
-    p.cos = cos;
-    p.sin = sin;
-    p.positions = positions;
-    p.status = st->status;
-    p.tokens = tokens;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.rot = rot;
-    p.max_positions = max_positions;
-    p.chunks_q = cq;
-    p.chunks_k = ck;
-    p.eps = eps;
+    const tab::NormRopeParams p = norm_params(
+        q, k, q_out, k_out, q_stride, k_stride, q_out_stride, k_out_stride, q_weight, k_weight, w_fp32,
+        cos, sin, positions, tokens, Hq, Hkv, rot, max_positions, eps, tab::kNormRows, st->status);
     return dispatch_norm<0>(p, D, interleaved, static_cast<cudaStream_t>(stream));
 }
 
@@ -289,31 +303,11 @@ attn_status_t attn_qk_norm_rope_cache(const void *q, const void *k, const void *
                         "descale factors and their reciprocals must be > 0 and finite, and 1 for a bf16 cache");
     DeviceState *st = nullptr;
     if ((s = device_state(&st)) != ATTN_OK) return s;
-    tab::NormRopeParams p;
-    memset(&p, 0, sizeof p);
-    p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.k = static_cast<const __nv_bfloat16 *>(k);
+    tab::NormRopeParams p = norm_params(
+        q, k, q_out, nullptr, q_stride, k_stride, q_out_stride, 0, q_weight, k_weight, w_fp32, cos, sin,
+        positions, tokens, Hq, Hkv, rot, max_positions, eps, tab::kNormRows, st->status);
     p.v = static_cast<const __nv_bfloat16 *>(v);
-    p.q_out = static_cast<__nv_bfloat16 *>(q_out);
-    p.q_stride = q_stride;
-    p.k_stride = k_stride;
     p.v_stride = v_stride;
-    p.q_out_stride = q_out_stride;
-    p.qw = q_weight;
-    p.kw = k_weight;
-    p.w_fp32 = w_fp32;
-    p.cos = cos;
-    p.sin = sin;
-    p.positions = positions;
-    p.status = st->status;
-    p.tokens = tokens;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.rot = rot;
-    p.max_positions = max_positions;
-    p.chunks_q = cq;
-    p.chunks_k = ck;
-    p.eps = eps;
     p.slots = slots;
     p.k_cache = k_cache;
     p.v_cache = v_cache;
@@ -361,31 +355,9 @@ attn_status_t attn_qk_norm_rope_bwd(const void *dq, const void *dk, int dq_fp32,
         return fail(ATTN_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     DeviceState *st = nullptr;
     if ((s = device_state(&st)) != ATTN_OK) return s;
-    tab::NormRopeParams p;
-    memset(&p, 0, sizeof p);
-    p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.k = static_cast<const __nv_bfloat16 *>(k);
-    p.q_out = static_cast<__nv_bfloat16 *>(dq_in);
-    p.k_out = static_cast<__nv_bfloat16 *>(dk_in);
-    p.q_stride = q_stride;
-    p.k_stride = k_stride;
-    p.q_out_stride = dq_in_stride;
-    p.k_out_stride = dk_in_stride;
-    p.qw = q_weight;
-    p.kw = k_weight;
-    p.w_fp32 = w_fp32;
-    p.cos = cos;
-    p.sin = sin;
-    p.positions = positions;
-    p.status = st->status;
-    p.tokens = tokens;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.rot = rot;
-    p.max_positions = max_positions;
-    p.chunks_q = cq;
-    p.chunks_k = ck;
-    p.eps = eps;
+    tab::NormRopeParams p = norm_params(
+        q, k, dq_in, dk_in, q_stride, k_stride, dq_in_stride, dk_in_stride, q_weight, k_weight, w_fp32,
+        cos, sin, positions, tokens, Hq, Hkv, rot, max_positions, eps, tab::kNormBwdRows, st->status);
     p.dq = dq;
     p.dk = dk;
     p.dq_stride = dq_stride;
