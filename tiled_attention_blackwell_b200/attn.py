@@ -211,7 +211,8 @@ def _torch_stream(stream, device):
     if isinstance(stream, torch.cuda.Stream):
         return stream
     handle = _handle(stream)
-    if handle in (0, 1):  # cudaStreamLegacy; an ExternalStream of 0 would be a stream from torch's pool
+    # 0, or cudaStreamLegacy; an ExternalStream of 0 would be a stream from torch's pool.
+    if handle in (0, 1):
         return torch.cuda.default_stream(device)
     return torch.cuda.ExternalStream(handle, device=device)
 
@@ -226,19 +227,19 @@ def _bring(t, device, stream):
     return t
 
 
-def _on_stream(stream, q, call):
-    """The results of call() made with `stream` (a stream, or its handle) as the
-    current one: all that it allocates belongs to `stream`.  The results are
+def _on_stream(stream, q, call, *args, **kw):
+    """The results of call(*args, **kw) made with `stream` (a stream, or its handle) as
+    the current one: all that it allocates belongs to `stream`.  The results are
     marked as used by the caller's stream too, where they are read (once that
     stream waits for `stream`) and dropped; and by `stream`, for those that the
     caller gave."""
     if not torch.is_tensor(q) or q.device.type != "cuda":
-        return call()  # which refuses q
+        return call(*args, **kw)  # which refuses q
     caller, own = torch.cuda.current_stream(q.device), _torch_stream(stream, q.device)
     if own.cuda_stream == caller.cuda_stream and torch.cuda.current_device() == q.device.index:
-        return call()
+        return call(*args, **kw)
     with torch.cuda.stream(own):
-        out = call()
+        out = call(*args, **kw)
     for t in out if isinstance(out, tuple) else (out,):
         t.record_stream(caller)
         t.record_stream(own)
@@ -260,8 +261,6 @@ def _slopes(alibi_slopes, Hq, device, stream):
 
 def _device_docs(doc_offsets, device, stream):
     """Document offsets on the device, as _slopes has its slopes there."""
-    if doc_offsets is None:
-        return None
     if not torch.is_tensor(doc_offsets):
         doc_offsets = torch.as_tensor(doc_offsets, dtype=torch.int32)
     return doc_offsets if doc_offsets.is_cuda else _bring(doc_offsets, device, stream)
@@ -343,13 +342,16 @@ def attention(q, k, v, *, scale=None, causal=False, window=None, doc_offsets=Non
     _check_sinks(sinks, doc_offsets)
     if alibi_slopes is not None:
         alibi_slopes = _slopes(alibi_slopes, q.shape[2], q.device, stream)
-    doc_offsets = _device_docs(doc_offsets, q.device, stream)
+    if doc_offsets is not None:
+        doc_offsets = _device_docs(doc_offsets, q.device, stream)
     if stream is not None:
-        return _on_stream(stream, q, lambda: attention(
-            q, k, v, scale=scale, causal=causal, window=window, doc_offsets=doc_offsets,
-            options=options, softcap=softcap, alibi_slopes=alibi_slopes, sinks=sinks))
+        return _on_stream(
+            stream, q, attention, q, k, v, scale=scale, causal=causal, window=window,
+            doc_offsets=doc_offsets, options=options, softcap=softcap,
+            alibi_slopes=alibi_slopes, sinks=sinks)
     if sinks:
-        return _attention_sinks(q, k, v, scale, causal, window, sinks, options, softcap, alibi_slopes)
+        return _attention_sinks(q, k, v, scale, causal, window, sinks, options, softcap,
+                                alibi_slopes)
     B, Sq, Hq, D = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(D)
@@ -392,11 +394,13 @@ def attn_fwd_fp8(q, k, v, o, lse, *, q_descale, k_descale, v_descale, scale, cau
 def attention_fp8(q, k, v, *, q_descale, k_descale, v_descale, scale=None, causal=False,
                   window=None, doc_offsets=None, options=None, stream=None):
     """Allocate O (bf16) and LSE with torch and run the fp8 forward."""
-    doc_offsets = _device_docs(doc_offsets, q.device, stream)
+    if doc_offsets is not None:
+        doc_offsets = _device_docs(doc_offsets, q.device, stream)
     if stream is not None:
-        return _on_stream(stream, q, lambda: attention_fp8(
-            q, k, v, q_descale=q_descale, k_descale=k_descale, v_descale=v_descale, scale=scale,
-            causal=causal, window=window, doc_offsets=doc_offsets, options=options))
+        return _on_stream(
+            stream, q, attention_fp8, q, k, v, q_descale=q_descale, k_descale=k_descale,
+            v_descale=v_descale, scale=scale, causal=causal, window=window,
+            doc_offsets=doc_offsets, options=options)
     B, Sq, Hq, D = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(D)
@@ -474,12 +478,14 @@ def attention_fp4(q_codes, q_scales, q_global, k_codes, k_scales, k_global, v_co
                   classifier="affine", mma=None, options=None, stream=None, workspace=None):
     """Allocate O, LSE (and the workspace unless given) with torch and run the
     FP4 Direct-P forward.  Returns (O, LSE)."""
-    doc_offsets = _device_docs(doc_offsets, q_codes.device, stream)
+    if doc_offsets is not None:
+        doc_offsets = _device_docs(doc_offsets, q_codes.device, stream)
     if stream is not None:
-        return _on_stream(stream, q_codes, lambda: attention_fp4(
-            q_codes, q_scales, q_global, k_codes, k_scales, k_global, v_codes, v_scales, v_global,
-            scale=scale, causal=causal, window=window, doc_offsets=doc_offsets,
-            classifier=classifier, mma=mma, options=options, workspace=workspace))
+        return _on_stream(
+            stream, q_codes, attention_fp4, q_codes, q_scales, q_global, k_codes, k_scales,
+            k_global, v_codes, v_scales, v_global, scale=scale, causal=causal, window=window,
+            doc_offsets=doc_offsets, classifier=classifier, mma=mma, options=options,
+            workspace=workspace)
     B, Sq, Hq, Dh = q_codes.shape
     _, Sk, Hkv, _ = k_codes.shape
     D = 2 * Dh
@@ -576,11 +582,13 @@ def attention_backward(q, k, v, o, lse, dout, *, scale=None, causal=False, windo
     _check_sinks(sinks, doc_offsets)
     if alibi_slopes is not None:
         alibi_slopes = _slopes(alibi_slopes, q.shape[2], q.device, stream)
-    doc_offsets = _device_docs(doc_offsets, q.device, stream)
+    if doc_offsets is not None:
+        doc_offsets = _device_docs(doc_offsets, q.device, stream)
     if stream is not None:
-        return _on_stream(stream, q, lambda: attention_backward(
-            q, k, v, o, lse, dout, scale=scale, causal=causal, window=window,
-            doc_offsets=doc_offsets, softcap=softcap, alibi_slopes=alibi_slopes, sinks=sinks))
+        return _on_stream(
+            stream, q, attention_backward, q, k, v, o, lse, dout, scale=scale, causal=causal,
+            window=window, doc_offsets=doc_offsets, softcap=softcap, alibi_slopes=alibi_slopes,
+            sinks=sinks)
     if sinks:
         return _attention_backward_sinks(q, k, v, o, lse, dout, scale, causal, window, sinks,
                                          softcap, alibi_slopes)
@@ -675,9 +683,9 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6, int
     `interleaved`, in neighbouring pairs; positions int32 [...].  q_out and
     k_out are allocated unless given; they may be q and k themselves."""
     if stream is not None:
-        return _on_stream(stream, q, lambda: qk_norm_rope(
-            q, k, q_weight, k_weight, cos, sin, positions, eps=eps, interleaved=interleaved,
-            q_out=q_out, k_out=k_out))
+        return _on_stream(
+            stream, q, qk_norm_rope, q, k, q_weight, k_weight, cos, sin, positions, eps=eps,
+            interleaved=interleaved, q_out=q_out, k_out=k_out)
     return _native().norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
                                q_out, k_out)
 
@@ -689,9 +697,9 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos, sin, positions,
     (dq_in, dk_in, dq_weight, dk_weight): bf16 like q and k (allocated unless
     given: views of a packed gradient are fine), fp32 [D]."""
     if stream is not None:
-        return _on_stream(stream, q, lambda: qk_norm_rope_backward(
-            dq, dk, q, k, q_weight, k_weight, cos, sin, positions, eps=eps, interleaved=interleaved,
-            dq_in=dq_in, dk_in=dk_in))
+        return _on_stream(
+            stream, q, qk_norm_rope_backward, dq, dk, q, k, q_weight, k_weight, cos, sin,
+            positions, eps=eps, interleaved=interleaved, dq_in=dq_in, dk_in=dk_in)
     return _native().norm_rope_backward(q, k, q_weight, k_weight, cos, sin, positions, eps,
                                         interleaved, dq, dk, dq_in, dk_in)
 
@@ -706,9 +714,10 @@ def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos, sin, positions, slots, 
     negative slot marks padding, for which nothing is written (its row of
     q_out keeps what it held)."""
     if stream is not None:
-        return _on_stream(stream, q, lambda: qk_norm_rope_cache(
-            q, k, v, q_weight, k_weight, cos, sin, positions, slots, k_cache, v_cache,
-            k_descale=k_descale, v_descale=v_descale, eps=eps, interleaved=interleaved, q_out=q_out))
+        return _on_stream(
+            stream, q, qk_norm_rope_cache, q, k, v, q_weight, k_weight, cos, sin, positions,
+            slots, k_cache, v_cache, k_descale=k_descale, v_descale=v_descale, eps=eps,
+            interleaved=interleaved, q_out=q_out)
     return _native().norm_rope_cache(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
                                      v, slots, k_cache, v_cache, k_descale, v_descale, q_out)
 
@@ -763,10 +772,10 @@ def decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, scale=None, windo
     if alibi_slopes is not None:
         alibi_slopes = _slopes(alibi_slopes, q.shape[-2], q.device, stream)
     if stream is not None:
-        return _on_stream(stream, q, lambda: decode_paged(
-            q, k_cache, v_cache, page_table, seq_lens, scale=scale, window=window, sinks=sinks,
-            softcap=softcap, alibi_slopes=alibi_slopes, k_descale=k_descale, v_descale=v_descale, o=o,
-            lse=lse, workspace=workspace))
+        return _on_stream(
+            stream, q, decode_paged, q, k_cache, v_cache, page_table, seq_lens, scale=scale,
+            window=window, sinks=sinks, softcap=softcap, alibi_slopes=alibi_slopes,
+            k_descale=k_descale, v_descale=v_descale, o=o, lse=lse, workspace=workspace)
     left, right = (-1, -1) if window is None else window
     if right < -1:
         raise ValueError("window bounds must be -1 or >= 0")
