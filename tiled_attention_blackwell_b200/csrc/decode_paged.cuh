@@ -865,10 +865,21 @@ decode_join_kernel(const JoinParams p) {
         o.z = fmaf(o.z, f, v.z * g);
         o.w = fmaf(o.w, f, v.w * g);
     };
-#pragma unroll 4
-    for (int i = part; i < n; i += kParts) {
-        const size_t at = (((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * kHeads + head) * kDecRows + row;
-        add(p.part_ml[at], *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * c));
+    // Four partials' loads at a time, each before the first is used.
+    constexpr int kAhead = 4;
+    for (int i0 = part; i0 < n; i0 += kAhead * kParts) {
+        float2 ml[kAhead];
+        float4 v[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + u * kParts;
+            const size_t at = (((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * kHeads + head) * kDecRows + row;
+            ml[u] = i < n ? p.part_ml[at] : make_float2(-INFINITY, 0.0f);
+            v[u] = i < n ? *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * c)
+                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) add(ml[u], v[u]);
     }
     sum_o[part][c] = o;
     if (c == 0) sum_ml[part] = make_float2(mx, l);
