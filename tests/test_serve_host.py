@@ -203,6 +203,30 @@ def test_decode_binding_refuses(L, name, bad):
         attn.decode_paged(cpu(2, 4, 128), *list(t.values())[1:], window=(3, -2))
 
 
+class _OnOther(torch.Tensor):
+    """A CPU tensor that says it is on a second GPU."""
+
+    @property
+    def device(self):
+        return torch.device("cuda", 1)
+
+
+def test_a_stream_of_another_device_is_refused(L, monkeypatch):
+    """Calls run on the device's current stream: one that another device's stream
+    was given to would run elsewhere than asked."""
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 0), 0x100
+    monkeypatch.setattr(attn, "_torch_stream", lambda stream, device: Stream())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream())
+    t = norm_tensors(q=cpu(5, 4, 128).as_subclass(_OnOther))
+    x = cpu(1, 16, 2, 64).as_subclass(_OnOther)
+    calls = [lambda: attn.attention(x, x, x, stream=7), lambda: attn.attention(x, x, x, window=(3, 0), sinks=1, stream=7),
+             lambda: attn.decode_paged(t["q"], x, x, None, None, stream=7)]
+    for call in calls + [lambda call=call: call(stream=7) for call in norm_calls(t)]:
+        with pytest.raises(TypeError, match="stream is of cuda:0"):
+            call()
+
+
 # ------------------------------------------------- windows with first tokens
 
 def call_fwd_sinks(L, **kw):

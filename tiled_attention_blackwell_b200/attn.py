@@ -236,6 +236,8 @@ def _on_stream(stream, q, call, *args, **kw):
     if not torch.is_tensor(q) or q.device.type != "cuda":
         return call(*args, **kw)  # which refuses q
     caller, own = torch.cuda.current_stream(q.device), _torch_stream(stream, q.device)
+    if own.device != q.device:
+        raise TypeError(f"stream is of {own.device}, the tensors are on {q.device}")
     if own.cuda_stream == caller.cuda_stream and torch.cuda.current_device() == q.device.index:
         return call(*args, **kw)
     with torch.cuda.stream(own):
