@@ -873,13 +873,16 @@ decode_join_kernel(const JoinParams p) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int i = i0 + u * kParts;
+            if (i >= n) break;
             const size_t at = (((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * kHeads + head) * kDecRows + row;
-            ml[u] = i < n ? p.part_ml[at] : make_float2(-INFINITY, 0.0f);
-            v[u] = i < n ? *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * c)
-                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            ml[u] = p.part_ml[at];
+            v[u] = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * c);
         }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) add(ml[u], v[u]);
+        for (int u = 0; u < kAhead; ++u) {
+            if (i0 + u * kParts >= n) break;
+            add(ml[u], v[u]);
+        }
     }
     sum_o[part][c] = o;
     if (c == 0) sum_ml[part] = make_float2(mx, l);
