@@ -130,6 +130,9 @@ ATTN_API void attn_fwd_default_options(attn_fwd_options_t *opts);
  * scale > 0 and finite; window bounds -1 (unbounded) or >= 0; a document
  * mask requires Sq == Sk and num_docs >= 1.  q, k, v, o must be 16-byte
  * aligned.  Returns ATTN_OK once the kernel is enqueued.
+ * What stands in K at a hidden key has no part in a row's result.  V has to be
+ * finite there too (here and in the other forwards; in the backward all inputs):
+ * a hidden weight is a product with 0 where another row of the tile sees the key.
  */
 ATTN_API attn_status_t attn_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
                        int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,

@@ -343,10 +343,10 @@ void attn_fwd_default_options(attn_fwd_options_t *opts) {
 // Parts that the steps of an item (256 query rows of a head) are cut into
 // (attn_fwd_sinks): as many as give every SM of the device a CTA, each with
 // two steps at least, where there are six or more.  A step takes about 2 us,
-// and so does the join: 777 queries of 8 heads under a window of 501 keys
-// (8 steps) take 19.9 us whole, 16.5 in three parts, 14.6 in four; 600 of 16
-// heads under 301 (5 steps) 12.9 whole, 14.4 in two parts.  Items that fill the
-// device are not cut.
+// and so does the join.  Replayed in a graph, 777 queries of 8 heads of 64
+// under a window of 501 keys (8 steps) take 19.7 us whole, 16.3 in three parts,
+// 14.5 in four; 600 of 16 heads of 128 under 301 (5 steps) 13.7 whole, 19.1 in
+// two parts.  Items that fill the device are not cut.
 constexpr int kFwdPartCtas = 148;
 static int fwd_parts(int B, int Hq, int Sq, int Sk, int causal, int window_left, int window_right,
                      int sinks) {
@@ -756,8 +756,9 @@ static int sink_parts(int B, int Hq, int Hkv, int Sq, int Sk, int sinks) {
 }
 // Parts of a key block without first keys that `items` (query block, head of
 // the group) pairs see: as many as give every SM of the device a CTA, of four
-// items or more.  (One key head under 32 query heads, 1000 tokens, window 501:
-// the backward takes 301 us with those blocks whole, 86 in parts.)
+// items or more.  (One key head of 128 under 32 query heads, 1000 tokens, window
+// 501: the backward takes 295 us with those blocks whole, 78 in parts; of 64,
+// 277 and 59.)
 static int other_parts(int B, int Hkv, int Sk, long long items) {
     const long long ctas = (Sk + 127LL) / 128 * Hkv * B;
     return (int)std::max(1LL, std::min(148 / ctas, items / 4));

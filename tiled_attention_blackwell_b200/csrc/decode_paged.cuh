@@ -159,11 +159,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 // Weights of two heads in the operand type.  bf16: in two words, what the first
 // rounding leaves in `rest`, so that a weight is off by 2^-17, and their sum in
 // fp32 normalises them.  (One word, normalised by the sum of what it held, put
-// the output off by sqrt(2) of its own rounding; the time is the keys' bytes
-// either way: 64 ragged sequences of 32 / 8 heads of 128 172.2 us, 173.9 with one word,
-// 48 of 16 / 16 heads of 64 128.2 against 127.2.)  f16 weights are off by 2^-11 of themselves or by 2^-32 of the
-// largest (kDecBias): less than the output's own rounding, 2^-8 of the largest V,
-// for the 2^23 keys that n 2^-32 allows.
+// the output off by sqrt(2) of its own rounding.  The time is the keys' bytes
+// either way: 64 ragged sequences of 32 / 8 heads of 128 172.9 us, as with one
+// word; 48 of 16 / 16 heads of 64 128.0 against 127.4.)  f16 weights are off by
+// 2^-11 of themselves or by 2^-32 of the largest (kDecBias): less than the
+// output's own rounding, 2^-8 of the largest V, for the 2^23 keys that n 2^-32
+// allows.
 template <bool F8>
 __device__ __forceinline__ uint32_t pack_weights(float p0, float p1, uint32_t &rest) {
     if constexpr (F8) {
@@ -865,7 +866,9 @@ decode_join_kernel(const JoinParams p) {
         o.z = fmaf(o.z, f, v.z * g);
         o.w = fmaf(o.w, f, v.w * g);
     };
-    // Four partials' loads at a time, each before the first is used.
+    // Four partials' loads at a time, each before the first is used: a sequence of
+    // 8000 keys, whose pairs have 36, takes 11.1 us in a graph, and 12.6 with one
+    // at a time.
     constexpr int kAhead = 4;
     for (int i0 = part; i0 < n; i0 += kAhead * kParts) {
         float2 ml[kAhead];

@@ -29,8 +29,9 @@ namespace tab {
 
 // Small blocks: one that ends makes room for the next's loads at once.
 // Measured on 16384 tokens of 32 heads of 128 (273 MB in and out): 49 us with
-// blocks of 128 threads, eight per SM (64 registers, a few of them spilled), as
-// long as a plain copy of the same bytes takes; 51 us with 256 threads, four
+// blocks of 128 threads, eight per SM (64 registers: none spilled in this form,
+// 124 to 156 bytes a thread in the one with a bf16 cache, 52 to 56 with an e4m3
+// one), as long as a plain copy of the same bytes takes; 51 us with 256 threads, four
 // per SM, or with blocks that walk over the items and load one ahead; 59 us
 // with 71 registers and three blocks of 256.
 constexpr int kNormThreads = 128;
@@ -315,7 +316,7 @@ norm_rope_kernel(const NormRopeParams p) {
 // each block's share of dw stays in registers until its end, and the sum of
 // the blocks' shares (norm_rope_dw_kernel, in the blocks' order) does not
 // depend on the timing.  Measured on 16384 tokens of 40 heads of 128 (646
-// MB): 111 us, 88 % of the copy rate; two heads at a time, or more blocks
+// MB): 112 us, 87 % of the copy rate; two heads at a time, or more blocks
 // than four of 128 threads per SM, 122 us and more.
 constexpr int kNormBwdRows = 4;
 
