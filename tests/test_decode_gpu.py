@@ -145,6 +145,18 @@ def test_windows_and_sinks(window, sinks, dtype):
     check(t, run(t, window=(window, -1), sinks=sinks), scale=0.125, window=window, sinks=sinks)
 
 
+def test_more_first_keys_than_fit_an_int_are_all_of_them():
+    t = problem([200, 33], 4, 2, 64, 16, torch.bfloat16, seed=74)
+    want = run(t, window=(20, 0), sinks=200)
+    for sinks in (201, 2 ** 31 - 1, 2 ** 31, 2 ** 40, 10 ** 30):
+        got = run(t, window=(20, 0), sinks=sinks)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for sinks in (-1, -2 ** 40):
+        with pytest.raises(attn.AttnError) as e:
+            run(t, window=(20, 0), sinks=sinks)
+        assert e.value.status == attn.ATTN_ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
 @pytest.mark.parametrize("D", [64, 128])
 def test_pages_outside_a_window_may_be_given_away(dtype, D):

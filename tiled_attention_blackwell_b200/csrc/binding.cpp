@@ -81,6 +81,15 @@ int integer(PyObject *o) {
     return (int)v;
 }
 
+// A number of first keys: more than `most` are `most` (more than there are keys are
+// all of them), a negative one is the library's to refuse.
+int first_keys(PyObject *o, int most) {
+    int overflow = 0;
+    const long long n = PyLong_AsLongLongAndOverflow(o, &overflow);
+    if (n == -1 && PyErr_Occurred()) throw PythonError{};
+    return overflow > 0 || n > most ? most : overflow < 0 || n < 0 ? -1 : (int)n;
+}
+
 // Calls run on the device's current stream, whose pool the outputs come from.
 void *current_stream(int device) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream(); }
 
@@ -315,7 +324,7 @@ PyObject *decode(PyObject *const *a) {
                    static_cast<const int *>(table.data_ptr()), static_cast<const int *>(lens.data_ptr()),
                    o.data_ptr(), static_cast<float *>(lse.data_ptr()), (int)B, (int)Hq, (int)kc.size(2), (int)D,
                    (int)kc.size(0), (int)kc.size(1), (int)table.size(1), number(a[5]), integer(a[6]),
-                   integer(a[7]), number(a[8]), slopes, ws.data_ptr(), (size_t)ws.numel(),
+                   first_keys(a[7], INT_MAX), number(a[8]), slopes, ws.data_ptr(), (size_t)ws.numel(),
                    current_stream(dev.index())),
           "attn_decode_paged");
     return Py_BuildValue("(NN)", wrap(o), wrap(lse));
@@ -344,11 +353,7 @@ struct Masked {
             for (int i = 0; i < 4; ++i) require(t->size(i) <= INT_MAX, "q or k", "smaller");
         B = (int)q.size(0), Sq = (int)q.size(1), Hq = (int)q.size(2), D = (int)q.size(3);
         Sk = (int)k.size(1), Hkv = (int)k.size(2);
-        // More first keys than keys are all of them.
-        int overflow = 0;
-        const long long n = PyLong_AsLongLongAndOverflow(a[7], &overflow);
-        if (n == -1 && PyErr_Occurred()) throw PythonError{};
-        sinks = overflow > 0 || n > Sk ? Sk : overflow < 0 || n < 0 ? -1 : (int)n;
+        sinks = first_keys(a[7], Sk);
     }
     void on(Device &dev) const {
         dev.add(q, "q");
